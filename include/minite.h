@@ -58,12 +58,14 @@ typedef enum {
   MINITE_ERR_CUDA = 3,             /* a CUDA launch or runtime call failed */
   MINITE_ERR_TIMEOUT = 4,          /* device: a pipeline wait gave up (status bit 1<<4) */
   MINITE_ERR_BAD_ROUTING = 5,      /* device: a routing id outside [0, E) (status bit 1<<5) */
-  MINITE_ERR_SCRATCH_LIMIT = 6     /* the problem needs more scratch than the built-in array */
+  MINITE_ERR_SCRATCH_LIMIT = 6,    /* the problem needs more scratch than the built-in array */
+  MINITE_ERR_BAD_TOKEN = 7         /* device: a target token id at or above V (status bit 1<<7) */
 } minite_status_t;
 
 enum { MINITE_SCALE_PER_ROW = 0, MINITE_SCALE_PER_GROUP = 1 };
 enum { MINITE_ALONG_COLS = 0, MINITE_ALONG_ROWS = 1 };
 enum { MINITE_OUT_BF16 = 0, MINITE_OUT_FP32 = 1 };
+enum { MINITE_W_NK = 0, MINITE_W_KN = 1 };  /* a BF16 expert weight stored [N, K] or [K, N] */
 enum {
   MINITE_OP_QUANTIZE = 0,
   MINITE_OP_PERMUTE_QUANT = 1,
@@ -544,6 +546,164 @@ int minite_quantize_tokens_nvfp4(const void* x, int64_t x_rows, const int32_t* r
                                  const int32_t* expert_offsets, int64_t k_cap, uint8_t* codes,
                                  uint8_t* sf, float* g_out, int32_t* kofs_out, void* workspace,
                                  size_t ws_bytes, int32_t* status, minite_stream_t stream);
+
+/*
+ * minite_grouped_gemm_bf16 -- BF16 matrix products grouped by expert, one
+ * launch for all experts: the BF16 counterpart of minite_grouped_gemm_nvfp4
+ * for a learner whose backward (or first and last layers) stay in BF16.
+ *
+ * Cites: miniTE report summary, "Respect the timing boundaries" (the measured
+ * learner paths run the backward in BF16) and "Two complementary
+ * interventions" (contiguous expert buffers, device-side metadata).
+ *
+ * For every row m in [0, expert_offsets[E]) of expert e and n in [0, N):
+ *   MINITE_W_NK:  out[m, n] = sum_k a[m, k] * w[e, n, k]    (forward)
+ *   MINITE_W_KN:  out[m, n] = sum_k a[m, k] * w[e, k, n]    (activation
+ *                 gradient: the forward's weight, read as stored)
+ * summed in FP32 on the tensor cores in a fixed order (no split of a sum
+ * over CTAs), rounded once to BF16 or kept in FP32. A row's result depends on
+ * its own values and its expert's weight alone. An expert may have no rows.
+ *
+ * a:        device, BF16 [M_total, K], rows `a_stride` elements apart.
+ * w:        device, BF16 [E, N, K] or [E, K, N], contiguous.
+ * expert_offsets: device, int32 [E+1]: 0, non-decreasing, at most M_total;
+ *           otherwise nothing is written and bit 1<<MINITE_ERR_INVALID_ARG is
+ *           set in *status. {0, M} with E = 1 is a plain matrix product.
+ * out:      device, [M_total, N] BF16 or FP32 (out_dtype), rows `out_stride`
+ *           elements apart; rows at or beyond offsets[E] are not written.
+ * Shape rules: N, K, a_stride, out_stride multiples of 8, 8 <= N, K <= 2^20,
+ * 1 <= E <= 1024, M_total < 2^31 - 128 (0 is allowed: nothing is enqueued);
+ * a, w and out 16-byte aligned. Waits are bounded as in
+ * minite_grouped_gemm_nvfp4.
+ */
+int minite_grouped_gemm_bf16(const void* a, int64_t a_stride, const void* w, int w_layout,
+                             const int32_t* expert_offsets, int64_t M_total, int64_t N, int64_t K,
+                             int32_t E, void* out, int64_t out_stride, int out_dtype,
+                             int32_t* status, minite_stream_t stream);
+
+/*
+ * minite_grouped_wgrad_bf16 -- weight gradients of a grouped projection from
+ * BF16 rows in expert order, one launch for all experts:
+ *   out[e, i, j] (+)= sum_{m in [offsets[e], offsets[e+1])} a[m, i] * b[m, j]
+ * summed in FP32 (see minite_grouped_gemm_bf16 for the order); with
+ * `accumulate` the sum is added to what out holds (FP32 only: the running sum
+ * over micro-batches). An expert without rows gets zeros, or keeps its values
+ * with `accumulate`. Cites: as minite_grouped_gemm_bf16.
+ *
+ * a:   device, BF16 [M_total, Na], rows `a_stride` elements apart (the
+ *      gradient of the projection's output).
+ * b:   device, BF16 [M_total, Nb], rows `b_stride` apart (its input).
+ * out: device, [E, Na, Nb] BF16 or FP32 (out_dtype), contiguous.
+ * Offsets, shape rules and errors as minite_grouped_gemm_bf16, with Na, Nb in
+ * place of N, K; M_total = 0 is allowed (zeros are written).
+ */
+int minite_grouped_wgrad_bf16(const void* a, int64_t a_stride, const void* b, int64_t b_stride,
+                              const int32_t* expert_offsets, int64_t M_total, int64_t Na,
+                              int64_t Nb, int32_t E, void* out, int out_dtype, int accumulate,
+                              int32_t* status, minite_stream_t stream);
+
+/*
+ * minite_token_logprobs -- the log probability of a given token of each row
+ * of logits, the row's entropy and its top alternatives, in one pass.
+ *
+ * Cites: miniTE report summary, "Follow the numerical execution path" (token
+ * log probabilities are what the learner and the sampler are compared by).
+ *
+ * With y = x / temperature over a row's V logits and p = softmax(y):
+ *   logprob = log p[target],  entropy = -sum_j p_j log p_j,
+ *   alternatives: the k largest logits' ids and log p, largest first, equal
+ *   logits by the lower id.
+ * All sums in FP32. -inf logits are masked tokens: probability 0, never an
+ * alternative (missing alternatives have id -1 and -inf). A row whose every
+ * logit is -inf has logprob -inf, entropy 0 and no alternatives. A NaN or
+ * +inf logit makes the row's results NaN (ids -1).
+ *
+ * logits:  device, BF16 or FP32 (dtype) [N, V], rows `row_stride` elements
+ *          apart, aligned to the element only. x / temperature must fit FP32.
+ * targets: device, int32 or int64 (targets_int64) [N], or NULL: no logprob. A
+ *          negative target marks a row without a token to score: the row is
+ *          not read and gets logprob 0, entropy 0, alternatives of id -1. One
+ *          at or above V sets bit 1<<MINITE_ERR_BAD_TOKEN in *status and gets
+ *          logprob NaN.
+ * logprob, entropy: device, float [N]; stats: device, float [N][2], what
+ *          the backward needs (8-byte aligned). entropy and stats may be
+ *          NULL, logprob only with NULL targets.
+ * alt_ids, alt_logprobs: device, int32 and float [N, k]; k = 0: not written.
+ * Shape rules: 1 <= V < 2^31, N < 2^31 (0 is allowed), 0 <= k <= min(32, V).
+ */
+int minite_token_logprobs(const void* logits, int dtype, int64_t N, int64_t V, int64_t row_stride,
+                          const void* targets, int targets_int64, float temperature,
+                          float* logprob, float* entropy, float* stats, int32_t k,
+                          int32_t* alt_ids, float* alt_logprobs, int32_t* status,
+                          minite_stream_t stream);
+
+/*
+ * minite_token_logprobs_backward -- gradient of minite_token_logprobs'
+ * logprob and entropy with respect to the logits:
+ *   d[j] = (grad_logprob * ([j = target] - p_j)
+ *           - grad_entropy * p_j * (log p_j + entropy)) / temperature
+ * rounded once to the logits' type. Rows with a negative target, without any
+ * logit above -inf, or with a target at or above V (status bit as above) get
+ * zeros.
+ *
+ * stats, entropy: what the forward wrote for these logits, targets and
+ *          temperature. grad_logprob, grad_entropy: device, float [N], either
+ *          may be NULL (0); grad_logprob needs targets.
+ * dlogits: device, the logits' type [N, V], rows `dlogits_stride` apart; may
+ *          be logits itself (with the same stride), otherwise no overlap.
+ * Shape rules as minite_token_logprobs.
+ */
+int minite_token_logprobs_backward(const void* logits, int dtype, int64_t N, int64_t V,
+                                   int64_t row_stride, const void* targets, int targets_int64,
+                                   float temperature, const float* stats, const float* entropy,
+                                   const float* grad_logprob, const float* grad_entropy,
+                                   void* dlogits, int64_t dlogits_stride, int32_t* status,
+                                   minite_stream_t stream);
+
+/*
+ * minite_adamw_step -- one AdamW step (Loshchilov and Hutter, 2019) over many
+ * tensors at once: one launch for up to 440 tensors.
+ *
+ * Per element, with g = grad * grad_scale[0] (1 if NULL) and t = step:
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in FP32, one rounding to the parameter's type. A BF16 parameter is rounded
+ * to nearest: an update below half its last place leaves it as it is (keep
+ * FP32 parameters with param_bf16 copies where that matters).
+ *
+ * state_bits 32: exp_avg, exp_avg_sq float [n], 16-byte aligned.
+ * state_bits 8:  exp_avg, exp_avg_sq uint8 [n], 8-byte aligned, E4M3 codes;
+ *   exp_avg_scale, exp_avg_sq_scale float [ceil(n / 256)]. Block b of 256
+ *   elements holds m = code * scale and sqrt(v) = code * scale, with scale =
+ *   max(largest magnitude * FP32(1/448), 2^-126). A sqrt(v) above zero never rounds
+ *   to code zero. A block with a non-finite m or v becomes NaN as a whole.
+ *   Zeroed codes and scales are the start's state.
+ *
+ * tensors: HOST array of n_tensors descriptors, read during the call. param
+ *   BF16 or FP32 (param_dtype), grad BF16 or FP32 (grad_dtype), both aligned
+ *   to their element; param_bf16 (or NULL): also receives the new parameter
+ *   rounded to BF16. n = 0 is skipped. Buffers must not overlap.
+ * grad_scale: device float or NULL: a factor on every gradient (a clipping
+ *   coefficient or an inverse loss scale that the host never reads).
+ * step: 1 for the first step; with hyper-parameters outside 0 <= beta < 1,
+ *   eps >= 0 or not finite, MINITE_ERR_INVALID_ARG and nothing is enqueued.
+ */
+typedef struct minite_adamw_tensor {
+  void* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;
+  float* exp_avg_sq_scale;
+  void* param_bf16;
+  int64_t n;
+} minite_adamw_tensor;
+
+int minite_adamw_step(const minite_adamw_tensor* tensors, int64_t n_tensors, int param_dtype,
+                      int grad_dtype, int state_bits, double lr, double beta1, double beta2,
+                      double eps, double weight_decay, int64_t step, const float* grad_scale,
+                      minite_stream_t stream);
 
 /* Workspace bytes needed by `op` (MINITE_OP_QUANTIZE: a = groups;
  * MINITE_OP_PERMUTE_QUANT: a = T, b = H, E, k; MINITE_OP_COMBINE_BACKWARD_QUANT:

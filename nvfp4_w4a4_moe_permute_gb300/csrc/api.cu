@@ -125,6 +125,7 @@ extern "C" const char* minite_status_string(int status) {
     case MINITE_ERR_TIMEOUT: return "device pipeline wait timed out";
     case MINITE_ERR_BAD_ROUTING: return "routing id out of range";
     case MINITE_ERR_SCRATCH_LIMIT: return "problem needs more scratch than the built-in array holds";
+    case MINITE_ERR_BAD_TOKEN: return "token id out of range";
     default: return "unknown status";
   }
 }

@@ -1749,6 +1749,8 @@ cudaError_t launch_pair_pdl(void (*kernel)(KArgs...), int pairs, int threads, si
 
 }  // namespace
 
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return encode_fn(); }
+
 uint64_t wait_budget_ns() {
   const uint64_t v = g_budget_ns.load();
   return v ? v : 2000000000ull;

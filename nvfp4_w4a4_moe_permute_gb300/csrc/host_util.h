@@ -3,6 +3,8 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 namespace minite {
@@ -16,6 +18,9 @@ int num_sms();
 
 // Budget of the GEMM's bounded pipeline waits, in nanoseconds.
 uint64_t wait_budget_ns();
+
+// The driver's tensor map encoder (looked up once), null when there is none.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // Token-chunk size of the permutation for top-k = k (pairs per chunk <= 512).
 inline int permute_chunk_tokens(int k) {

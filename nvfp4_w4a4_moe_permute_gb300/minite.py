@@ -9,9 +9,11 @@ every call raises ``MiniteError``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
+import numpy as np
 import torch
 
 from . import build as _build
@@ -21,7 +23,8 @@ ALONG_COLS, ALONG_ROWS = 0, 1
 OUT_BF16, OUT_FP32 = 0, 1
 OP_QUANTIZE, OP_PERMUTE_QUANT, OP_COMBINE_BACKWARD_QUANT, OP_QUANTIZE_TOKENS = 0, 1, 2, 3
 OP_GATE_UP_SWIGLU = 4
-ERR_TIMEOUT, ERR_BAD_ROUTING = 4, 5
+W_NK, W_KN = 0, 1
+ERR_TIMEOUT, ERR_BAD_ROUTING, ERR_BAD_TOKEN = 4, 5, 7
 
 EXPORTS = [
     "minite_quantize_nvfp4", "minite_moe_permute_quant", "minite_grouped_gemm_nvfp4",
@@ -33,6 +36,8 @@ EXPORTS = [
     "minite_moe_combine_backward_quant", "minite_quantize_tokens_nvfp4",
     "minite_swiglu_weighted_quant_keep_h", "minite_grouped_gemm_wgrad_nvfp4",
     "minite_swiglu_backward_quant_keep", "minite_gate_up_swiglu_quant_nvfp4",
+    "minite_grouped_gemm_bf16", "minite_grouped_wgrad_bf16", "minite_token_logprobs",
+    "minite_token_logprobs_backward", "minite_adamw_step",
 ]
 
 
@@ -80,6 +85,16 @@ def load(path: str | None = None):
         "minite_swiglu_backward_quant_keep": [_vp, _vp, _vp, _i64, _i64, _i32, _vp, _vp, _vp, _vp,
                                               _vp, _vp, _vp, _vp, _vp],
         "minite_moe_combine": [_vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp],
+        "minite_grouped_gemm_bf16": [_vp, _i64, _vp, _int, _vp, _i64, _i64, _i64, _i32, _vp, _i64,
+                                     _int, _vp, _vp],
+        "minite_grouped_wgrad_bf16": [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _int,
+                                      _int, _vp, _vp],
+        "minite_token_logprobs": [_vp, _int, _i64, _i64, _i64, _vp, _int, ctypes.c_float, _vp, _vp,
+                                  _vp, _i32, _vp, _vp, _vp, _vp],
+        "minite_token_logprobs_backward": [_vp, _int, _i64, _i64, _i64, _vp, _int, ctypes.c_float,
+                                           _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp],
+        "minite_adamw_step": [_vp, _i64, _int, _int, _int] + [ctypes.c_double] * 5 +
+                             [_i64, _vp, _vp],
         "minite_test_convert": [_vp, _i64, _vp, _vp, _vp, _vp],
         "minite_test_div6_exhaustive": [_vp, _vp],
         "minite_test_convert_digest": [ctypes.c_ulonglong, ctypes.c_ulonglong, _vp, _vp],
@@ -343,6 +358,133 @@ def minite_moe_combine(expert_out, dest_row, y, status=None, stream=None):
     _check(rc, "minite_moe_combine")
 
 
+def _dtype(t, name):
+    """OUT_BF16 or OUT_FP32 of a tensor."""
+    if t.dtype == torch.bfloat16:
+        return OUT_BF16
+    if t.dtype == torch.float32:
+        return OUT_FP32
+    raise MiniteError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+
+
+def _need(cond, what):
+    if not cond:
+        raise MiniteError(what)
+
+
+def _rows(t, name):
+    """Row stride of a 2-D tensor whose rows are contiguous."""
+    _need(t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1) and
+          (t.shape[0] <= 1 or t.stride(0) >= t.shape[1]),
+          f"{name}: expected 2-D with contiguous rows that do not overlap")
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+
+
+def minite_grouped_gemm_bf16(a, w, expert_offsets, out, w_layout=W_NK, status=None, stream=None):
+    """a bf16 [M, K]; w bf16 [E, N, K] (W_NK) or [E, K, N] (W_KN); out [M, N] bf16 or fp32."""
+    name = "minite_grouped_gemm_bf16"
+    E, N, K = w.shape if w_layout == W_NK else (w.shape[0], w.shape[2], w.shape[1])
+    _need(a.dtype == torch.bfloat16 and w.dtype == torch.bfloat16, f"{name}: a and w are bfloat16")
+    _need(expert_offsets.dtype == torch.int32 and expert_offsets.numel() == E + 1 and
+          expert_offsets.is_contiguous(), f"{name}: expert_offsets is int32 [E + 1]")
+    _need(w.is_contiguous(), f"{name}: w is contiguous")
+    _need(a.dim() == 2 and a.shape[1] == K and tuple(out.shape) == (a.shape[0], N),
+          f"{name}: shapes of a, w and out do not match")
+    rc = load().minite_grouped_gemm_bf16(_p(a), _rows(a, name), _p(w), w_layout, _p(expert_offsets),
+                                         a.shape[0], N, K, E, _p(out), _rows(out, name),
+                                         _dtype(out, name), _p(status), _s(stream))
+    _check(rc, name)
+
+
+def minite_grouped_wgrad_bf16(a, b, expert_offsets, out, accumulate=False, status=None, stream=None):
+    """a bf16 [M, Na], b bf16 [M, Nb] in expert order; out [E, Na, Nb] bf16 or fp32."""
+    name = "minite_grouped_wgrad_bf16"
+    E, Na, Nb = out.shape
+    _need(a.dtype == torch.bfloat16 and b.dtype == torch.bfloat16, f"{name}: a and b are bfloat16")
+    _need(expert_offsets.dtype == torch.int32 and expert_offsets.numel() == E + 1 and
+          expert_offsets.is_contiguous(), f"{name}: expert_offsets is int32 [E + 1]")
+    _need(out.is_contiguous(), f"{name}: out is contiguous")
+    _need(a.dim() == 2 and b.dim() == 2 and a.shape == (b.shape[0], Na) and b.shape[1] == Nb,
+          f"{name}: shapes of a, b and out do not match")
+    rc = load().minite_grouped_wgrad_bf16(_p(a), _rows(a, name), _p(b), _rows(b, name),
+                                          _p(expert_offsets), a.shape[0], Na, Nb, E, _p(out),
+                                          _dtype(out, name), 1 if accumulate else 0, _p(status),
+                                          _s(stream))
+    _check(rc, name)
+
+
+def _targets(targets, N, name):
+    if targets is None:
+        return 0
+    _need(targets.dtype in (torch.int32, torch.int64) and targets.shape == (N,) and
+          targets.is_contiguous(), f"{name}: targets is int32 or int64 [N], contiguous")
+    return 1 if targets.dtype == torch.int64 else 0
+
+
+def _f32(t, shape, name, what):
+    _need(t is None or (t.dtype == torch.float32 and tuple(t.shape) == shape and t.is_contiguous()),
+          f"{name}: {what} is float32 {list(shape)}, contiguous")
+
+
+def minite_token_logprobs(logits, targets, logprob, entropy=None, stats=None, temperature=1.0,
+                          alt_ids=None, alt_logprobs=None, status=None, stream=None):
+    """logits [N, V] bf16 or fp32; logprob, entropy fp32 [N]; stats fp32 [N, 2];
+    alt_ids int32 and alt_logprobs fp32 [N, k]."""
+    name = "minite_token_logprobs"
+    ld = _rows(logits, name)
+    N, V = logits.shape
+    k = 0 if alt_ids is None else alt_ids.shape[1]
+    t64 = _targets(targets, N, name)
+    _f32(logprob, (N,), name, "logprob")
+    _f32(entropy, (N,), name, "entropy")
+    _f32(stats, (N, 2), name, "stats")
+    _f32(alt_logprobs, (N, k), name, "alt_logprobs")
+    _need(alt_ids is None or (alt_ids.dtype == torch.int32 and alt_ids.shape[0] == N and
+                              alt_ids.is_contiguous()), f"{name}: alt_ids is int32 [N, k]")
+    rc = load().minite_token_logprobs(_p(logits), _dtype(logits, name), N, V, ld, _p(targets), t64,
+                                      float(temperature), _p(logprob), _p(entropy), _p(stats), k,
+                                      _p(alt_ids), _p(alt_logprobs), _p(status), _s(stream))
+    _check(rc, name)
+
+
+def minite_token_logprobs_backward(logits, targets, stats, entropy, grad_logprob, grad_entropy,
+                                   dlogits, temperature=1.0, status=None, stream=None):
+    """dlogits: the type and shape of logits (may be logits itself)."""
+    name = "minite_token_logprobs_backward"
+    ld = _rows(logits, name)
+    N, V = logits.shape
+    t64 = _targets(targets, N, name)
+    _need(dlogits.dtype == logits.dtype and dlogits.shape == logits.shape,
+          f"{name}: dlogits has the type and shape of logits")
+    _need(stats is not None, f"{name}: stats of the forward are needed")
+    _f32(stats, (N, 2), name, "stats")
+    _f32(entropy, (N,), name, "entropy")
+    _f32(grad_logprob, (N,), name, "grad_logprob")
+    _f32(grad_entropy, (N,), name, "grad_entropy")
+    rc = load().minite_token_logprobs_backward(
+        _p(logits), _dtype(logits, name), N, V, ld, _p(targets), t64, float(temperature), _p(stats),
+        _p(entropy), _p(grad_logprob), _p(grad_entropy), _p(dlogits), _rows(dlogits, name),
+        _p(status), _s(stream))
+    _check(rc, name)
+
+
+# struct minite_adamw_tensor
+ADAMW_TENSOR = np.dtype([("param", "u8"), ("grad", "u8"), ("exp_avg", "u8"), ("exp_avg_sq", "u8"),
+                         ("exp_avg_scale", "u8"), ("exp_avg_sq_scale", "u8"), ("param_bf16", "u8"),
+                         ("n", "i8")])
+
+
+def minite_adamw_step(tensors, param_dtype, grad_dtype, state_bits, lr, beta1, beta2, eps,
+                      weight_decay, step, grad_scale=None, stream=None):
+    """tensors: numpy array of ADAMW_TENSOR on the host, one descriptor a tensor."""
+    _need(tensors.dtype == ADAMW_TENSOR and tensors.flags.c_contiguous,
+          "minite_adamw_step: tensors is a contiguous array of ADAMW_TENSOR")
+    rc = load().minite_adamw_step(tensors.ctypes.data, len(tensors), param_dtype, grad_dtype,
+                                  state_bits, lr, beta1, beta2, eps, weight_decay, step,
+                                  _p(grad_scale), _s(stream))
+    _check(rc, "minite_adamw_step")
+
+
 def minite_test_convert(x, out_e2m1=None, out_e4m3=None, out_exp=None, stream=None):
     rc = load().minite_test_convert(_p(x), x.numel(), _p(out_e2m1), _p(out_e4m3), _p(out_exp),
                                     _s(stream))
@@ -390,6 +532,138 @@ def quantize(x, per_group=False, along_rows=False, g_in=None, stream=None):
     if x.dim() == 2:
         codes, sf = codes[0], sf[0]
     return dict(codes=codes, sf=sf, g=g)
+
+
+def _on(stream):
+    """Allocations made inside belong to the stream that the kernels run on."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def grouped_gemm_bf16(x, w, expert_offsets, w_as_stored=False, out=None, out_dtype=torch.bfloat16,
+                      status=None, stream=None):
+    """x [M, K] bf16 in expert order times each expert's w: x @ w[e].T for w
+    [E, N, K] (the forward), or x @ w[e] for w [E, K, N] with ``w_as_stored``
+    (the activation gradient of that forward, x its output's gradient).
+    Returns [M, N]."""
+    if out is None:
+        with _on(stream):
+            out = torch.empty((x.shape[0], w.shape[2 if w_as_stored else 1]), dtype=out_dtype,
+                              device=x.device)
+    minite_grouped_gemm_bf16(x, w, expert_offsets, out, W_KN if w_as_stored else W_NK, status, stream)
+    return out
+
+
+def grouped_wgrad_bf16(dy, x, expert_offsets, out=None, out_dtype=torch.float32, accumulate=False,
+                       status=None, stream=None):
+    """dw[e] = dy_e.T @ x_e over each expert's rows, [E, Na, Nb]; added to
+    ``out`` (fp32) with ``accumulate``."""
+    if out is None:
+        _need(not accumulate, "grouped_wgrad_bf16: accumulate needs out")
+        with _on(stream):
+            out = torch.empty((expert_offsets.numel() - 1, dy.shape[1], x.shape[1]), dtype=out_dtype,
+                              device=x.device)
+    minite_grouped_wgrad_bf16(dy, x, expert_offsets, out, accumulate, status, stream)
+    return out
+
+
+def token_logprobs(logits, targets=None, temperature=1.0, alternatives=0, status=None, stream=None):
+    """Log probability of each row's target token under softmax(logits /
+    temperature), with the row's entropy and its ``alternatives`` most likely
+    tokens. Returns dict(logprob (None without targets), entropy, stats,
+    alt_ids, alt_logprobs); a negative target marks a row that is skipped."""
+    N, dev = logits.shape[0], logits.device
+    with _on(stream):
+        f32 = torch.empty((4, N), dtype=torch.float32, device=dev)
+        r = dict(logprob=None if targets is None else f32[0], entropy=f32[1],
+                 stats=f32[2:].view(N, 2), alt_ids=None, alt_logprobs=None)
+        if alternatives:
+            r["alt_ids"] = torch.empty((N, alternatives), dtype=torch.int32, device=dev)
+            r["alt_logprobs"] = torch.empty((N, alternatives), dtype=torch.float32, device=dev)
+    minite_token_logprobs(logits, targets, r["logprob"], r["entropy"], r["stats"], temperature,
+                          r["alt_ids"], r["alt_logprobs"], status, stream)
+    return r
+
+
+def token_logprobs_backward(logits, targets, forward, grad_logprob=None, grad_entropy=None,
+                            temperature=1.0, out=None, status=None, stream=None):
+    """Gradient of token_logprobs' logprob and entropy with respect to the
+    logits; ``forward`` is its result for the same logits, targets and
+    temperature. ``out`` may be the logits themselves."""
+    if out is None:
+        with _on(stream):
+            out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    minite_token_logprobs_backward(logits, targets, forward["stats"], forward["entropy"],
+                                   grad_logprob, grad_entropy, out, temperature, status, stream)
+    return out
+
+
+class AdamW:
+    """AdamW over a list of contiguous tensors of one type (bf16 or fp32), one
+    launch a step, with FP32 states or 8-bit ones (E4M3 codes and one scale per
+    256 elements). ``copies``: bf16 tensors that receive the rounded parameters
+    (for fp32 parameters). The states are flat buffers in which each tensor
+    starts at a multiple of 256 elements (``starts``); ``state`` takes buffers
+    of this layout and a step count to continue from."""
+
+    BLOCK = 256
+
+    def __init__(self, params, copies=None, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
+                 weight_decay=0.01, state_bits=32, state=None):
+        _need(len(params) > 0 and state_bits in (8, 32), "AdamW: needs tensors and state_bits 8 or 32")
+        dev = params[0].device
+        self._param_dtype = _dtype(params[0], "AdamW")
+        for i, p in enumerate(params):
+            _need(p.is_cuda and p.device == dev and p.dtype == params[0].dtype and p.is_contiguous(),
+                  f"AdamW: parameter {i} is not a contiguous {params[0].dtype} CUDA tensor")
+        _need(copies is None or (len(copies) == len(params) and all(
+            c.dtype == torch.bfloat16 and c.shape == p.shape and c.is_contiguous() and c.device == dev
+            for c, p in zip(copies, params))), "AdamW: copies are bfloat16 tensors like the parameters")
+        self.params, self.copies = list(params), None if copies is None else list(copies)
+        self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
+        self.state_bits = state_bits
+        self._numel = [p.numel() for p in params]
+        sizes = np.array(self._numel, dtype=np.int64)
+        blocks = -(-sizes // self.BLOCK)
+        first = np.concatenate([[0], np.cumsum(blocks)[:-1]]).astype(np.int64)
+        self.starts = (first * self.BLOCK).tolist()
+        n_blocks = int(blocks.sum())
+        kinds = dict(exp_avg=(n_blocks * self.BLOCK, torch.float8_e4m3fn if state_bits == 8 else torch.float32))
+        kinds["exp_avg_sq"] = kinds["exp_avg"]
+        if state_bits == 8:
+            kinds["exp_avg_scale"] = kinds["exp_avg_sq_scale"] = (n_blocks, torch.float32)
+        self.step_count = 0 if state is None else int(state["step"])
+        for name, (n, dtype) in kinds.items():
+            t = torch.zeros(n, dtype=dtype, device=dev) if state is None else state[name]
+            _need(t.numel() == n and t.dtype == dtype and t.is_contiguous() and t.device == dev,
+                  f"AdamW: state {name} is not {dtype} [{n}]")
+            setattr(self, name, t)
+        d = self._tensors = np.zeros(len(params), dtype=ADAMW_TENSOR)
+        d["param"] = [p.data_ptr() for p in params]
+        d["n"] = sizes
+        if copies is not None:
+            d["param_bf16"] = [c.data_ptr() for c in copies]
+        for name in ("exp_avg", "exp_avg_sq"):
+            t = getattr(self, name)
+            d[name] = t.data_ptr() + first * (self.BLOCK * t.element_size())
+            if state_bits == 8:
+                d[name + "_scale"] = getattr(self, name + "_scale").data_ptr() + first * 4
+
+    def step(self, grads, grad_scale=None, lr=None, stream=None):
+        """One step with grads[i] (bf16 or fp32, all one type) for tensor i, each
+        times the device scalar ``grad_scale``."""
+        _need(len(grads) == len(self.params), "AdamW.step: one gradient a parameter")
+        kind = grads[0].dtype
+        for g, n in zip(grads, self._numel):
+            if not (g.is_cuda and g.dtype == kind and g.numel() == n and g.is_contiguous()):
+                raise MiniteError("AdamW.step: gradients are contiguous CUDA tensors of one type, "
+                                  "each of its parameter's size")
+        _need(grad_scale is None or (grad_scale.dtype == torch.float32 and grad_scale.numel() == 1),
+              "AdamW.step: grad_scale is one float32")
+        self._tensors["grad"] = [g.data_ptr() for g in grads]
+        minite_adamw_step(self._tensors, self._param_dtype, _dtype(grads[0], "AdamW.step"),
+                          self.state_bits, self.lr if lr is None else lr, *self.betas, self.eps,
+                          self.weight_decay, self.step_count + 1, grad_scale, stream)
+        self.step_count += 1
 
 
 class MoEMLP:
