@@ -27,7 +27,10 @@ namespace logprobs {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxSegments = 8;        // a portable cluster's CTAs at most
+constexpr int64_t kSegmentBytes = 131072;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e+38f;
 
 struct Params {
@@ -37,6 +40,10 @@ struct Params {
   const void* targets;      // int32 or int64 [N], or null
   int targets64;
   float inv_t;
+  float k2;                 // log2(e) / temperature
+  int fast;                 // fast_k(k2)
+  int segments;             // of a row, a power of two
+  int cluster;              // CTAs per row, a power of two up to segments
   float* logprob;
   float* entropy;
   float2* stats;            // [N] {largest logit, log s}, or null
@@ -83,31 +90,112 @@ struct Row {
   __device__ __forceinline__ int64_t tail0() const { return head + nv * Elem<T>::kVec; }
 };
 
-// Running (maximum, sum, weighted sum) of a set of logits; `k` turns a
-// difference of logits into a power of two.
+constexpr float kMask = -1.152921504606846976e+18f;   // -2^60, a BF16 value
+
+// 2^x, within 2 units in the last place; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The larger, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Two floats in one 64-bit register: the packed FP32 instructions take half
+// the issue slots.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+  return p;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// A vector's logits as float pairs, those below -2^60 (masked ones among
+// them) raised to it, and their maximum.
+__device__ __forceinline__ void pairs_of(const float*, const uint4& u, uint64_t (&x)[2], float& mx) {
+  const float a = max_nan(__uint_as_float(u.x), kMask), b = max_nan(__uint_as_float(u.y), kMask);
+  const float c = max_nan(__uint_as_float(u.z), kMask), d = max_nan(__uint_as_float(u.w), kMask);
+  mx = fmaxf(fmaxf(a, b), fmaxf(c, d));
+  x[0] = pair(a, b);
+  x[1] = pair(c, d);
+}
+__device__ __forceinline__ void pairs_of(const uint16_t*, const uint4& u, uint64_t (&x)[4], float& mx) {
+  constexpr uint32_t kMask2 = 0xDD80DD80u;   // -2^60 twice
+  const uint32_t w0 = max_nan_bf16x2(u.x, kMask2), w1 = max_nan_bf16x2(u.y, kMask2);
+  const uint32_t w2 = max_nan_bf16x2(u.z, kMask2), w3 = max_nan_bf16x2(u.w, kMask2);
+  const uint32_t m = max_bf16x2(max_bf16x2(w0, w1), max_bf16x2(w2, w3));
+  mx = fmaxf(bf16lo(m), bf16hi(m));
+  x[0] = pair(bf16lo(w0), bf16hi(w0));
+  x[1] = pair(bf16lo(w1), bf16hi(w1));
+  x[2] = pair(bf16lo(w2), bf16hi(w2));
+  x[3] = pair(bf16lo(w3), bf16hi(w3));
+}
+
+// Running (maximum, sum, weighted sum) of a set of logits in powers of two,
+// with k = log2(e) / T and y = (x - m) k:  s = sum 2^y,  t = sum y 2^y. The
+// difference is taken before the product, so that y is exactly 0 at the
+// maximum (a row with one token left has logprob 0 and entropy 0).
 struct Stat {
-  float m = kLowest, s = 0.0f, t = 0.0f;
+  float m, s, t;
   __device__ __forceinline__ void raise(float nm, float k) {
-    const float d = m - nm;
-    const float c = exp2f(d * k);
+    const float d = (m - nm) * k;
+    const float c = ex2(d);
     t = c > 0.0f ? c * (t + d * s) : 0.0f;   // d * s may be infinite where c is 0
     s = c * s;
     m = nm;
   }
-  __device__ __forceinline__ void add(float x, float k) {
-    const float d = x - m;
-    const float e = exp2f(d * k);
-    s += e;
-    t += fmaxf(d, -1e30f) * e;   // a masked logit (-inf) adds 0, not -inf * 0
+  __device__ __forceinline__ void merge(Stat o, float k) {
+    if (o.m > m) raise(o.m, k);
+    else if (o.m < m) o.raise(m, k);
+    s += o.s;
+    t += o.t;
   }
-  __device__ __forceinline__ void merge(const Stat& o, float k) {
-    Stat a = o;
-    if (a.m > m) raise(a.m, k);
-    else if (a.m < m) a.raise(m, k);
-    s += a.s;
-    t += a.t;
+  // One logit, every special value looked at: for a row whose maximum lies
+  // beyond +-2^59 (all of it masked, or infinite) or an extreme temperature.
+  __device__ __forceinline__ void add_any(float x, float k) {
+    if (x > m) raise(x, k);
+    const float y = (x - m) * k;
+    const float e = ex2(y);
+    s += e;
+    t += fmaxf(y, -1e30f) * e;   // a masked logit (-inf) adds 0, not -inf * 0
   }
 };
+// k in (2^-40, 2^13): a logit of -2^60 then has probability zero beside any
+// maximum above -2^59 (2^-(2^59 k)), and no product with it comes near
+// overflow.
+__host__ __device__ inline bool fast_k(float k) { return k > 9.094947e-13f && k < 8192.0f; }
+__device__ __forceinline__ bool fast_row(float m) { return fabsf(m) < 5.76460752303423488e+17f; }
 
 __device__ __forceinline__ Stat shfl_xor(const Stat& a, int o) {
   Stat r;
@@ -141,6 +229,15 @@ __device__ __forceinline__ void list_insert(uint64_t& mine, uint64_t key) {
   else if (lane > pos) mine = up;
 }
 
+// Join another warp's sorted list of k into this warp's. Warp-collective.
+__device__ __forceinline__ void list_join(uint64_t& mine, const uint64_t* other, int k) {
+  for (int l = 0; l < k; ++l) {
+    const uint64_t cand = other[l];
+    if (cand <= __shfl_sync(0xffffffffu, mine, k - 1)) break;
+    list_insert(mine, cand);
+  }
+}
+
 // Offer one value per lane (absent: x = -inf) to the warp's list of k.
 __device__ __forceinline__ void list_offer(uint64_t& mine, int k, float x, int64_t i, float thr) {
   const float inf = __int_as_float(0x7F800000);
@@ -155,21 +252,183 @@ __device__ __forceinline__ void list_offer(uint64_t& mine, int k, float x, int64
   }
 }
 
+constexpr int kGroups = kThreads / 4;   // threads whose maxima are compared for the threshold
+constexpr int kCandidates = 512;
+
+struct Shared {
+  Stat stat[kMaxSegments][kWarps];
+  Stat part[kMaxSegments];        // every segment's sums (the cluster's first CTA: all of the row)
+  Stat row;
+  alignas(16) float group_max[kGroups];   // read four at a time
+  uint32_t thr;
+  int n_sets, n_cand;
+  uint8_t sets[kThreads];         // threads that hold candidates
+  uint64_t cand[kCandidates];
+  float thread_max[kThreads];     // more candidates than that: every thread's maximum,
+  uint64_t list[kWarps][32];      // and each warp's best
+  uint64_t best[32];              // the CTA's best, sorted, 0 where there is none
+  uint64_t part_best[kMaxSegments][32];   // the cluster's first CTA: the others' best
+};
+
+// A row's segments [s0, s1) of `segs`: segment s holds the 16-byte vectors
+// [begin(s), begin(s + 1)), thread t of it the vectors begin(s) + t + i kThreads.
+struct Segments {
+  int64_t nv;
+  int segs, s0, s1;
+  __device__ __forceinline__ int64_t begin(int s) const { return nv * s / segs; }
+  __device__ __forceinline__ bool first() const { return s0 == 0; }
+  __device__ __forceinline__ bool last() const { return s1 == segs; }
+};
+
+// A warp's stats, joined in a fixed order (on lane 0).
+__device__ __forceinline__ Stat join_warp(Stat st, float k) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) st.merge(shfl_xor(st, o), k);
+  return st;
+}
+// S.stat of n segments to S.part[s0 ...], one thread a segment. Block-wide, a
+// barrier at both ends.
+__device__ __forceinline__ void join_segments(Shared& S, int s0, int n, float k) {
+  __syncthreads();
+  if (threadIdx.x < n) {
+    Stat st = S.stat[threadIdx.x][0];
+    for (int w = 1; w < kWarps; ++w) st.merge(S.stat[threadIdx.x][w], k);
+    S.part[s0 + threadIdx.x] = st;
+  }
+  __syncthreads();
+}
+
+// The k largest of n keys to best[0..k), by the number of larger ones (keys
+// differ). Block-wide, without a barrier.
+__device__ __forceinline__ void rank_keys(const uint64_t* keys, int n, uint64_t* best, int k) {
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint64_t key = keys[i];
+    int larger = 0;
+    for (int j = 0; j < n; ++j) larger += keys[j] > key;
+    if (larger < k) best[larger] = key;
+  }
+}
+
+// The k best of some segments (with the row's head if they are the first, its
+// tail if the last) to S.best. `mine` is the largest logit that this thread saw
+// in them: its vectors, head element tid, tail element tid. Ends with a barrier.
+template <typename T>
+__device__ __forceinline__ void block_alternatives(Shared& S, const Row<T>& r, const Segments& sg,
+                                                   float mine, int k) {
+  constexpr int VEC = Elem<T>::kVec;
+  const float inf = __int_as_float(0x7F800000);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool first = sg.first(), last = sg.last();
+  float g = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
+  g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
+  if ((tid & 3) == 0) S.group_max[tid >> 2] = g;
+  if (tid == 0) {
+    S.thr = 0;
+    S.n_sets = 0;
+    S.n_cand = 0;
+  }
+  if (tid < 32) S.best[tid] = 0;
+  __syncthreads();
+  if (tid < kGroups) {   // the largest of the groups' maxima that at least k of them reach
+    const float own = S.group_max[tid];
+    int reach = 0;
+#pragma unroll
+    for (int j = 0; j < kGroups / 4; ++j) {
+      const float4 o = reinterpret_cast<const float4*>(S.group_max)[j];
+      reach += (o.x >= own) + (o.y >= own) + (o.z >= own) + (o.w >= own);
+    }
+    if (reach >= k) atomicMax(&S.thr, static_cast<uint32_t>(rank_key(own, 0) >> 32));
+  }
+  __syncthreads();
+  float thr = key_value(static_cast<uint64_t>(S.thr) << 32);
+  if (thr <= kMask) thr = -inf;   // what threads with masked logits only hold, or none
+  auto offer = [&](float x, int64_t i) {
+    if (x >= thr && x > -inf) {
+      const int at = atomicAdd(&S.n_cand, 1);
+      if (at < kCandidates) S.cand[at] = rank_key(x, i);
+    }
+  };
+  if (mine >= thr) {
+    S.sets[atomicAdd(&S.n_sets, 1)] = static_cast<uint8_t>(tid);
+    if (first && tid < r.head) offer(Elem<T>::value(r.x[tid]), tid);
+    if (last && tid < r.tail) offer(Elem<T>::value(r.x[r.tail0() + tid]), r.tail0() + tid);
+  }
+  __syncthreads();
+  // all threads read the vectors of those sets again
+  const int64_t per = (sg.nv / sg.segs + kThreads) / kThreads;   // vectors a thread has at most
+  for (int s = sg.s0; s < sg.s1; ++s) {
+    const int64_t v0 = sg.begin(s), v1 = sg.begin(s + 1);
+    const int64_t todo = S.n_sets * per;
+    for (int64_t q = tid; q < todo; q += kThreads) {
+      const int64_t set = div_nonneg(q, per);
+      const int64_t i = v0 + S.sets[set] + (q - set * per) * kThreads;
+      if (i >= v1) continue;
+      float v[VEC];
+      Elem<T>::unpack(r.vec(i), v);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) offer(v[j], r.head + i * VEC + j);
+    }
+  }
+  __syncthreads();
+  const int n = S.n_cand;
+  if (n <= kCandidates) {
+    rank_keys(S.cand, n, S.best, k);
+    __syncthreads();
+    return;
+  }
+  // Many equal logits: each warp keeps its k best in its lanes.
+  S.thread_max[tid] = mine;
+  __syncthreads();
+  uint64_t list = 0;
+  for (int j = warp; j < kThreads; j += kWarps) {
+    if (!(S.thread_max[j] >= thr)) continue;
+    float x = -inf;
+    int64_t at = 0;
+    if (lane == 0 && first && j < r.head) x = Elem<T>::value(r.x[at = j]);
+    if (lane == 1 && last && j < r.tail) x = Elem<T>::value(r.x[at = r.tail0() + j]);
+    if (first || last) list_offer(list, k, x, at, thr);
+    for (int s = sg.s0; s < sg.s1; ++s) {
+      const int64_t v1 = sg.begin(s + 1);
+      for (int64_t i0 = sg.begin(s) + j; i0 < v1; i0 += 32 * kThreads) {
+        const int64_t i = i0 + static_cast<int64_t>(lane) * kThreads;
+        float v[VEC];
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) v[q] = -inf;
+        if (i < v1) Elem<T>::unpack(r.vec(i), v);
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) list_offer(list, k, v[q], r.head + i * VEC + q, thr);
+      }
+    }
+  }
+  S.list[warp][lane] = list;
+  __syncthreads();
+  if (warp == 0) {
+    for (int w = 1; w < kWarps; ++w) list_join(list, S.list[w], k);
+    if (lane < k) S.best[lane] = list;
+  }
+  __syncthreads();
+}
+
+// One row per cluster of CTAs (of one CTA where there are rows enough). A row is
+// cut into segments by its length alone, a segment is summed by the 256 threads
+// of one CTA, and the segments are joined in order by the cluster's first CTA:
+// the results do not depend on how many CTAs shared a row.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Params p) {
   constexpr int VEC = Elem<T>::kVec;
-  __shared__ float s_m[kThreads];
-  __shared__ Stat s_stat[kWarps];
-  __shared__ uint32_t s_thr;
-  __shared__ uint64_t s_list[kWarps][32];
+  constexpr int UNROLL = 4;
+  __shared__ Shared S;
   pdl_wait();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x;
+  const int C = p.cluster;
+  const int rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int64_t row = C > 1 ? blockIdx.x / static_cast<unsigned>(C) : blockIdx.x;
   int64_t target = -1;
   if (p.targets) {
     target = p.targets64 ? static_cast<const int64_t*>(p.targets)[row]
                          : static_cast<const int32_t*>(p.targets)[row];
     if (target < 0) {   // a row without a token to score: nothing is read
+      if (rank != 0) return;
       if (tid == 0) {
         p.logprob[row] = 0.0f;
         if (p.entropy) p.entropy[row] = 0.0f;
@@ -182,42 +441,139 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Params p) {
       return;
     }
   }
+  if (C > 1) cluster_arrive();
   const Row<T> r(static_cast<const T*>(p.logits) + row * p.ld, p.V);
-  const float k2 = p.inv_t * kLog2e;
+  const Segments sg = {r.nv, p.segments, rank * (p.segments / C), (rank + 1) * (p.segments / C)};
+  const float k2 = p.k2;
   Stat st;
-  if (tid < r.head) {
-    const float x = Elem<T>::value(r.x[tid]);
-    if (x > st.m) st.raise(x, k2);
-    st.add(x, k2);
+  if (p.fast) {
+    const uint64_t kk = pair(k2, k2);
+    float mine = kMask;
+    for (int seg = sg.s0; seg < sg.s1; ++seg) {
+      st = Stat{kMask, 0.0f, 0.0f};
+      uint64_t s2 = 0, t2 = 0, m2 = pair(-kMask, -kMask);
+      auto up = [&](float mx) {   // a new maximum: rare after the first few vectors
+        const float d = (st.m - mx) * k2;
+        const float c = ex2(d);
+        const uint64_t cc = pair(c, c), dd = pair(d, d);
+        t2 = c > 0.0f ? mul2(cc, fma2(dd, s2, t2)) : 0;
+        s2 = mul2(cc, s2);
+        st.m = mx;
+        m2 = pair(-mx, -mx);
+      };
+      auto add = [&](const uint4& u) {
+        uint64_t x[VEC / 2];
+        float mx;
+        pairs_of(static_cast<const T*>(nullptr), u, x, mx);
+        if (mx > st.m) up(mx);
+#pragma unroll
+        for (int q = 0; q < VEC / 2; ++q) {
+          const uint64_t y = mul2(add2(x[q], m2), kk);
+          float a, b;
+          unpair(y, a, b);
+          const uint64_t e = pair(ex2(a), ex2(b));
+          s2 = add2(s2, e);
+          t2 = fma2(y, e, t2);
+        }
+      };
+      auto single = [&](float x) {
+        x = max_nan(x, kMask);
+        if (x > st.m) up(x);
+        float s, s1, t, t1;
+        unpair(s2, s, s1);
+        unpair(t2, t, t1);
+        const float y = (x - st.m) * k2;
+        const float e = ex2(y);
+        s2 = pair(s + e, s1);
+        t2 = pair(fmaf(y, e, t), t1);
+      };
+      if (seg == 0 && tid < r.head) single(Elem<T>::value(r.x[tid]));
+      if (seg == p.segments - 1 && tid < r.tail) single(Elem<T>::value(r.x[r.tail0() + tid]));
+      const int64_t v1 = sg.begin(seg + 1);
+      int64_t i = sg.begin(seg) + tid;
+      for (; i + (UNROLL - 1) * kThreads < v1; i += UNROLL * kThreads) {
+        uint4 u[UNROLL];
+#pragma unroll
+        for (int j = 0; j < UNROLL; ++j) u[j] = r.vec(i + j * kThreads);
+#pragma unroll
+        for (int j = 0; j < UNROLL; ++j) add(u[j]);
+      }
+      for (; i < v1; i += kThreads) add(r.vec(i));
+      float a, b;
+      unpair(s2, a, b);
+      st.s = a + b;
+      unpair(t2, a, b);
+      st.t = a + b;
+      mine = fmaxf(mine, st.m);
+      st = join_warp(st, k2);
+      if ((tid & 31) == 0) S.stat[seg - sg.s0][tid >> 5] = st;
+    }
+    join_segments(S, sg.s0, sg.s1 - sg.s0, k2);
+    if (p.k > 0) block_alternatives<T>(S, r, sg, mine, p.k);
+    if (C > 1) {
+      cluster_wait();   // all CTAs run: their shared memory can be written
+      if (rank != 0 && tid < 32) {
+        if (tid < sg.s1 - sg.s0) {
+          const Stat& o = S.part[sg.s0 + tid];
+          const uint32_t to = mapa_shared(smem_u32(&o), 0);
+          st_shared_cluster(to, __float_as_uint(o.m));
+          st_shared_cluster(to + 4, __float_as_uint(o.s));
+          st_shared_cluster(to + 8, __float_as_uint(o.t));
+        }
+        if (tid < p.k) {
+          const uint32_t at = mapa_shared(smem_u32(&S.part_best[rank][tid]), 0);
+          st_shared_cluster(at, static_cast<uint32_t>(S.best[tid]));
+          st_shared_cluster(at + 4, static_cast<uint32_t>(S.best[tid] >> 32));
+        }
+        __syncwarp();
+      }
+      cluster_arrive();
+      if (rank != 0) return;
+      cluster_wait();
+      if (p.k > 0) {   // the best of C sorted lists
+        const int n = C * p.k;
+        if (tid < p.k) S.part_best[0][tid] = S.best[tid];
+        __syncthreads();
+        if (tid < 32) S.best[tid] = 0;
+        for (int i = tid; i < n; i += kThreads) {
+          const int c = i / p.k;
+          S.cand[i] = S.part_best[c][i - c * p.k];
+        }
+        __syncthreads();
+        rank_keys(S.cand, n, S.best, p.k);
+      }
+    }
+    if (tid == 0) {
+      st = S.part[0];
+      for (int s = 1; s < p.segments; ++s) st.merge(S.part[s], k2);
+      S.row = st;
+    }
+    __syncthreads();
+    st = S.row;
   }
-  if (tid < r.tail) {
-    const float x = Elem<T>::value(r.x[r.tail0() + tid]);
-    if (x > st.m) st.raise(x, k2);
-    st.add(x, k2);
+  if (!p.fast || !fast_row(st.m)) {   // the first CTA does the whole row
+    const Segments all = {r.nv, 1, 0, 1};
+    st = Stat{kLowest, 0.0f, 0.0f};
+    if (tid < r.head) st.add_any(Elem<T>::value(r.x[tid]), k2);
+    if (tid < r.tail) st.add_any(Elem<T>::value(r.x[r.tail0() + tid]), k2);
+    for (int64_t i = tid; i < r.nv; i += kThreads) {
+      float x[VEC];
+      Elem<T>::unpack(r.vec(i), x);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) st.add_any(x[j], k2);
+    }
+    const float mine = st.m;
+    __syncthreads();   // S is written again
+    st = join_warp(st, k2);
+    if ((tid & 31) == 0) S.stat[0][tid >> 5] = st;
+    join_segments(S, 0, 1, k2);
+    st = S.part[0];
+    if (p.k > 0) block_alternatives<T>(S, r, all, mine, p.k);
   }
-  for (int64_t i = tid; i < r.nv; i += kThreads) {
-    float x[VEC];
-    Elem<T>::unpack(r.vec(i), x);
-    float vm = x[0];
-#pragma unroll
-    for (int j = 1; j < VEC; ++j) vm = fmaxf(vm, x[j]);
-    if (vm > st.m) st.raise(vm, k2);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) st.add(x[j], k2);
-  }
-  const float mine_max = st.m;
-  s_m[tid] = mine_max;
-  if (tid == 0) s_thr = 0;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) st.merge(shfl_xor(st, o), k2);
-  if (lane == 0) s_stat[warp] = st;
-  __syncthreads();
-  st = s_stat[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) st.merge(s_stat[w], k2);
   const float inf = __int_as_float(0x7F800000);
-  const float log_s = logf(st.s);
   const bool none = st.s == 0.0f;   // every logit is -inf
+  const float log2_s = log2f(st.s);
+  const float log_s = log2_s * kLn2;
   if (tid == 0) {
     if (p.targets) {
       float lp;
@@ -225,53 +581,19 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Params p) {
         set_status(p.status, MINITE_ERR_BAD_TOKEN);
         lp = __int_as_float(0x7FC00000);
       } else {
-        lp = none ? -inf : (Elem<T>::value(r.x[target]) - st.m) * p.inv_t - log_s;
+        lp = none ? -inf : fmaf(Elem<T>::value(r.x[target]) - st.m, p.inv_t, -log_s);
       }
       p.logprob[row] = lp;
     }
-    if (p.entropy) p.entropy[row] = none ? 0.0f : log_s - (st.t / st.s) * p.inv_t;
+    if (p.entropy) p.entropy[row] = none ? 0.0f : (log2_s - st.t / st.s) * kLn2;
     if (p.stats) p.stats[row] = make_float2(none ? -inf : st.m, none ? 0.0f : log_s);
   }
-  if (p.k == 0) return;
-  // threshold: the largest thread maximum that at least k maxima reach
-  int reach = 0;
-  for (int j = 0; j < kThreads; ++j) reach += s_m[j] >= mine_max ? 1 : 0;
-  if (reach >= p.k) atomicMax(&s_thr, static_cast<uint32_t>(rank_key(mine_max, 0) >> 32));
-  __syncthreads();
-  float thr = key_value(static_cast<uint64_t>(s_thr) << 32);
-  if (thr <= kLowest) thr = -inf;   // a thread without elements has this maximum too
-  uint64_t list = 0;
-  for (int j = warp; j < kThreads; j += kWarps) {
-    if (!(s_m[j] >= thr)) continue;
-    float x = -inf;
-    int64_t at = 0;
-    if (lane == 0 && j < r.head) x = Elem<T>::value(r.x[at = j]);
-    if (lane == 1 && j < r.tail) x = Elem<T>::value(r.x[at = r.tail0() + j]);
-    list_offer(list, p.k, x, at, thr);
-    for (int64_t i0 = j; i0 < r.nv; i0 += 32 * kThreads) {
-      const int64_t i = i0 + static_cast<int64_t>(lane) * kThreads;
-      float v[VEC];
-#pragma unroll
-      for (int q = 0; q < VEC; ++q) v[q] = -inf;
-      if (i < r.nv) Elem<T>::unpack(r.vec(i), v);
-#pragma unroll
-      for (int q = 0; q < VEC; ++q) list_offer(list, p.k, v[q], r.head + i * VEC + q, thr);
-    }
-  }
-  s_list[warp][lane] = list;
-  __syncthreads();
-  if (warp != 0) return;
-  for (int w = 1; w < kWarps; ++w)
-    for (int l = 0; l < p.k; ++l) {
-      const uint64_t cand = s_list[w][l];
-      if (cand <= __shfl_sync(0xffffffffu, list, p.k - 1)) break;   // the lists are sorted
-      list_insert(list, cand);
-    }
-  if (lane < p.k) {
-    const bool ok = list != 0 && st.s == st.s;   // a NaN or +inf logit: no ranking
-    p.alt_ids[row * p.k + lane] = ok ? key_index(list) : -1;
-    p.alt_lp[row * p.k + lane] =
-        st.s != st.s ? st.s : (ok ? (key_value(list) - st.m) * p.inv_t - log_s : -inf);
+  if (tid < p.k) {
+    const uint64_t key = S.best[tid];
+    const bool ok = key != 0 && st.s == st.s;   // a NaN or +inf logit: no ranking
+    p.alt_ids[row * p.k + tid] = ok ? key_index(key) : -1;
+    p.alt_lp[row * p.k + tid] =
+        st.s != st.s ? st.s : (ok ? fmaf(key_value(key) - st.m, p.inv_t, -log_s) : -inf);
   }
 }
 
@@ -297,7 +619,8 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(const BackParams p) {
   constexpr int VEC = Elem<T>::kVec;
   pdl_wait();
-  const int64_t row = blockIdx.y;
+  // last rows first: the forward read them last, so L2 still holds some
+  const int64_t row = gridDim.y - 1 - blockIdx.y;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kBackChunk;
   const int64_t c1 = c0 + kBackChunk < p.V ? c0 + kBackChunk : p.V;
   T* d = static_cast<T*>(p.d) + row * p.ldd;
@@ -316,39 +639,101 @@ __global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(const BackP
   const float gl = p.g_lp && p.targets && !zero ? p.g_lp[row] : 0.0f;
   const float ge = p.g_ent && !zero ? p.g_ent[row] : 0.0f;
   const float h = p.g_ent && !zero ? p.entropy[row] : 0.0f;
+  // d = q (a y + b) with y = log2 of the probability q
+  const float k2 = p.inv_t * kLog2e;
+  const float log2_s = st.y * kLog2e;
+  const float a = -ge * kLn2 * p.inv_t, b = -fmaf(ge, h, gl) * p.inv_t;
+  const float at_target = gl * p.inv_t;
   auto grad = [&](float v, int64_t j) {
-    const float lp = fmaf(v - st.x, p.inv_t, -st.y);
-    const float q = exp2f(lp * kLog2e);
-    float g = -q * fmaf(ge, fmaxf(lp, -1e30f) + h, gl);
-    if (j == target) g += gl;
-    return zero ? 0.0f : g * p.inv_t;
+    const float y = fmaf(v - st.x, k2, -log2_s);
+    const float g = ex2(y) * fmaf(a, fmaxf(y, -1e30f), b);
+    return j == target ? g + at_target : g;
   };
   const uintptr_t ax = reinterpret_cast<uintptr_t>(x + c0) & 15, ad = reinterpret_cast<uintptr_t>(d + c0) & 15;
-  int64_t a = c0, b = c0;
+  int64_t va = c0, vb = c0;
   if (ax == ad) {   // 16-byte vectors over the part where both rows are aligned
-    a = c0 + static_cast<int64_t>(((16 - ax) & 15) / sizeof(T));
-    if (a > c1) a = c1;
-    b = a + (c1 - a) / VEC * VEC;
+    va = c0 + static_cast<int64_t>(((16 - ax) & 15) / sizeof(T));
+    if (va > c1) va = c1;
+    vb = va + (c1 - va) / VEC * VEC;
   }
-  for (int64_t i = a + static_cast<int64_t>(threadIdx.x) * VEC; i < b; i += kThreads * VEC) {
-    float v[VEC];
-    if (!zero) Elem<T>::unpack(*reinterpret_cast<const uint4*>(x + i), v);
+  if (zero) {
+    for (int64_t i = va + static_cast<int64_t>(threadIdx.x) * VEC; i < vb; i += kThreads * VEC)
+      *reinterpret_cast<uint4*>(d + i) = make_uint4(0, 0, 0, 0);
+  } else if (fast_row(st.x) && fast_k(k2)) {
+    const uint64_t kk = pair(k2, k2), mm = pair(-st.x, -st.x), ll = pair(-log2_s, -log2_s);
+    const uint64_t aa = pair(a, a), bb = pair(b, b);
+    auto one = [&](const uint4& u, int64_t i) {
+      uint64_t v[VEC / 2];
+      float mx, g[VEC];
+      pairs_of(static_cast<const T*>(nullptr), u, v, mx);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) v[j] = zero ? 0.0f : grad(v[j], i + j);
-    if constexpr (sizeof(T) == 2)
-      *reinterpret_cast<uint4*>(d + i) =
-          make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]),
-                     pack_bf16x2_rn(v[4], v[5]), pack_bf16x2_rn(v[6], v[7]));
-    else
-      *reinterpret_cast<float4*>(d + i) = make_float4(v[0], v[1], v[2], v[3]);
+      for (int q = 0; q < VEC / 2; ++q) {
+        const uint64_t y = fma2(add2(v[q], mm), kk, ll);
+        float y0, y1;
+        unpair(y, y0, y1);
+        unpair(mul2(pair(ex2(y0), ex2(y1)), fma2(aa, y, bb)), g[2 * q], g[2 * q + 1]);
+      }
+      const int64_t hit = target - i;
+      if (hit >= 0 && hit < VEC) {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) g[q] += q == hit ? at_target : 0.0f;
+      }
+      if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<uint4*>(d + i) =
+            make_uint4(pack_bf16x2_rn(g[0], g[1]), pack_bf16x2_rn(g[2], g[3]),
+                       pack_bf16x2_rn(g[4], g[5]), pack_bf16x2_rn(g[6], g[7]));
+      else
+        *reinterpret_cast<float4*>(d + i) = make_float4(g[0], g[1], g[2], g[3]);
+    };
+    // four loads before the first store: d may be x, so the compiler keeps their order
+    constexpr int UNROLL = 4;
+    int64_t i = va + static_cast<int64_t>(threadIdx.x) * VEC;
+    for (; i + (UNROLL - 1) * kThreads * VEC < vb; i += UNROLL * kThreads * VEC) {
+      uint4 u[UNROLL];
+#pragma unroll
+      for (int j = 0; j < UNROLL; ++j) u[j] = *reinterpret_cast<const uint4*>(x + i + j * kThreads * VEC);
+#pragma unroll
+      for (int j = 0; j < UNROLL; ++j) one(u[j], i + j * kThreads * VEC);
+    }
+    for (; i < vb; i += kThreads * VEC) one(*reinterpret_cast<const uint4*>(x + i), i);
+  } else {
+    vb = va;   // element by element
   }
-  const int64_t rest = (a - c0) + (c1 - b);
+  const int64_t rest = (va - c0) + (c1 - vb);
   for (int64_t i = threadIdx.x; i < rest; i += kThreads) {
-    const int64_t j = i < a - c0 ? c0 + i : b + (i - (a - c0));
+    const int64_t j = i < va - c0 ? c0 + i : vb + (i - (va - c0));
     const float g = zero ? 0.0f : grad(Elem<T>::value(x[j]), j);
     if constexpr (sizeof(T) == 2) d[j] = static_cast<T>(pack_bf16x2_rn(g, 0.0f));
     else d[j] = g;
   }
+}
+
+template <typename T>
+cudaError_t launch_forward(Params& p, int64_t N, cudaStream_t s) {
+  // segments of about 128 KB; without the fast sums a row is summed as a whole
+  p.segments = 1;
+  while (p.fast && p.segments < kMaxSegments &&
+         p.V * static_cast<int64_t>(sizeof(T)) > kSegmentBytes * p.segments)
+    p.segments *= 2;
+  // CTAs per row: up to one a segment while about two an SM suffice for all rows
+  int c = p.segments;
+  while (c > 1 && N * c > 2 * num_sms()) c /= 2;
+  p.cluster = c;
+  if (N > 0x7FFFFFFF / c) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(N * c));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(c);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = c > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T>, p);
 }
 
 }  // namespace logprobs
@@ -380,6 +765,8 @@ extern "C" int minite_token_logprobs(const void* logits, int dtype, int64_t N, i
   p.targets = targets;
   p.targets64 = targets_int64;
   p.inv_t = 1.0f / temperature;
+  p.k2 = p.inv_t * kLog2e;
+  p.fast = fast_k(p.k2);
   p.logprob = logprob;
   p.entropy = entropy;
   p.stats = reinterpret_cast<float2*>(stats);
@@ -388,10 +775,8 @@ extern "C" int minite_token_logprobs(const void* logits, int dtype, int64_t N, i
   p.alt_lp = alt_logprobs;
   p.status = status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>(N));
-  const cudaError_t e = dtype == MINITE_OUT_FP32
-                            ? launch_pdl(logprobs_kernel<float>, grid, dim3(kThreads), 0, s, p)
-                            : launch_pdl(logprobs_kernel<uint16_t>, grid, dim3(kThreads), 0, s, p);
+  const cudaError_t e = dtype == MINITE_OUT_FP32 ? launch_forward<float>(p, N, s)
+                                                 : launch_forward<uint16_t>(p, N, s);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MINITE_OK : MINITE_ERR_CUDA;
 }
 

@@ -9,7 +9,6 @@ every call raises ``MiniteError``.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -358,72 +357,102 @@ def minite_moe_combine(expert_out, dest_row, y, status=None, stream=None):
     _check(rc, "minite_moe_combine")
 
 
+# The BF16 learner operators are called for as little as one token, so their
+# checks below build no text and no ctypes object unless something is wrong.
+_DTYPES = {torch.bfloat16: OUT_BF16, torch.float32: OUT_FP32}
+
+
 def _dtype(t, name):
     """OUT_BF16 or OUT_FP32 of a tensor."""
-    if t.dtype == torch.bfloat16:
-        return OUT_BF16
-    if t.dtype == torch.float32:
-        return OUT_FP32
-    raise MiniteError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise MiniteError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+    return d
 
 
-def _need(cond, what):
-    if not cond:
-        raise MiniteError(what)
+def _ptr(t):
+    """Device address of a tensor, None for None."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise MiniteError("expected a CUDA tensor")
+    return t.data_ptr()
+
+
+def _raw(stream, t):
+    """The stream's handle: t's device's current stream when none is given."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _rows(t, name):
-    """Row stride of a 2-D tensor whose rows are contiguous."""
-    _need(t.dim() == 2 and (t.shape[1] <= 1 or t.stride(1) == 1) and
-          (t.shape[0] <= 1 or t.stride(0) >= t.shape[1]),
-          f"{name}: expected 2-D with contiguous rows that do not overlap")
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+    """Row stride of a 2-D tensor whose rows are contiguous and do not overlap."""
+    n, c = t.shape
+    rs, cs = t.stride()
+    if (c > 1 and cs != 1) or (n > 1 and rs < c):
+        raise MiniteError(f"{name}: expected 2-D with contiguous rows that do not overlap")
+    return rs if n > 1 else (c + 7) // 8 * 8
+
+
+def _offsets(t, E, name):
+    if t.dtype is not torch.int32 or t.shape != (E + 1,) or not t.is_contiguous():
+        raise MiniteError(f"{name}: expert_offsets is int32 [E + 1], contiguous")
+    return _ptr(t)
 
 
 def minite_grouped_gemm_bf16(a, w, expert_offsets, out, w_layout=W_NK, status=None, stream=None):
     """a bf16 [M, K]; w bf16 [E, N, K] (W_NK) or [E, K, N] (W_KN); out [M, N] bf16 or fp32."""
     name = "minite_grouped_gemm_bf16"
-    E, N, K = w.shape if w_layout == W_NK else (w.shape[0], w.shape[2], w.shape[1])
-    _need(a.dtype == torch.bfloat16 and w.dtype == torch.bfloat16, f"{name}: a and w are bfloat16")
-    _need(expert_offsets.dtype == torch.int32 and expert_offsets.numel() == E + 1 and
-          expert_offsets.is_contiguous(), f"{name}: expert_offsets is int32 [E + 1]")
-    _need(w.is_contiguous(), f"{name}: w is contiguous")
-    _need(a.dim() == 2 and a.shape[1] == K and tuple(out.shape) == (a.shape[0], N),
-          f"{name}: shapes of a, w and out do not match")
-    rc = load().minite_grouped_gemm_bf16(_p(a), _rows(a, name), _p(w), w_layout, _p(expert_offsets),
-                                         a.shape[0], N, K, E, _p(out), _rows(out, name),
-                                         _dtype(out, name), _p(status), _s(stream))
-    _check(rc, name)
+    if a.dtype is not torch.bfloat16 or w.dtype is not torch.bfloat16 or not w.is_contiguous():
+        raise MiniteError(f"{name}: a and w are bfloat16, w contiguous")
+    E, N, K = w.shape
+    if w_layout == W_KN:
+        N, K = K, N
+    M, Ka = a.shape
+    if Ka != K or out.shape != (M, N):
+        raise MiniteError(f"{name}: shapes of a, w and out do not match")
+    rc = load().minite_grouped_gemm_bf16(_ptr(a), _rows(a, name), _ptr(w), w_layout,
+                                         _offsets(expert_offsets, E, name), M, N, K, E, _ptr(out),
+                                         _rows(out, name), _dtype(out, name), _ptr(status),
+                                         _raw(stream, a))
+    if rc:
+        _check(rc, name)
 
 
 def minite_grouped_wgrad_bf16(a, b, expert_offsets, out, accumulate=False, status=None, stream=None):
     """a bf16 [M, Na], b bf16 [M, Nb] in expert order; out [E, Na, Nb] bf16 or fp32."""
     name = "minite_grouped_wgrad_bf16"
+    if a.dtype is not torch.bfloat16 or b.dtype is not torch.bfloat16 or not out.is_contiguous():
+        raise MiniteError(f"{name}: a and b are bfloat16, out contiguous")
     E, Na, Nb = out.shape
-    _need(a.dtype == torch.bfloat16 and b.dtype == torch.bfloat16, f"{name}: a and b are bfloat16")
-    _need(expert_offsets.dtype == torch.int32 and expert_offsets.numel() == E + 1 and
-          expert_offsets.is_contiguous(), f"{name}: expert_offsets is int32 [E + 1]")
-    _need(out.is_contiguous(), f"{name}: out is contiguous")
-    _need(a.dim() == 2 and b.dim() == 2 and a.shape == (b.shape[0], Na) and b.shape[1] == Nb,
-          f"{name}: shapes of a, b and out do not match")
-    rc = load().minite_grouped_wgrad_bf16(_p(a), _rows(a, name), _p(b), _rows(b, name),
-                                          _p(expert_offsets), a.shape[0], Na, Nb, E, _p(out),
-                                          _dtype(out, name), 1 if accumulate else 0, _p(status),
-                                          _s(stream))
-    _check(rc, name)
+    M = a.shape[0]
+    if a.shape != (M, Na) or b.shape != (M, Nb):
+        raise MiniteError(f"{name}: shapes of a, b and out do not match")
+    rc = load().minite_grouped_wgrad_bf16(_ptr(a), _rows(a, name), _ptr(b), _rows(b, name),
+                                          _offsets(expert_offsets, E, name), M, Na, Nb, E, _ptr(out),
+                                          _dtype(out, name), 1 if accumulate else 0, _ptr(status),
+                                          _raw(stream, out))
+    if rc:
+        _check(rc, name)
 
 
 def _targets(targets, N, name):
     if targets is None:
         return 0
-    _need(targets.dtype in (torch.int32, torch.int64) and targets.shape == (N,) and
-          targets.is_contiguous(), f"{name}: targets is int32 or int64 [N], contiguous")
-    return 1 if targets.dtype == torch.int64 else 0
+    if targets.dtype not in (torch.int32, torch.int64) or targets.shape != (N,) or \
+            not targets.is_contiguous():
+        raise MiniteError(f"{name}: targets is int32 or int64 [N], contiguous")
+    return 1 if targets.dtype is torch.int64 else 0
 
 
 def _f32(t, shape, name, what):
-    _need(t is None or (t.dtype == torch.float32 and tuple(t.shape) == shape and t.is_contiguous()),
-          f"{name}: {what} is float32 {list(shape)}, contiguous")
+    """Device address of an FP32 tensor of this shape, None for None."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous():
+        raise MiniteError(f"{name}: {what} is float32 {list(shape)}, contiguous")
+    return _ptr(t)
 
 
 def minite_token_logprobs(logits, targets, logprob, entropy=None, stats=None, temperature=1.0,
@@ -433,18 +462,20 @@ def minite_token_logprobs(logits, targets, logprob, entropy=None, stats=None, te
     name = "minite_token_logprobs"
     ld = _rows(logits, name)
     N, V = logits.shape
-    k = 0 if alt_ids is None else alt_ids.shape[1]
-    t64 = _targets(targets, N, name)
-    _f32(logprob, (N,), name, "logprob")
-    _f32(entropy, (N,), name, "entropy")
-    _f32(stats, (N, 2), name, "stats")
-    _f32(alt_logprobs, (N, k), name, "alt_logprobs")
-    _need(alt_ids is None or (alt_ids.dtype == torch.int32 and alt_ids.shape[0] == N and
-                              alt_ids.is_contiguous()), f"{name}: alt_ids is int32 [N, k]")
-    rc = load().minite_token_logprobs(_p(logits), _dtype(logits, name), N, V, ld, _p(targets), t64,
-                                      float(temperature), _p(logprob), _p(entropy), _p(stats), k,
-                                      _p(alt_ids), _p(alt_logprobs), _p(status), _s(stream))
-    _check(rc, name)
+    k = 0
+    if alt_ids is not None:
+        k = alt_ids.shape[1]
+        if alt_ids.dtype is not torch.int32 or alt_ids.shape[0] != N or not alt_ids.is_contiguous():
+            raise MiniteError(f"{name}: alt_ids is int32 [N, k], contiguous")
+    rc = load().minite_token_logprobs(_ptr(logits), _dtype(logits, name), N, V, ld,
+                                      _ptr(targets), _targets(targets, N, name), temperature,
+                                      _f32(logprob, (N,), name, "logprob"),
+                                      _f32(entropy, (N,), name, "entropy"),
+                                      _f32(stats, (N, 2), name, "stats"), k, _ptr(alt_ids),
+                                      _f32(alt_logprobs, (N, k), name, "alt_logprobs"),
+                                      _ptr(status), _raw(stream, logits))
+    if rc:
+        _check(rc, name)
 
 
 def minite_token_logprobs_backward(logits, targets, stats, entropy, grad_logprob, grad_entropy,
@@ -453,19 +484,15 @@ def minite_token_logprobs_backward(logits, targets, stats, entropy, grad_logprob
     name = "minite_token_logprobs_backward"
     ld = _rows(logits, name)
     N, V = logits.shape
-    t64 = _targets(targets, N, name)
-    _need(dlogits.dtype == logits.dtype and dlogits.shape == logits.shape,
-          f"{name}: dlogits has the type and shape of logits")
-    _need(stats is not None, f"{name}: stats of the forward are needed")
-    _f32(stats, (N, 2), name, "stats")
-    _f32(entropy, (N,), name, "entropy")
-    _f32(grad_logprob, (N,), name, "grad_logprob")
-    _f32(grad_entropy, (N,), name, "grad_entropy")
+    if dlogits.dtype is not logits.dtype or dlogits.shape != logits.shape or stats is None:
+        raise MiniteError(f"{name}: needs the forward's stats, and dlogits of the type and shape of logits")
     rc = load().minite_token_logprobs_backward(
-        _p(logits), _dtype(logits, name), N, V, ld, _p(targets), t64, float(temperature), _p(stats),
-        _p(entropy), _p(grad_logprob), _p(grad_entropy), _p(dlogits), _rows(dlogits, name),
-        _p(status), _s(stream))
-    _check(rc, name)
+        _ptr(logits), _dtype(logits, name), N, V, ld, _ptr(targets), _targets(targets, N, name),
+        temperature, _f32(stats, (N, 2), name, "stats"), _f32(entropy, (N,), name, "entropy"),
+        _f32(grad_logprob, (N,), name, "grad_logprob"), _f32(grad_entropy, (N,), name, "grad_entropy"),
+        _ptr(dlogits), _rows(dlogits, name), _ptr(status), _raw(stream, logits))
+    if rc:
+        _check(rc, name)
 
 
 # struct minite_adamw_tensor
@@ -477,11 +504,11 @@ ADAMW_TENSOR = np.dtype([("param", "u8"), ("grad", "u8"), ("exp_avg", "u8"), ("e
 def minite_adamw_step(tensors, param_dtype, grad_dtype, state_bits, lr, beta1, beta2, eps,
                       weight_decay, step, grad_scale=None, stream=None):
     """tensors: numpy array of ADAMW_TENSOR on the host, one descriptor a tensor."""
-    _need(tensors.dtype == ADAMW_TENSOR and tensors.flags.c_contiguous,
-          "minite_adamw_step: tensors is a contiguous array of ADAMW_TENSOR")
+    if tensors.dtype != ADAMW_TENSOR or not tensors.flags.c_contiguous:
+        raise MiniteError("minite_adamw_step: tensors is a contiguous array of ADAMW_TENSOR")
     rc = load().minite_adamw_step(tensors.ctypes.data, len(tensors), param_dtype, grad_dtype,
                                   state_bits, lr, beta1, beta2, eps, weight_decay, step,
-                                  _p(grad_scale), _s(stream))
+                                  _ptr(grad_scale), _s(stream))
     _check(rc, "minite_adamw_step")
 
 
@@ -534,9 +561,17 @@ def quantize(x, per_group=False, along_rows=False, g_in=None, stream=None):
     return dict(codes=codes, sf=sf, g=g)
 
 
-def _on(stream):
-    """Allocations made inside belong to the stream that the kernels run on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _need(cond, what):
+    if not cond:
+        raise MiniteError(what)
+
+
+def _empty(shape, dtype, like, stream):
+    """A new tensor that belongs to the stream that the kernel runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def grouped_gemm_bf16(x, w, expert_offsets, w_as_stored=False, out=None, out_dtype=torch.bfloat16,
@@ -546,9 +581,7 @@ def grouped_gemm_bf16(x, w, expert_offsets, w_as_stored=False, out=None, out_dty
     (the activation gradient of that forward, x its output's gradient).
     Returns [M, N]."""
     if out is None:
-        with _on(stream):
-            out = torch.empty((x.shape[0], w.shape[2 if w_as_stored else 1]), dtype=out_dtype,
-                              device=x.device)
+        out = _empty((x.shape[0], w.shape[2 if w_as_stored else 1]), out_dtype, x, stream)
     minite_grouped_gemm_bf16(x, w, expert_offsets, out, W_KN if w_as_stored else W_NK, status, stream)
     return out
 
@@ -558,10 +591,9 @@ def grouped_wgrad_bf16(dy, x, expert_offsets, out=None, out_dtype=torch.float32,
     """dw[e] = dy_e.T @ x_e over each expert's rows, [E, Na, Nb]; added to
     ``out`` (fp32) with ``accumulate``."""
     if out is None:
-        _need(not accumulate, "grouped_wgrad_bf16: accumulate needs out")
-        with _on(stream):
-            out = torch.empty((expert_offsets.numel() - 1, dy.shape[1], x.shape[1]), dtype=out_dtype,
-                              device=x.device)
+        if accumulate:
+            raise MiniteError("grouped_wgrad_bf16: accumulate needs out")
+        out = _empty((expert_offsets.numel() - 1, dy.shape[1], x.shape[1]), out_dtype, x, stream)
     minite_grouped_wgrad_bf16(dy, x, expert_offsets, out, accumulate, status, stream)
     return out
 
@@ -571,14 +603,13 @@ def token_logprobs(logits, targets=None, temperature=1.0, alternatives=0, status
     temperature), with the row's entropy and its ``alternatives`` most likely
     tokens. Returns dict(logprob (None without targets), entropy, stats,
     alt_ids, alt_logprobs); a negative target marks a row that is skipped."""
-    N, dev = logits.shape[0], logits.device
-    with _on(stream):
-        f32 = torch.empty((4, N), dtype=torch.float32, device=dev)
-        r = dict(logprob=None if targets is None else f32[0], entropy=f32[1],
-                 stats=f32[2:].view(N, 2), alt_ids=None, alt_logprobs=None)
-        if alternatives:
-            r["alt_ids"] = torch.empty((N, alternatives), dtype=torch.int32, device=dev)
-            r["alt_logprobs"] = torch.empty((N, alternatives), dtype=torch.float32, device=dev)
+    N, f32 = logits.shape[0], torch.float32
+    r = dict(logprob=None if targets is None else _empty((N,), f32, logits, stream),
+             entropy=_empty((N,), f32, logits, stream), stats=_empty((N, 2), f32, logits, stream),
+             alt_ids=None, alt_logprobs=None)
+    if alternatives:
+        r["alt_ids"] = _empty((N, alternatives), torch.int32, logits, stream)
+        r["alt_logprobs"] = _empty((N, alternatives), f32, logits, stream)
     minite_token_logprobs(logits, targets, r["logprob"], r["entropy"], r["stats"], temperature,
                           r["alt_ids"], r["alt_logprobs"], status, stream)
     return r
@@ -590,8 +621,7 @@ def token_logprobs_backward(logits, targets, forward, grad_logprob=None, grad_en
     logits; ``forward`` is its result for the same logits, targets and
     temperature. ``out`` may be the logits themselves."""
     if out is None:
-        with _on(stream):
-            out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        out = _empty(logits.shape, logits.dtype, logits, stream)
     minite_token_logprobs_backward(logits, targets, forward["stats"], forward["entropy"],
                                    grad_logprob, grad_entropy, out, temperature, status, stream)
     return out
@@ -651,12 +681,10 @@ class AdamW:
     def step(self, grads, grad_scale=None, lr=None, stream=None):
         """One step with grads[i] (bf16 or fp32, all one type) for tensor i, each
         times the device scalar ``grad_scale``."""
-        _need(len(grads) == len(self.params), "AdamW.step: one gradient a parameter")
-        kind = grads[0].dtype
-        for g, n in zip(grads, self._numel):
-            if not (g.is_cuda and g.dtype == kind and g.numel() == n and g.is_contiguous()):
-                raise MiniteError("AdamW.step: gradients are contiguous CUDA tensors of one type, "
-                                  "each of its parameter's size")
+        if [g.numel() for g in grads] != self._numel or len({g.dtype for g in grads}) != 1 or \
+                not all([g.is_contiguous() and g.is_cuda for g in grads]):
+            raise MiniteError("AdamW.step: gradients are contiguous CUDA tensors of one type, one a "
+                              "parameter and of its size")
         _need(grad_scale is None or (grad_scale.dtype == torch.float32 and grad_scale.numel() == 1),
               "AdamW.step: grad_scale is one float32")
         self._tensors["grad"] = [g.data_ptr() for g in grads]
