@@ -21,6 +21,16 @@
 //    tcgen05.mma.cta_group::2: each loads 128 features and half the rows, K
 //    consumed 64 values (128 bytes) a stage, and holds 128 x N sums in TMEM,
 //    twice, so that a tile's epilogue runs under the next one's products.
+//  * Two such pairs share a cluster of four and one of their operands, each
+//    box of which is loaded once and multicast to both pairs: an expert of up
+//    to 256 rows gives them two feature tiles of the same rows, a larger one
+//    two tiles of rows of the same features. What bounds pairs that share
+//    nothing is the traffic from L2, about 44 bytes a cycle and SM (32 KB for
+//    the 512 cycles of a full stage are 64; shared, 48): 8 experts of 8192 rows,
+//    2048 x 1536, took 255 us, now 233. Two tiles of rows on separate clusters
+//    also fetched part of the weight twice from DRAM.
+//  * Large experts (bound by the tensor cores) and small ones (bound by DRAM)
+//    are interleaved, so that both are busy all the time.
 //  * Operands come by TMA with the 128-byte swizzle, K-major (rows of 64 K
 //    values) or, where memory has the other dimension contiguous (dgrad's
 //    weight, both operands of the weight gradient), MN-major: boxes of 64 such
@@ -60,20 +70,20 @@ constexpr int A_BYTES = 128 * 128;                // this CTA's 128 features
 constexpr int B_BYTES = (MAX_N / 2) * 128;        // this CTA's half of the rows
 constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int BOX_BYTES = 64 * 128;               // MN-major box: 64 values x 64 K rows
-constexpr int ROW_BOX = 32;                       // rows of a K-major box of tokens
+constexpr int kTokenBoxes = 4;                    // K-major boxes of 16, 32, 64 and 128 tokens
 constexpr int NUM_EPI_WARPS = 16;                 // four per TMEM lane quarter, 64 columns each
 constexpr int EPI_WARP0 = 2;
-constexpr int NUM_THREADS = (EPI_WARP0 + NUM_EPI_WARPS) * 32;
+constexpr int B_WARP = EPI_WARP0 + NUM_EPI_WARPS;   // the rows' producer
+constexpr int NUM_THREADS = (B_WARP + 1) * 32;
 constexpr int EPI_COLS = MAX_N / (NUM_EPI_WARPS / 4);
 constexpr int kChunkBlocks = 4;                   // FP32 outputs: K blocks summed in TMEM at a time
 constexpr size_t kMaxSmem = 232448;
-constexpr uint16_t kBoth = 0x3;
 
 enum Mode { FORWARD = 0, DGRAD = 1, WGRAD = 2 };
 
 struct Smem {
-  uint64_t full[MAX_STAGES];        // even CTA: both CTAs' copies have landed
-  uint64_t empty[MAX_STAGES];
+  uint64_t full[MAX_STAGES];        // even CTA: all copies to both CTAs have landed
+  uint64_t empty[MAX_STAGES];       // every pair of the cluster is done with the stage
   uint64_t tail_full[MAX_STAGES];   // odd CTA: its copies of a stage with rows to zero
   uint64_t tail_ready[MAX_STAGES];  // even CTA: the odd CTA has zeroed them
   uint64_t acc_full[2];
@@ -94,55 +104,95 @@ struct Params {
   int F;           // features: columns of the output
   int K;           // forward, dgrad: length of the sums; wgrad: output rows of an expert
   int E;
+  int units;       // wgrad: length of the list of work
   int max_n;       // rows of a tile at most, a multiple of 32
+  int by_rows;     // wgrad: the cluster's pairs take two row tiles, not two feature tiles
+  int a_two, b_two;  // the maps of two boxes of features (wgrad: of output rows) serve
   int stages;
   int chunk;       // K blocks summed in TMEM before the epilogue takes them
   int accumulate;  // FP32 output: added to what it holds
   uint64_t budget_ns;
 };
 
+// Boxes of every size that a stage can need: a stage is two copies a CTA.
+struct Maps {
+  CUtensorMap a1, a2;           // 64 and 128 features
+  CUtensorMap b[kTokenBoxes];   // tokens; wgrad: b[0], b[1] are 64 and 128 output rows
+};
+
 struct Tile {
   int e, f0;
+  bool by_rows;    // the cluster's pairs share the features, not the rows
   int row0;        // forward, dgrad: first token; wgrad: first of the rows summed over
   int i0;          // wgrad: first output row within the expert
   int64_t orow0;   // first output row
-  int rows;        // output rows of the tile
+  int rows;        // output rows of the tile (none in a pair that ran out of them)
   int n;           // rows the matrix instruction covers: `rows` rounded up to 32
   int len;         // length of the sums
 };
 
+// The list of a cluster's work: for each expert the tiles of its two pairs.
+struct Work {
+  const int32_t* off;      // [E+1]
+  const int32_t* large;    // [E+1] units of the larger experts before e
+  const int32_t* small;    // [E+1] units of the experts of at most max_n rows before e
+  int f_tiles;
+};
+
+__device__ __forceinline__ int expert_of(const int32_t* prefix, int E, int u) {
+  int lo = 0, hi = E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= u) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Unit t of the list, for one of the cluster's pairs.
 template <int MODE>
-__device__ __forceinline__ Tile decode(int t, int f_tiles, const int32_t* prefix,
-                                       const int32_t* off, const Params& p) {
+__device__ __forceinline__ Tile decode(int t, int pair, const Work& w, const Params& p) {
   Tile r;
-  const int bt = t / f_tiles;
-  r.f0 = (t - bt * f_tiles) * BF;
+  const int f_groups = (w.f_tiles + 1) >> 1;
   if constexpr (MODE == WGRAD) {
-    const int per = (p.K + p.max_n - 1) / p.max_n;
-    r.e = bt / per;
-    r.i0 = (bt - r.e * per) * p.max_n;
-    r.row0 = off[r.e];
+    r.by_rows = p.by_rows;
+    const int per_row = r.by_rows ? w.f_tiles : f_groups;
+    const int bt = t / per_row, f = t - bt * per_row;
+    const int i_tiles = (p.K + p.max_n - 1) / p.max_n;
+    const int per_e = r.by_rows ? (i_tiles + 1) >> 1 : i_tiles;
+    r.e = bt / per_e;
+    const int it = bt - r.e * per_e;
+    r.f0 = (r.by_rows ? f : 2 * f + pair) * BF;
+    r.i0 = (r.by_rows ? 2 * it + pair : it) * p.max_n;
+    r.row0 = w.off[r.e];
     r.orow0 = static_cast<int64_t>(r.e) * p.K + r.i0;
-    r.rows = min(p.max_n, p.K - r.i0);
-    r.len = off[r.e + 1] - off[r.e];
+    r.rows = max(0, min(p.max_n, p.K - r.i0));
+    r.len = w.off[r.e + 1] - w.off[r.e];
   } else {
-    int lo = 0, hi = p.E;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (prefix[mid] <= bt) lo = mid; else hi = mid;
+    // the larger experts' units spread evenly over the list
+    const int64_t L = w.large[p.E], all = L + w.small[p.E];
+    const int before = static_cast<int>(div_nonneg(t * L, all));
+    r.by_rows = div_nonneg((t + 1) * L, all) > before;
+    int at = 0, size = p.max_n;
+    if (r.by_rows) {
+      r.e = expert_of(w.large, p.E, before);
+      const int u = before - w.large[r.e];
+      const int twos = (w.large[r.e + 1] - w.large[r.e]) / w.f_tiles;   // pairs of row tiles
+      const int cnt = w.off[r.e + 1] - w.off[r.e];
+      size = ((cnt + 2 * twos - 1) / (2 * twos) + 31) & ~31;            // about equal tiles
+      r.f0 = (u % w.f_tiles) * BF;
+      at = (2 * (u / w.f_tiles) + pair) * size;
+    } else {
+      const int u = t - before;
+      r.e = expert_of(w.small, p.E, u);
+      r.f0 = (2 * (u - w.small[r.e]) + pair) * BF;   // may lie past the last feature
     }
-    r.e = lo;
-    // an expert's tiles have about the same number of rows
-    const int cnt = off[lo + 1] - off[lo], tiles = prefix[lo + 1] - prefix[lo];
-    const int size = ((cnt + tiles - 1) / tiles + 31) & ~31;
-    const int at = (bt - prefix[lo]) * size;
     r.i0 = 0;
-    r.row0 = off[lo] + at;
+    r.row0 = w.off[r.e] + at;
     r.orow0 = r.row0;
-    r.rows = min(size, cnt - at);
+    r.rows = max(0, min(size, w.off[r.e + 1] - r.row0));
     r.len = p.K;
   }
-  r.n = (r.rows + 31) & ~31;
+  r.n = max(32, (r.rows + 31) & ~31);
   return r;
 }
 
@@ -164,15 +214,30 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b
       :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// 3-D TMA load whose completion is counted on an mbarrier of either CTA.
-__device__ __forceinline__ void tma_load_3d_pair(void* dst, const void* desc, uint32_t mbar_cluster,
-                                                 int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile"
-      ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
-      :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(desc)), "r"(mbar_cluster), "r"(x),
-         "r"(y), "r"(z)
-      : "memory");
+// TMA loads for the pairs of a cluster. Plain: into this CTA, counted on an
+// mbarrier of either CTA of its pair. Multicast: into the same place of every
+// CTA in `mask`, counted there on the barrier at mbar's place of that CTA or of
+// the other one of its pair, whichever has the parity of mbar's CTA.
+template <int D>
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, uint32_t mbar, bool mc,
+                                              uint16_t mask, int x, int y, int z = 0, int w = 0) {
+  const uint32_t d = smem_u32(dst);
+  const uint64_t m = reinterpret_cast<uint64_t>(map);
+#define MINITE_TMA(dim, mcast, coords, ...)                                                        \
+  asm volatile("cp.async.bulk.tensor." dim ".cta_group::2.shared::cluster.global.tile"             \
+               ".mbarrier::complete_tx::bytes" mcast " [%0], [%1, " coords "], [%2]" __VA_ARGS__    \
+               :: "r"(d), "l"(m), "r"(mbar), "h"(mask), "r"(x), "r"(y), "r"(z), "r"(w) : "memory")
+  if constexpr (D == 2) {
+    if (mc) MINITE_TMA("2d", ".multicast::cluster", "{%4, %5}", ", %3;");
+    else MINITE_TMA("2d", "", "{%4, %5}", ";");
+  } else if constexpr (D == 3) {
+    if (mc) MINITE_TMA("3d", ".multicast::cluster", "{%4, %5, %6}", ", %3;");
+    else MINITE_TMA("3d", "", "{%4, %5, %6}", ";");
+  } else {
+    if (mc) MINITE_TMA("4d", ".multicast::cluster", "{%4, %5, %6, %7}", ", %3;");
+    else MINITE_TMA("4d", "", "{%4, %5, %6, %7}", ";");
+  }
+#undef MINITE_TMA
 }
 
 // Arrival and wait that order shared-memory writes between the two CTAs.
@@ -257,28 +322,32 @@ __device__ __forceinline__ void store_64rows(float* out, int64_t ldo, int rows, 
 
 template <int MODE, bool F32>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
-grouped_bf16_kernel(const __grid_constant__ CUtensorMap tmap_a,
-                    const __grid_constant__ CUtensorMap tmap_b, const Params p) {
+grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
   constexpr bool A_MN = MODE != FORWARD, B_MN = MODE == WGRAD;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Smem& S = *reinterpret_cast<Smem*>(stages + p.stages * STAGE_BYTES);
-  int32_t* s_off = reinterpret_cast<int32_t*>(&S + 1);   // [E+1]
-  int32_t* s_prefix = s_off + (p.E + 1);                 // [E+1] row tiles of the experts before
+  int32_t* s_off = reinterpret_cast<int32_t*>(&S + 1);   // [E+1] each
+  int32_t* s_large = s_off + (p.E + 1);
+  int32_t* s_small = s_large + (p.E + 1);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
+  const uint32_t rank4 = cluster_ctarank();
+  const uint32_t rank = rank4 & 1u;                      // within the pair
+  const uint32_t leader = rank4 & ~1u;                   // the pair's even CTA
+  const int pair = static_cast<int>(rank4 >> 1);         // within the cluster
   const int cid = static_cast<int>(cluster_id_x());
   const int ncl = static_cast<int>(num_clusters_x());
-  const int f_tiles = (p.F + BF - 1) / BF;
+  const Work work = {s_off, s_large, s_small, (p.F + BF - 1) / BF};
+  const uint16_t pair_mask = static_cast<uint16_t>(0x3u << leader);
 
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmap_a);
-    tma_prefetch_desc(&tmap_b);
+    tma_prefetch_desc(&maps.a1);
+    tma_prefetch_desc(&maps.a2);
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&S.full[s], 1);
-      mbar_init(&S.empty[s], 1);
+      mbar_init(&S.empty[s], 2);
       mbar_init(&S.tail_full[s], 1);
       mbar_init(&S.tail_ready[s], 1);
     }
@@ -293,32 +362,43 @@ grouped_bf16_kernel(const __grid_constant__ CUtensorMap tmap_a,
   if (warp == 1) tmem_alloc_pair(&S.tmem_base, 2 * MAX_N);
   pdl_wait();
   if (warp == 2) {
-    int carry = 0;
+    int n_large = 0, n_small = 0;
     bool bad = false;
-    if (lane == 0) s_prefix[0] = 0;
+    if (lane == 0) {
+      s_large[0] = 0;
+      s_small[0] = 0;
+    }
     for (int base = 0; base < p.E; base += 32) {
       const int e = base + lane;
-      int cnt = 0;
+      int large = 0, small = 0;
       if (e < p.E) {
         const int o0 = __ldg(p.offsets + e), o1 = __ldg(p.offsets + e + 1);
         s_off[e + 1] = o1;
         if (e == 0) s_off[0] = o0;
         if (o1 < o0 || (e == 0 && o0 != 0) || (e == p.E - 1 && o1 > p.M)) bad = true;
-        cnt = o1 > o0 ? (o1 - o0 + p.max_n - 1) / p.max_n : 0;
+        const int cnt = o1 - o0;
+        if (cnt > p.max_n) large = (cnt + 2 * p.max_n - 1) / (2 * p.max_n) * work.f_tiles;
+        else if (cnt > 0) small = (work.f_tiles + 1) >> 1;
       }
-      int incl = cnt;
+      int il = large, is = small;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
+        const int tl = __shfl_up_sync(0xffffffffu, il, o), ts = __shfl_up_sync(0xffffffffu, is, o);
+        if (lane >= o) {
+          il += tl;
+          is += ts;
+        }
       }
-      if (e < p.E) s_prefix[e + 1] = carry + incl;
-      carry += __shfl_sync(0xffffffffu, incl, 31);
+      if (e < p.E) {
+        s_large[e + 1] = n_large + il;
+        s_small[e + 1] = n_small + is;
+      }
+      n_large += __shfl_sync(0xffffffffu, il, 31);
+      n_small += __shfl_sync(0xffffffffu, is, 31);
     }
     bad = __any_sync(0xffffffffu, bad);
-    if (MODE == WGRAD) carry = p.E * ((p.K + p.max_n - 1) / p.max_n);
     if (lane == 0) {
-      S.total_tiles = bad ? 0 : carry * f_tiles;
+      S.total_tiles = bad ? 0 : MODE == WGRAD ? p.units : n_large + n_small;
       if (bad && blockIdx.x == 0) set_status(p.status, MINITE_ERR_INVALID_ARG);
     }
   }
@@ -330,12 +410,11 @@ grouped_bf16_kernel(const __grid_constant__ CUtensorMap tmap_a,
   const uint32_t tmem = S.tmem_base;
   const int total = S.total_tiles;
   volatile int* abort_flag = &S.abort_flag;
-  const uint32_t peer_abort = mapa_shared(smem_u32(&S.abort_flag), rank ^ 1u);
   const uint64_t budget = p.budget_ns;
   constexpr uint64_t kDrainBudget = 200000000ull;
   auto fail = [&]() {
-    *abort_flag = 1;
-    st_shared_cluster(peer_abort, 1u);
+    for (int c = 0; c < 4; ++c)
+      st_shared_cluster(mapa_shared(smem_u32(&S.abort_flag), c), 1u);
     set_status(p.status, MINITE_ERR_TIMEOUT);
   };
   // the stage whose rows [left, 16 steps) belong to the next expert
@@ -349,67 +428,105 @@ grouped_bf16_kernel(const __grid_constant__ CUtensorMap tmap_a,
     __syncwarp();
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      const uint32_t leader_full0 = mapa_shared(smem_u32(&S.full[0]), 0);
-      uint32_t armed_mask = 0, armed_parity = 0;
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int t = cid; t < total && ok; t += ncl) {
-        const Tile tl = decode<MODE>(t, f_tiles, s_prefix, s_off, p);
-        const int kt_n = (tl.len + BK - 1) / BK;
-        const int half = tl.n / 2;
-        const int f0 = tl.f0 + 128 * static_cast<int>(rank);
-        const int b0 = (B_MN ? tl.i0 : tl.row0) + half * static_cast<int>(rank);
-        const int b_boxes = B_MN ? (half + 63) / 64 : (half + ROW_BOX - 1) / ROW_BOX;
-        const uint32_t bytes = A_BYTES + b_boxes * (B_MN ? BOX_BYTES : ROW_BOX * 128);
-        for (int kt = 0; kt < kt_n; ++kt) {
-          if (!mbar_wait(&S.empty[stage], phase ^ 1u, budget, abort_flag)) { ok = false; break; }
-          uint8_t* sA = stages + stage * STAGE_BYTES;
-          uint8_t* sB = sA + A_BYTES;
-          const int left = tl.len - kt * BK;
-          const bool tail = MODE == WGRAD && left < BK && left % 16 != 0;
-          uint32_t bar = leader_full0 + 8u * stage;
-          if (rank == 0) {
-            mbar_arrive_expect_tx(&S.full[stage], tail ? bytes : 2 * bytes);
-          } else if (tail) {
-            mbar_arrive_expect_tx(&S.tail_full[stage], bytes);
-            bar = smem_u32(&S.tail_full[stage]);
-          }
-          const int k0 = MODE == WGRAD ? tl.row0 + kt * BK : kt * BK;
-          if constexpr (MODE == FORWARD) {
-            tma_load_3d_pair(sA, &tmap_a, bar, k0, f0, tl.e);
-          } else if constexpr (MODE == DGRAD) {
-            tma_load_3d_pair(sA, &tmap_a, bar, f0, k0, tl.e);
-            tma_load_3d_pair(sA + BOX_BYTES, &tmap_a, bar, f0 + 64, k0, tl.e);
-          } else {
-            tma_load_2d_pair(sA, &tmap_a, bar, f0, k0);
-            tma_load_2d_pair(sA + BOX_BYTES, &tmap_a, bar, f0 + 64, k0);
-          }
-          for (int b = 0; b < b_boxes; ++b) {
-            if constexpr (B_MN) tma_load_2d_pair(sB + b * BOX_BYTES, &tmap_b, bar, b0 + 64 * b, k0);
-            else tma_load_2d_pair(sB + b * ROW_BOX * 128, &tmap_b, bar, k0, b0 + ROW_BOX * b);
-          }
-          armed_mask |= 1u << stage;
-          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+  if (warp == 0 || warp == B_WARP) {
+    // ------------------------------------------------------------ producers: features, rows
+    const bool is_a = warp == 0;
+    // The whole warp runs the loop and one elected lane issues, so that a
+    // copy's operands are warp-uniform. Each copy costs its warp about 180 cycles,
+    // so the two operands have a warp each and a stage is one or two copies of it.
+    const uint16_t both = rank == 0 ? 0x5 : 0xA;   // the CTAs of this rank of both pairs
+    const uint32_t leader_full0 = mapa_shared(smem_u32(&S.full[0]), leader);
+    uint32_t armed_mask = 0, armed_parity = 0;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = cid; t < total && ok; t += ncl) {
+      const Tile tl = decode<MODE>(t, pair, work, p);
+      const int kt_n = (tl.len + BK - 1) / BK;
+      const int half = tl.n / 2;
+      const int f0 = tl.f0 + 128 * static_cast<int>(rank);
+      // Features: 128 of its own, or 64 from each pair to both. Rows: its half
+      // of them in a main box and a second one, both its own, or one from each
+      // pair to both. Boxes hold 2^i 16 rows (wgrad: 64), the main one at least
+      // half of them: rows that nobody needs cost traffic from L2.
+      int box, box2;   // index of the main box and of the second, -1 if there is none
+      if constexpr (B_MN) {
+        box = 0;
+        box2 = half > 64 ? 0 : -1;
+      } else if (tl.by_rows && half == 128) {
+        box = 3;
+        box2 = -1;
+      } else {
+        box = 28 - __clz((half / 2 - 1) | 15);
+        box2 = half > 16 << box ? 28 - __clz((half - (16 << box) - 1) | 15) : -1;
+      }
+      const int main_rows = (B_MN ? 64 : 16) << box;
+      const int b0 = (B_MN ? tl.i0 : tl.row0) + half * static_cast<int>(rank);
+      const uint32_t bytes =
+          A_BYTES + 128 * (main_rows + (box2 >= 0 ? (B_MN ? 64 : 16) << box2 : 0));
+      const bool first_box = tl.by_rows || pair == 0, second_box = box2 >= 0 && (tl.by_rows || pair == 1);
+      const int f_box = tl.by_rows ? f0 + 64 * pair : f0;
+      const bool a_two = !tl.by_rows && p.a_two;
+      const bool b_two = B_MN && tl.by_rows && box2 >= 0 && p.b_two && b0 % 64 == 0;
+      for (int kt = 0; kt < kt_n; ++kt) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&S.empty[stage], phase ^ 1u, budget, abort_flag))) {
+          ok = false;
+          break;
         }
+        uint8_t* sA = stages + stage * STAGE_BYTES;
+        uint8_t* sB = sA + A_BYTES;
+        const int left = tl.len - kt * BK;
+        const bool tail = MODE == WGRAD && left < BK && left % 16 != 0;
+        const uint32_t bar = rank != 0 && tail ? smem_u32(&S.tail_full[stage]) : leader_full0 + 8u * stage;
+        const int k0 = MODE == WGRAD ? tl.row0 + kt * BK : kt * BK;
+        uint8_t* dst = sA + (tl.by_rows ? pair * BOX_BYTES : 0);
+        const CUtensorMap* am = a_two ? &maps.a2 : &maps.a1;
+        if (is_a && elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(&S.full[stage], tail ? bytes : 2 * bytes);
+          else if (tail) mbar_arrive_expect_tx(&S.tail_full[stage], bytes);
+          if constexpr (MODE == FORWARD) {
+            tma_load_pair<3>(dst, am, bar, tl.by_rows, both, k0, f_box, tl.e);
+          } else if constexpr (MODE == DGRAD) {
+            if (a_two) tma_load_pair<4>(dst, am, bar, false, both, 0, k0, f_box / 64, tl.e);
+            else tma_load_pair<3>(dst, am, bar, tl.by_rows, both, f_box, k0, tl.e);
+          } else {
+            if (a_two) tma_load_pair<3>(dst, am, bar, false, both, 0, k0, f_box / 64);
+            else tma_load_pair<2>(dst, am, bar, tl.by_rows, both, f_box, k0);
+          }
+          if (A_MN && !tl.by_rows && !a_two) {   // features that do not come in whole boxes
+            if constexpr (MODE == DGRAD)
+              tma_load_pair<3>(sA + BOX_BYTES, am, bar, false, both, f_box + 64, k0, tl.e);
+            else tma_load_pair<2>(sA + BOX_BYTES, am, bar, false, both, f_box + 64, k0);
+          }
+        }
+        if (!is_a && elect_one()) {
+          const uint32_t at2 = main_rows * 128;
+          if constexpr (B_MN) {
+            if (b_two) {
+              tma_load_pair<3>(sB, &maps.b[1], bar, false, both, 0, k0, b0 / 64);
+            } else {
+              if (first_box) tma_load_pair<2>(sB, &maps.b[0], bar, !tl.by_rows, both, b0, k0);
+              if (second_box) tma_load_pair<2>(sB + at2, &maps.b[0], bar, !tl.by_rows, both, b0 + 64, k0);
+            }
+          } else {
+            if (first_box) tma_load_pair<2>(sB, &maps.b[box], bar, !tl.by_rows, both, k0, b0);
+            if (second_box)
+              tma_load_pair<2>(sB + at2, &maps.b[box2], bar, !tl.by_rows, both, k0, b0 + main_rows);
+          }
+        }
+        __syncwarp();
+        armed_mask |= 1u << stage;
+        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == p.stages) { stage = 0; phase ^= 1u; }
       }
-      if (!ok) fail();
-      volatile int no_abort = 0;
-      if (rank == 0) {
-        // every armed stage's copies must have landed before exit
-        for (int s = 0; s < p.stages; ++s)
-          if (armed_mask & (1u << s))
-            mbar_wait(&S.full[s], (armed_parity >> s) & 1u, kDrainBudget, &no_abort);
-      } else if (!ok) {
-        // this CTA's copies count on the other CTA's barriers: give any copy
-        // still in flight time to land before the CTA can exit
-        const uint64_t t0 = globaltimer();
-        while (globaltimer() - t0 < 100000ull) {}
-      }
+    }
+    if (!ok && lane == 0) fail();
+    volatile int no_abort = 0;
+    if (is_a && rank == 0) {
+      // every armed stage's copies must have landed before exit
+      for (int s = 0; s < p.stages; ++s)
+        if (armed_mask & (1u << s))
+          mbar_wait(&S.full[s], (armed_parity >> s) & 1u, kDrainBudget, &no_abort);
     }
   } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
@@ -426,7 +543,7 @@ grouped_bf16_kernel(const __grid_constant__ CUtensorMap tmap_a,
     uint32_t phase = 0, acc_phase = 0, tail_parity = 0;
     bool ok = true, issued = false;
     for (int t = cid; t < total && ok; t += ncl) {
-      const Tile tl = decode<MODE>(t, f_tiles, s_prefix, s_off, p);
+      const Tile tl = decode<MODE>(t, pair, work, p);
       const uint32_t idesc = idesc_base<MODE>() | (static_cast<uint32_t>(tl.n >> 3) << 17);
       int in_chunk = 0;
       for (int left = tl.len; left > 0; left -= BK) {
@@ -451,8 +568,8 @@ grouped_bf16_kernel(const __grid_constant__ CUtensorMap tmap_a,
             if (s < ks)
               mma_bf16_pair(acc, adesc0 + soff + a_step * s, bdesc0 + soff + b_step * s, idesc,
                             (in_chunk | s) != 0);
-          tc_commit_pair_mc(&S.empty[stage], kBoth);
-          if (last) tc_commit_pair_mc(&S.acc_full[buf], kBoth);
+          tc_commit_pair_mc(&S.empty[stage], 0xF);
+          if (last) tc_commit_pair_mc(&S.acc_full[buf], pair_mask);
         }
         __syncwarp();
         issued = true;
@@ -468,7 +585,7 @@ grouped_bf16_kernel(const __grid_constant__ CUtensorMap tmap_a,
     if (!ok && lane == 0) fail();
     if (issued) {
       // all MMAs complete before TMEM is freed
-      if (elect_one()) tc_commit_pair_mc(&S.drain, 0x1);
+      if (elect_one()) tc_commit_pair_mc(&S.drain, static_cast<uint16_t>(1u << leader));
       __syncwarp();
       volatile int no_abort = 0;
       mbar_wait(&S.drain, 0, kDrainBudget, &no_abort);
@@ -476,12 +593,12 @@ grouped_bf16_kernel(const __grid_constant__ CUtensorMap tmap_a,
   } else if (warp == 1) {
     // ------------------------------------------------------------ tail rows of the odd CTA
     if constexpr (MODE == WGRAD) {
-      const uint32_t leader_ready0 = mapa_shared(smem_u32(&S.tail_ready[0]), 0);
+      const uint32_t leader_ready0 = mapa_shared(smem_u32(&S.tail_ready[0]), leader);
       int stage = 0;
       uint32_t tail_parity = 0;
       bool ok = true;
       for (int t = cid; t < total && ok; t += ncl) {
-        const Tile tl = decode<MODE>(t, f_tiles, s_prefix, s_off, p);
+        const Tile tl = decode<MODE>(t, pair, work, p);
         const int kt_n = (tl.len + BK - 1) / BK;
         if (kt_n == 0) continue;
         stage = (stage + kt_n - 1) % p.stages;   // the sum's last stage
@@ -499,14 +616,14 @@ grouped_bf16_kernel(const __grid_constant__ CUtensorMap tmap_a,
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const uint32_t leader_acc_empty0 = mapa_shared(smem_u32(&S.acc_empty[0]), 0);
+    const uint32_t leader_acc_empty0 = mapa_shared(smem_u32(&S.acc_empty[0]), leader);
     const int quarter = warp & 3;
     const int c0 = ((warp - EPI_WARP0) >> 2) * EPI_COLS;   // this warp's rows of a tile
     int buf = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
     for (int t = cid; t < total && ok; t += ncl) {
-      const Tile tl = decode<MODE>(t, f_tiles, s_prefix, s_off, p);
+      const Tile tl = decode<MODE>(t, pair, work, p);
       const int chunks = ((tl.len + BK - 1) / BK + p.chunk - 1) / p.chunk;
       if (chunks == 0 && p.accumulate) continue;
       const int rows = tl.rows - c0;
@@ -573,6 +690,13 @@ grouped_bf16_kernel(const __grid_constant__ CUtensorMap tmap_a,
     if (!ok && lane == 0) fail();
   }
 
+  // after a wait that ran out, copies of a stage that was not armed may still be
+  // in flight: give them time to land before a CTA can exit
+  if (warp == 0 && *abort_flag) {
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 100000ull) {}
+  }
+  __syncwarp();
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
@@ -581,23 +705,31 @@ grouped_bf16_kernel(const __grid_constant__ CUtensorMap tmap_a,
 
 namespace {
 
-// BF16 tensor of up to three dimensions (innermost first, strides in elements
-// of the outer two), 128-byte swizzle, zeros outside.
-bool make_map(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, uint64_t ld1, uint64_t d2,
-              uint64_t ld2, uint32_t box1) {
+// BF16 tensor, 128-byte swizzle, zeros outside: dimensions innermost first,
+// strides in elements of all but the innermost, a box of 64 x box1 x box2.
+bool make_map(CUtensorMap* m, const void* base, int dims, const cuuint64_t (&d)[4],
+              const cuuint64_t (&ld)[3], uint32_t box1, uint32_t box2 = 1) {
   auto fn = tensor_map_encoder();
   if (!fn) return false;
-  cuuint64_t dims[3] = {d0, d1, d2};
-  cuuint64_t strides[2] = {ld1 * 2, ld2 * 2};
-  cuuint32_t box[3] = {64, box1, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d2 ? 3 : 2, const_cast<void*>(base), dims, strides,
-            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  cuuint64_t strides[3] = {ld[0] * 2, ld[1] * 2, ld[2] * 2};
+  cuuint32_t box[4] = {64, box1, box2, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, const_cast<void*>(base), d, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows x columns (row stride ld) as 64 x 64 boxes: `one` box, and `two` boxes
+// side by side where the columns are whole boxes (else *two_ok is 0).
+bool make_column_maps(CUtensorMap* one, CUtensorMap* two, int* two_ok, const void* base, cuuint64_t rows,
+                      cuuint64_t cols, cuuint64_t ld) {
+  *two_ok = cols % 64 == 0;
+  return make_map(one, base, 2, {cols, rows}, {ld}, 64) &&
+         (!*two_ok || make_map(two, base, 3, {64, rows, cols / 64}, {ld, 64}, 64, 2));
 }
 
 template <int MODE, bool F32>
-int launch_as(const CUtensorMap& ta, const CUtensorMap& tb, Params& p, cudaStream_t s) {
+int launch_as(const Maps& maps, Params& p, cudaStream_t s) {
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
@@ -608,31 +740,44 @@ int launch_as(const CUtensorMap& ta, const CUtensorMap& tb, Params& p, cudaStrea
   if (attr_err != cudaSuccess) return MINITE_ERR_CUDA;
   p.chunk = F32 ? kChunkBlocks : 1 << 30;
   p.budget_ns = wait_budget_ns();
-  const size_t rest = 1024 + sizeof(Smem) + 2 * (static_cast<size_t>(p.E) + 1) * sizeof(int32_t);
+  const size_t rest = 1024 + sizeof(Smem) + 3 * (static_cast<size_t>(p.E) + 1) * sizeof(int32_t);
   p.stages = static_cast<int>((kMaxSmem - rest) / STAGE_BYTES);
   if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
   const size_t smem = rest + static_cast<size_t>(p.stages) * STAGE_BYTES;
-  int pairs = resident_pairs<10 + 2 * MODE + F32>(grouped_bf16_kernel<MODE, F32>, NUM_THREADS, smem);
-  if (pairs <= 0) return MINITE_ERR_CUDA;
-  const int64_t f_tiles = (p.F + BF - 1) / BF;
-  // tiles of 256 rows, narrower ones where those would leave most pairs idle
-  p.max_n = MAX_N;
-  auto row_tiles = [&](int n) {
-    return MODE == WGRAD ? p.E * ((static_cast<int64_t>(p.K) + n - 1) / n) : (p.M + n - 1) / n;
+  int clusters = resident_clusters<10 + 2 * MODE + F32>(grouped_bf16_kernel<MODE, F32>, 4, NUM_THREADS, smem);
+  if (clusters <= 0) return MINITE_ERR_CUDA;
+  const int64_t f_tiles = (p.F + BF - 1) / BF, f_groups = (f_tiles + 1) / 2;
+  // units of work with tiles of n rows (forward and dgrad: if all experts had as many rows)
+  auto units = [&](int64_t n) -> int64_t {
+    if (MODE == WGRAD) {
+      const int64_t i_tiles = (p.K + n - 1) / n;
+      return p.E * (p.by_rows ? (i_tiles + 1) / 2 * f_tiles : i_tiles * f_groups);
+    }
+    const int64_t experts = p.E < p.M ? p.E : p.M;
+    const int64_t rows = (p.M + experts - 1) / experts;
+    return experts * (rows > n ? (rows + 2 * n - 1) / (2 * n) * f_tiles : f_groups);
   };
-  while (p.max_n > 64 && row_tiles(p.max_n) * f_tiles * 2 <= pairs) p.max_n /= 2;
-  const int64_t most = (MODE == WGRAD ? row_tiles(p.max_n) : p.M / p.max_n + (p.E < p.M ? p.E : p.M)) * f_tiles;
+  // tiles of 256 rows, narrower ones where those would leave most clusters idle
+  p.by_rows = f_tiles % 2 != 0;
+  p.max_n = MAX_N;
+  while (p.max_n > 64 && units(p.max_n) * 2 <= clusters) p.max_n /= 2;
+  // at most (forward and dgrad): every expert's last unit may be nearly empty
+  const int64_t most = MODE == WGRAD
+                           ? units(p.max_n)
+                           : (p.M / (2 * p.max_n) + (p.E < p.M ? p.E : p.M)) * f_tiles;
   if (most > 0x7FFFFFFF) return MINITE_ERR_UNSUPPORTED_SHAPE;
-  if (most < pairs) pairs = static_cast<int>(most);
-  if (launch_pair_pdl(grouped_bf16_kernel<MODE, F32>, pairs, NUM_THREADS, smem, s, ta, tb, p) != cudaSuccess)
+  p.units = static_cast<int>(most);
+  if (most < clusters) clusters = static_cast<int>(most);
+  if (launch_clusters_pdl(grouped_bf16_kernel<MODE, F32>, clusters, 4, NUM_THREADS, smem, s, maps, p) !=
+      cudaSuccess)
     return MINITE_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MINITE_OK : MINITE_ERR_CUDA;
 }
 
 template <int MODE>
-int launch(const CUtensorMap& ta, const CUtensorMap& tb, Params& p, int out_dtype, cudaStream_t s) {
-  return out_dtype == MINITE_OUT_FP32 ? launch_as<MODE, true>(ta, tb, p, s)
-                                      : launch_as<MODE, false>(ta, tb, p, s);
+int launch(const Maps& maps, Params& p, int out_dtype, cudaStream_t s) {
+  return out_dtype == MINITE_OUT_FP32 ? launch_as<MODE, true>(maps, p, s)
+                                      : launch_as<MODE, false>(maps, p, s);
 }
 
 constexpr int64_t kMaxDim = int64_t(1) << 20;
@@ -660,12 +805,23 @@ extern "C" int minite_grouped_gemm_bf16(const void* a, int64_t a_stride, const v
   if (!a || !w || !expert_offsets || !out) return MINITE_ERR_INVALID_ARG;
   if (!aligned(a, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(expert_offsets, 4))
     return MINITE_ERR_INVALID_ARG;
-  CUtensorMap ta, tb;
   const bool nk = w_layout == MINITE_W_NK;
-  if (nk ? !make_map(&ta, w, K, N, K, E, N * K, 128) : !make_map(&ta, w, N, K, N, E, N * K, 64))
-    return MINITE_ERR_CUDA;
-  if (!make_map(&tb, a, K, M_total, a_stride, 0, 0, ROW_BOX)) return MINITE_ERR_CUDA;
+  Maps maps = {};
   Params p = {};
+  const cuuint64_t un = N, uk = K, ue = E, um = M_total, us = a_stride;
+  bool ok = true;
+  if (nk) {
+    p.a_two = 1;
+    ok = make_map(&maps.a1, w, 3, {uk, un, ue}, {uk, un * uk}, 64) &&
+         make_map(&maps.a2, w, 3, {uk, un, ue}, {uk, un * uk}, 128);
+  } else {
+    p.a_two = N % 64 == 0;   // else a box of two could reach past the last row's end
+    ok = make_map(&maps.a1, w, 3, {un, uk, ue}, {un, un * uk}, 64) &&
+         (!p.a_two || make_map(&maps.a2, w, 4, {64, uk, un / 64, ue}, {un, 64, un * uk}, 64, 2));
+  }
+  for (int i = 0; i < kTokenBoxes; ++i)
+    ok = ok && make_map(&maps.b[i], a, 2, {uk, um}, {us}, 16u << i);
+  if (!ok) return MINITE_ERR_CUDA;
   p.offsets = expert_offsets;
   p.out = out;
   p.ldo = out_stride;
@@ -675,7 +831,7 @@ extern "C" int minite_grouped_gemm_bf16(const void* a, int64_t a_stride, const v
   p.K = static_cast<int>(K);
   p.E = E;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return nk ? launch<FORWARD>(ta, tb, p, out_dtype, s) : launch<DGRAD>(ta, tb, p, out_dtype, s);
+  return nk ? launch<FORWARD>(maps, p, out_dtype, s) : launch<DGRAD>(maps, p, out_dtype, s);
 }
 
 extern "C" int minite_grouped_wgrad_bf16(const void* a, int64_t a_stride, const void* b,
@@ -694,11 +850,11 @@ extern "C" int minite_grouped_wgrad_bf16(const void* a, int64_t a_stride, const 
   if (!expert_offsets || !out || (M_total > 0 && (!a || !b))) return MINITE_ERR_INVALID_ARG;
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(out, 16) || !aligned(expert_offsets, 4))
     return MINITE_ERR_INVALID_ARG;
-  CUtensorMap ta = {}, tb = {};   // without rows no copy is issued
-  if (M_total > 0 && (!make_map(&ta, b, Nb, M_total, b_stride, 0, 0, 64) ||
-                      !make_map(&tb, a, Na, M_total, a_stride, 0, 0, 64)))
-    return MINITE_ERR_CUDA;
+  Maps maps = {};   // without rows no copy is issued
   Params p = {};
+  if (M_total > 0 && (!make_column_maps(&maps.a1, &maps.a2, &p.a_two, b, M_total, Nb, b_stride) ||
+                      !make_column_maps(&maps.b[0], &maps.b[1], &p.b_two, a, M_total, Na, a_stride)))
+    return MINITE_ERR_CUDA;
   p.offsets = expert_offsets;
   p.out = out;
   p.ldo = Nb;
@@ -708,5 +864,5 @@ extern "C" int minite_grouped_wgrad_bf16(const void* a, int64_t a_stride, const 
   p.K = static_cast<int>(Na);
   p.E = E;
   p.accumulate = accumulate ? 1 : 0;
-  return launch<WGRAD>(ta, tb, p, out_dtype, reinterpret_cast<cudaStream_t>(stream));
+  return launch<WGRAD>(maps, p, out_dtype, reinterpret_cast<cudaStream_t>(stream));
 }
