@@ -755,6 +755,14 @@ int minite_test_convert_digest(unsigned long long first_chunk, unsigned long lon
 int minite_test_div6_exhaustive(unsigned long long* mismatches, minite_stream_t stream);
 
 /*
+ * Test hook: the optimizer computes roots and quotients of pairs from the
+ * hardware's approximations with a correction. This adds, into the device
+ * counters mismatches[2] (caller zeroes them), how many of 4 * 2^24 roots and
+ * of 2^31 quotients differ from the IEEE ones (expected: 0).
+ */
+int minite_test_adamw_math(unsigned long long* mismatches, minite_stream_t stream);
+
+/*
  * Test hook for failure detection: sets the time budget of every bounded
  * pipeline wait (the GEMM and the streaming kernels that stage rows through
  * shared memory with asynchronous copies; nanoseconds; 0 restores the

@@ -12,9 +12,22 @@
 // zero code: it takes the smallest one instead, since a v of 0 beside an m
 // that is not would divide the step by eps alone.
 //
-// Every operation is one IEEE float operation in the order written above (no
-// contraction), so that the codes do not depend on how a compiler fuses them.
+// Every operation is rounded to nearest on its own in the order written above
+// (no contraction), so that the codes do not depend on how a compiler fuses
+// them. Where the moments lie in the usual range, two elements go through the
+// packed FP32 instructions with a root and a quotient of their own; the rest
+// (zeros among them) takes the IEEE ones.
+//
+// Bound by HBM. FP32 states (28 bytes an element with a BF16 copy): plain 16-byte
+// loads, 604M elements in 2.41 ms, 7.0 TB/s. 8-bit states (10 bytes an element
+// with BF16 parameters and gradients, 55 instructions): asynchronous copies three
+// reads ahead, the scales of 64 blocks read and written at once; 400M elements
+// in 0.65 ms, 6.2 TB/s (1.11 ms with plain loads and IEEE roots and quotients).
+// Up to 440 tensors' pointers travel as kernel parameters (48 in a small set),
+// so that a step is one launch and nothing is copied to the device first.
 #include <cmath>
+#include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "host_util.h"
@@ -24,7 +37,8 @@ namespace adamw {
 
 constexpr int kBlock = 256;      // elements per 8-bit scale
 constexpr int kThreads = 256;
-constexpr int kChunk = 4096;     // elements per CTA
+// Elements per CTA. The 8-bit states' CTAs run longer to fill their pipeline less often.
+__host__ __device__ constexpr int64_t chunk_elements(bool eight) { return eight ? 16384 : 4096; }
 constexpr float kInvMax = 1.0f / 448.0f;  // rounded to FP32
 constexpr float kTiny = 1.17549435e-38f;  // 2^-126
 
@@ -42,6 +56,7 @@ struct Tensor {
 struct Hyper {
   float b1, c1, b2, c2;      // beta1, 1 - beta1, beta2, 1 - beta2
   float keep, rate, isq, eps;  // 1 - lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+  float minus_zero;          // -0
   const float* scale;        // device factor of the gradients, or null
 };
 
@@ -53,39 +68,80 @@ struct Batch {
   Tensor t[CAP];
 };
 
-__device__ __forceinline__ void update(float& p, float g, float& m, float& v, float& r,
-                                       const Hyper& h) {
-  m = __fadd_rn(__fmul_rn(m, h.b1), __fmul_rn(g, h.c1));
-  v = __fadd_rn(__fmul_rn(v, h.b2), __fmul_rn(__fmul_rn(g, g), h.c2));
-  r = __fsqrt_rn(v);
-  const float u = __fdiv_rn(m, __fadd_rn(__fmul_rn(r, h.isq), h.eps));
-  p = __fsub_rn(__fmul_rn(p, h.keep), __fmul_rn(u, h.rate));
+__device__ __forceinline__ uint64_t twice(float x) { return pair(x, x); }
+
+// A product that no sum after it is contracted with: packed products and sums
+// are, in spite of their rounding modifiers, unless the product has an addend
+// that the compiler does not know (nz, -0: the product rounded once).
+struct Product {
+  uint64_t nz;
+  __device__ __forceinline__ uint64_t operator()(uint64_t a, uint64_t b) const { return fma2(a, b, nz); }
+};
+
+// sqrt(v) of two floats in [2^-100, 2^100], correctly rounded: the remainder of
+// v y, y the hardware's approximate 1 / sqrt(v), corrects it (Markstein, 1990;
+// equal to the IEEE root for every significand, counted on the device).
+__device__ __forceinline__ uint64_t sqrt2_rn(uint64_t v) {
+  float a, b, ya, yb;
+  unpair(v, a, b);
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(ya) : "f"(a));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(yb) : "f"(b));
+  const uint64_t y = pair(ya, yb), r = mul2(v, y);
+  return fma2(fma2(mul2(r, twice(-1.0f)), r, v), mul2(y, twice(0.5f)), r);
 }
 
-// Eight consecutive elements from index i of a tensor of n; `vec` when all
-// eight exist and the address is 16-byte aligned.
+// m / d of two floats, |m| <= 2^60 and d in [2^-51, 2^51] or so, rounded to
+// nearest in the same way from 1 / d after a Newton step (equal to the IEEE
+// quotient in 2^36 pairs drawn on the device).
+__device__ __forceinline__ uint64_t div2_rn(uint64_t m, uint64_t d) {
+  float a, b, ya, yb;
+  unpair(d, a, b);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(ya) : "f"(a));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(yb) : "f"(b));
+  const uint64_t y0 = pair(ya, yb), nd = mul2(d, twice(-1.0f));
+  const uint64_t y = fma2(fma2(nd, y0, twice(1.0f)), y0, y0);
+  const uint64_t q = mul2(m, y);
+  return fma2(fma2(nd, q, m), y, q);
+}
+
+// The larger magnitude, with some sign; NaN if either is.
+__device__ __forceinline__ float max_abs_nan(float a, float b) {
+  float d;
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Eight consecutive elements as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T* a, int64_t i, int64_t n, bool vec, float (&x)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    if (vec) {
-      const float4 u = *reinterpret_cast<const float4*>(a + i);
-      const float4 w = *reinterpret_cast<const float4*>(a + i + 4);
-      x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-      x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
-    } else {
+struct Raw8 {
+  uint4 w[sizeof(T) / 2];   // BF16: one, FP32: two (codes below: half of one)
+  __device__ __forceinline__ void load(const T* a) {   // 16-byte aligned
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = i + j < n ? static_cast<float>(a[i + j]) : 0.0f;
-    }
-  } else {
-    if (vec) {
-      unpack_bf16x8(*reinterpret_cast<const uint4*>(a + i), x);
-    } else {
+    for (int j = 0; j < static_cast<int>(sizeof(T) / 2); ++j) w[j] = reinterpret_cast<const uint4*>(a)[j];
+  }
+  __device__ __forceinline__ void load(const T* a, int64_t left) {   // any alignment, `left` exist
+    uint32_t* u = reinterpret_cast<uint32_t*>(w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        x[j] = i + j < n ? __uint_as_float(static_cast<uint32_t>(a[i + j]) << 16) : 0.0f;
+    for (int j = 0; j < 8; ++j) {
+      if constexpr (sizeof(T) == 4) {
+        u[j] = j < left ? __float_as_uint(a[j]) : 0u;
+      } else {
+        const uint32_t x = j < left ? static_cast<uint32_t>(a[j]) : 0u;
+        u[j >> 1] = (j & 1) ? u[j >> 1] | (x << 16) : x;
+      }
     }
   }
-}
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    if constexpr (sizeof(T) == 4) {
+      x[0] = __uint_as_float(w[0].x); x[1] = __uint_as_float(w[0].y);
+      x[2] = __uint_as_float(w[0].z); x[3] = __uint_as_float(w[0].w);
+      x[4] = __uint_as_float(w[1].x); x[5] = __uint_as_float(w[1].y);
+      x[6] = __uint_as_float(w[1].z); x[7] = __uint_as_float(w[1].w);
+    } else {
+      unpack_bf16x8(w[0], x);
+    }
+  }
+};
 
 template <typename T>
 __device__ __forceinline__ void store8(T* a, int64_t i, int64_t n, bool vec, const float (&x)[8]) {
@@ -125,21 +181,26 @@ __device__ __forceinline__ void e4m3x2_values(uint32_t c, float& lo, float& hi) 
       : "=f"(lo), "=f"(hi) : "r"(h));
 }
 
-__device__ __forceinline__ void load_codes(const uint8_t* a, int64_t i, int64_t n, bool vec,
-                                           float (&x)[8]) {
-  uint32_t w[2] = {0, 0};
-  if (vec) {
-    const uint2 u = *reinterpret_cast<const uint2*>(a + i);
-    w[0] = u.x;
-    w[1] = u.y;
-  } else {
+// Eight E4M3 codes.
+template <>
+struct Raw8<uint8_t> {
+  uint2 w;
+  __device__ __forceinline__ void load(const uint8_t* a) { w = *reinterpret_cast<const uint2*>(a); }
+  __device__ __forceinline__ void load(const uint8_t* a, int64_t left) {
+    uint32_t u[2] = {0, 0};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (i + j < n) w[j >> 2] |= static_cast<uint32_t>(a[i + j]) << (8 * (j & 3));
+      if (j < left) u[j >> 2] |= static_cast<uint32_t>(a[j]) << (8 * (j & 3));
+    w = make_uint2(u[0], u[1]);
   }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) e4m3x2_values((w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu, x[2 * j], x[2 * j + 1]);
-}
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t c = j < 2 ? w.x : w.y;
+      e4m3x2_values((c >> (16 * (j & 1))) & 0xFFFFu, x[2 * j], x[2 * j + 1]);
+    }
+  }
+};
 
 __device__ __forceinline__ void store_codes(uint8_t* a, int64_t i, int64_t n, bool vec,
                                             const float (&x)[8]) {
@@ -156,25 +217,93 @@ __device__ __forceinline__ void store_codes(uint8_t* a, int64_t i, int64_t n, bo
   }
 }
 
-// Scale of a block whose largest magnitude is the warp's: the bits of
-// non-negative floats order as integers, NaN above all, so that a block with
-// a NaN gets a NaN scale.
-__device__ __forceinline__ float warp_block_scale(float amax) {
-  const float a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+// Scale of a block whose largest magnitude is a.
+__device__ __forceinline__ float block_scale_of(float a) {
   const float s = __fmul_rn(a, kInvMax);
   return s < kTiny ? kTiny : s;
 }
-
-__device__ __forceinline__ float abs_max_nan(const float (&x)[8]) {
-  uint32_t b = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) b = max(b, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-  return __uint_as_float(b);
+// The warp's largest non-negative float: their bits order as integers, NaN
+// above all, so that a block with a NaN gets a NaN scale.
+__device__ __forceinline__ float warp_max_nan(float a) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
 }
+
+// What a thread reads for its eight elements.
+template <typename P, typename G, bool EIGHT>
+struct Input {
+  using S = std::conditional_t<EIGHT, uint8_t, float>;
+  Raw8<P> p;
+  Raw8<G> g;
+  Raw8<S> m, v;
+  // `wide`: parameters and gradients are 16-byte aligned; `full`: all eight exist
+  __device__ __forceinline__ void load(const Tensor& t, int64_t i, bool full, bool wide) {
+    const P* tp = static_cast<const P*>(t.p) + i;
+    const G* tg = static_cast<const G*>(t.g) + i;
+    const S* tm = static_cast<const S*>(t.m) + i;
+    const S* tv = static_cast<const S*>(t.v) + i;
+    if (full && wide) {
+      p.load(tp);
+      g.load(tg);
+    } else {
+      p.load(tp, t.n - i);
+      g.load(tg, t.n - i);
+    }
+    if (full) {
+      m.load(tm);
+      v.load(tv);
+    } else {
+      m.load(tm, t.n - i);
+      v.load(tv, t.n - i);
+    }
+  }
+};
+
+// The same by asynchronous copies to slots of shared memory that only this
+// thread uses (so that no barrier is needed), kDepth reads ahead. The 8-bit
+// states need it: their step has 55 instructions an element for 10 bytes, and
+// with loads into registers a warp waited 40% of its time for them.
+constexpr int kDepth = 3;
+template <typename T>
+struct Slots {
+  static constexpr int kWords = sizeof(T) == 1 ? 1 : sizeof(T) / 2;
+  using Word = std::conditional_t<sizeof(T) == 1, uint2, uint4>;
+  Word w[kWords][kThreads];
+  __device__ __forceinline__ void fetch(const T* a) {
+#pragma unroll
+    for (int j = 0; j < kWords; ++j)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;"
+                   :: "r"(smem_u32(&w[j][threadIdx.x])), "l"(reinterpret_cast<const Word*>(a) + j),
+                      "n"(sizeof(Word)) : "memory");
+  }
+  __device__ __forceinline__ void take(Raw8<T>& r) const {
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) reinterpret_cast<Word*>(&r)[j] = w[j][threadIdx.x];
+  }
+};
+template <typename P, typename G>
+struct Stage {
+  Slots<P> p;
+  Slots<G> g;
+  Slots<uint8_t> m, v;
+  __device__ __forceinline__ void fetch(const Tensor& t, int64_t i) {
+    p.fetch(static_cast<const P*>(t.p) + i);
+    g.fetch(static_cast<const G*>(t.g) + i);
+    m.fetch(static_cast<const uint8_t*>(t.m) + i);
+    v.fetch(static_cast<const uint8_t*>(t.v) + i);
+  }
+  __device__ __forceinline__ void take(Input<P, G, true>& in) const {
+    p.take(in.p);
+    g.take(in.g);
+    m.take(in.m);
+    v.take(in.v);
+  }
+};
 
 template <typename P, typename G, bool EIGHT, int CAP>
 __global__ void __launch_bounds__(kThreads)
 adamw_kernel(const __grid_constant__ Batch<CAP> b) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  Stage<P, G>* stages = reinterpret_cast<Stage<P, G>*>(smem_raw);   // kDepth of them, 8-bit states only
   pdl_wait();
   int lo = 0, hi = b.count;
   const int chunk = static_cast<int>(blockIdx.x);
@@ -182,71 +311,157 @@ adamw_kernel(const __grid_constant__ Batch<CAP> b) {
     const int mid = (lo + hi) >> 1;
     if (b.chunk0[mid] <= chunk) lo = mid; else hi = mid;
   }
-  const Tensor& t = b.t[lo];
-  const Hyper& h = b.h;
-  const int64_t base = static_cast<int64_t>(chunk - b.chunk0[lo]) * kChunk;
+  const Tensor t = b.t[lo];
+  const Hyper h = b.h;
   const int64_t n = t.n;
+  constexpr int64_t kPart = chunk_elements(EIGHT);
+  const int64_t base = static_cast<int64_t>(chunk - b.chunk0[lo]) * kPart;
+  const int64_t end = base + kPart < n ? base + kPart : n;
   P* p = static_cast<P*>(t.p);
-  const G* g = static_cast<const G*>(t.g);
-  const bool wide = ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(g) |
+  const bool wide = ((reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(t.g) |
                       reinterpret_cast<uintptr_t>(t.copy)) & 15) == 0;
+  const Product mul = {twice(h.minus_zero)};
+  const int lane8 = 8 * (threadIdx.x & 31);
+  constexpr int64_t kStep = 8 * kThreads;
+  // a read of less than eight elements, or of unaligned ones, waits for its turn
+  auto ask = [&](int64_t i, int stage) {
+    if (wide && i + 8 <= end) stages[stage].fetch(t, i);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int64_t i = base + 8 * threadIdx.x;
+  int stage = 0;
+  if constexpr (EIGHT) {
+#pragma unroll
+    for (int j = 0; j < kDepth; ++j) ask(i + j * kStep, j);
+  }
+  // The chunk's scales are read at once and written at once: a word a block,
+  // read and written by its warp, cost a third of the kernel's time.
+  constexpr int kBlocks = static_cast<int>(kPart) / kBlock;
+  __shared__ float s_scale[2][EIGHT ? kBlocks : 1];
+  const int my_blk = threadIdx.x % kBlocks;
+  const int my_side = threadIdx.x / kBlocks;   // 0: the first moment's, 1: the second's
+  const bool my_scale = EIGHT && my_side < 2 && base + static_cast<int64_t>(my_blk) * kBlock < end;
+  float* const scales = (my_side == 0 ? t.ms : t.vs) + base / kBlock + my_blk;
+  if constexpr (EIGHT) {
+    if (my_scale) s_scale[my_side][my_blk] = *scales;
+    __syncthreads();
+  }
   const float gs = h.scale ? __ldg(h.scale) : 1.0f;
+  // a warp's 256 elements are one block of the states
 #pragma unroll 1
-  for (int64_t i = base + 8 * threadIdx.x; i < base + kChunk; i += 8 * kThreads) {
-    // a warp's 256 elements are one block of the states
-    if (i - 8 * (threadIdx.x & 31) >= n) break;
+  for (; i - lane8 < end; i += kStep) {
     const bool full = i + 8 <= n;
     const bool vec = full && wide;
-    float x[8], d[8], m[8], v[8], r[8];
-    load8(p, i, n, vec, x);
-    load8(g, i, n, vec, d);
+    Input<P, G, EIGHT> in;
+    const int blk = static_cast<int>((i - base) / kBlock);
+    float old_sm = 0.0f, old_sv = 0.0f;
     if constexpr (EIGHT) {
-      const int64_t blk = i / kBlock;
-      const float sm = t.ms[blk], sv = t.vs[blk];
-      load_codes(static_cast<uint8_t*>(t.m), i, n, full, m);
-      load_codes(static_cast<uint8_t*>(t.v), i, n, full, v);
+      asm volatile("cp.async.wait_group %0;" :: "n"(kDepth - 1) : "memory");
+      old_sm = s_scale[0][blk];
+      old_sv = s_scale[1][blk];
+      if (vec) stages[stage].take(in);
+      else in.load(t, i, full, wide);
+    } else {
+      in.load(t, i, full, wide);
+    }
+    float x[8], d[8], m[8], v[8];
+    in.p.get(x);
+    in.g.get(d);
+    in.m.get(m);
+    in.v.get(v);
+    uint64_t m2[4], v2[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        m[j] = __fmul_rn(m[j], sm);
-        v[j] = __fmul_rn(v[j], sv);
-        v[j] = __fmul_rn(v[j], v[j]);
+    for (int j = 0; j < 4; ++j) {
+      m2[j] = pair(m[2 * j], m[2 * j + 1]);
+      v2[j] = pair(v[2 * j], v[2 * j + 1]);
+      if constexpr (EIGHT) {
+        m2[j] = mul(m2[j], twice(old_sm));
+        v2[j] = mul(v2[j], twice(old_sv));
+        v2[j] = mul(v2[j], v2[j]);
+      }
+    }
+    // the moments, and their range over this thread's elements
+    float m_max = 0.0f, v_max = 0.0f, v_min = kFltMax;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t gj = mul(pair(d[2 * j], d[2 * j + 1]), twice(gs));
+      m2[j] = add2(mul(m2[j], twice(h.b1)), mul(gj, twice(h.c1)));
+      v2[j] = add2(mul(v2[j], twice(h.b2)), mul(mul(gj, gj), twice(h.c2)));
+      unpair(m2[j], m[2 * j], m[2 * j + 1]);
+      unpair(v2[j], v[2 * j], v[2 * j + 1]);
+      m_max = max_abs_nan(m_max, max_abs_nan(m[2 * j], m[2 * j + 1]));
+      v_max = max_abs_nan(v_max, max_abs_nan(v[2 * j], v[2 * j + 1]));
+      v_min = fminf(v_min, fminf(v[2 * j], v[2 * j + 1]));
+    }
+    m_max = fabsf(m_max);
+    v_max = fabsf(v_max);
+    float sm = 0.0f, sv = 0.0f, im = 0.0f, iv = 0.0f;   // the block's new scales and their inverses
+    if constexpr (EIGHT) {
+      sm = block_scale_of(warp_max_nan(m_max));
+      sv = block_scale_of(__fsqrt_rn(warp_max_nan(v_max)));   // the root is monotone
+      im = __fdiv_rn(1.0f, sm);
+      iv = __fdiv_rn(1.0f, sv);
+    }
+    constexpr float kSmallest = 0.001953125f;   // 2^-9, the smallest E4M3 value above zero
+    float r[8];
+    if (v_min >= 7.888609e-31f && v_max <= 1.2676506e30f && m_max <= 1.1529215e18f) {
+      // 2^-100 <= v <= 2^100, |m| <= 2^60: two elements at a time
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t rj = sqrt2_rn(v2[j]);
+        const uint64_t u = div2_rn(m2[j], add2(mul(rj, twice(h.isq)), twice(h.eps)));
+        const uint64_t xj = add2(mul(pair(x[2 * j], x[2 * j + 1]), twice(h.keep)), mul(u, twice(-h.rate)));
+        unpair(xj, x[2 * j], x[2 * j + 1]);
+        if constexpr (EIGHT) {
+          unpair(mul(m2[j], twice(im)), m[2 * j], m[2 * j + 1]);
+          unpair(mul(rj, twice(iv)), r[2 * j], r[2 * j + 1]);
+          r[2 * j] = fmaxf(r[2 * j], kSmallest);
+          r[2 * j + 1] = fmaxf(r[2 * j + 1], kSmallest);
+        }
       }
     } else {
-      load8(static_cast<float*>(t.m), i, n, full, m);
-      load8(static_cast<float*>(t.v), i, n, full, v);
-    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) update(x[j], __fmul_rn(d[j], gs), m[j], v[j], r[j], h);
+      for (int j = 0; j < 8; ++j) {
+        r[j] = __fsqrt_rn(v[j]);
+        const float u = __fdiv_rn(m[j], __fadd_rn(__fmul_rn(r[j], h.isq), h.eps));
+        x[j] = __fsub_rn(__fmul_rn(x[j], h.keep), __fmul_rn(u, h.rate));
+        if constexpr (EIGHT) {
+          m[j] = __fmul_rn(m[j], im);
+          const float q = __fmul_rn(r[j], iv);
+          r[j] = r[j] > 0.0f && q < kSmallest ? kSmallest : q;
+        }
+      }
+    }
+    if constexpr (EIGHT) {
+      // everything that the slot held has been worked on
+      ask(i + kDepth * kStep, stage);
+      stage = stage + 1 == kDepth ? 0 : stage + 1;
+    }
     store8(p, i, n, vec, x);
     if (t.copy) store8(t.copy, i, n, vec, x);
     if constexpr (EIGHT) {
-      const int64_t blk = i / kBlock;
-      const float sm = warp_block_scale(abs_max_nan(m));
-      const float sv = warp_block_scale(abs_max_nan(r));
-      const float im = __fdiv_rn(1.0f, sm), iv = __fdiv_rn(1.0f, sv);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        m[j] = __fmul_rn(m[j], im);
-        const float q = __fmul_rn(r[j], iv);
-        r[j] = r[j] > 0.0f && q < 0.001953125f ? 0.001953125f : q;
-      }
       store_codes(static_cast<uint8_t*>(t.m), i, n, full, m);
       store_codes(static_cast<uint8_t*>(t.v), i, n, full, r);
-      __syncwarp();
+      __syncwarp();   // every lane has read the old scales
       if ((threadIdx.x & 31) == 0) {
-        t.ms[blk] = sm;
-        t.vs[blk] = sv;
+        s_scale[0][blk] = sm;
+        s_scale[1][blk] = sv;
       }
     } else {
       store8(static_cast<float*>(t.m), i, n, full, m);
       store8(static_cast<float*>(t.v), i, n, full, v);
     }
   }
+  if constexpr (EIGHT) {
+    __syncthreads();
+    if (my_scale) *scales = s_scale[my_side][my_blk];
+  }
 }
 
 template <typename P, typename G, bool EIGHT, int CAP>
 cudaError_t launch_batch(const minite_adamw_tensor* t, int64_t count, const Hyper& h,
                          cudaStream_t s) {
+  constexpr int64_t kChunk = chunk_elements(EIGHT);
   Batch<CAP> b;
   b.h = h;
   b.count = 0;
@@ -266,14 +481,25 @@ cudaError_t launch_batch(const minite_adamw_tensor* t, int64_t count, const Hype
     chunks += (t[i].n + kChunk - 1) / kChunk;
   }
   if (chunks == 0) return cudaSuccess;
+  constexpr size_t kSmem = EIGHT ? kDepth * sizeof(Stage<P, G>) : 0;
+  if constexpr (kSmem + 1024 > 48 * 1024) {   // with the static part
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [] {
+      attr_err = cudaFuncSetAttribute(adamw_kernel<P, G, EIGHT, CAP>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+  }
   return launch_pdl(adamw_kernel<P, G, EIGHT, CAP>, dim3(static_cast<unsigned>(chunks)),
-                    dim3(kThreads), 0, s, b);
+                    dim3(kThreads), kSmem, s, b);
 }
 
 template <typename P, typename G, bool EIGHT>
 int step(const minite_adamw_tensor* t, int64_t n, const Hyper& h, cudaStream_t s) {
   // kernel parameters carry the tensors' pointers (4 KB or 32 KB of them)
   constexpr int kSmall = 48, kLarge = 440;
+  constexpr int64_t kChunk = chunk_elements(EIGHT);
   static_assert(sizeof(Batch<kSmall>) <= 4096 && sizeof(Batch<kLarge>) <= 32764, "parameters");
   int64_t i = 0;
   while (i < n) {
@@ -290,6 +516,37 @@ int step(const minite_adamw_tensor* t, int64_t n, const Hyper& h, cudaStream_t s
     i += c;
   }
   return MINITE_OK;
+}
+
+// Roots of every significand at the even and the odd exponents of `scale`, and
+// quotients of 2^30 hashed pairs, that differ from the IEEE ones.
+__global__ void math_test_kernel(unsigned long long* mismatches) {
+  unsigned long long roots = 0, quotients = 0;
+  const uint32_t stride = gridDim.x * blockDim.x, first = blockIdx.x * blockDim.x + threadIdx.x;
+  for (uint32_t i = first; i < (1u << 24); i += stride) {
+    const float v = __uint_as_float(0x3F800000u + i);   // [1, 4)
+    float a, b;
+    unpair(sqrt2_rn(pair(v, v * 0x1p-98f)), a, b);
+    roots += (a != __fsqrt_rn(v)) + (b != __fsqrt_rn(v * 0x1p-98f));
+    unpair(sqrt2_rn(pair(v * 0x1p96f, v * 0x1p-40f)), a, b);
+    roots += (a != __fsqrt_rn(v * 0x1p96f)) + (b != __fsqrt_rn(v * 0x1p-40f));
+  }
+  for (uint32_t i = first; i < (1u << 30); i += stride) {
+    // SplitMix64 finaliser (Steele, Lea and Flood, 2014)
+    unsigned long long z = i + 0x9E3779B97F4A7C15ull;
+    z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+    z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+    z ^= z >> 31;
+    // m in +-[2^-60, 2^60), d in [2^-27, 2^51)
+    const uint32_t me = 67 + static_cast<uint32_t>((z >> 23) % 120), de = 100 + static_cast<uint32_t>((z >> 55) % 78);
+    const float m = __uint_as_float(static_cast<uint32_t>(z & 0x807FFFFFu) | (me << 23));
+    const float d = __uint_as_float(static_cast<uint32_t>((z >> 32) & 0x7FFFFFu) | (de << 23));
+    float a, b;
+    unpair(div2_rn(pair(m, -m), pair(d, d)), a, b);
+    quotients += (a != __fdiv_rn(m, d)) + (b != __fdiv_rn(-m, d));
+  }
+  if (roots) atomicAdd(mismatches, roots);
+  if (quotients) atomicAdd(mismatches + 1, quotients);
 }
 
 }  // namespace adamw
@@ -337,6 +594,7 @@ extern "C" int minite_adamw_step(const minite_adamw_tensor* tensors, int64_t n_t
   h.rate = static_cast<float>(lr / bc1);
   h.isq = static_cast<float>(1.0 / std::sqrt(bc2));
   h.eps = static_cast<float>(eps);
+  h.minus_zero = -0.0f;
   h.scale = grad_scale;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool pf = param_dtype == MINITE_OUT_FP32, gf = grad_dtype == MINITE_OUT_FP32;
@@ -350,4 +608,10 @@ extern "C" int minite_adamw_step(const minite_adamw_tensor* tensors, int64_t n_t
   if (pf) return adamw::step<float, uint16_t, false>(tensors, n_tensors, h, s);
   if (gf) return adamw::step<uint16_t, float, false>(tensors, n_tensors, h, s);
   return adamw::step<uint16_t, uint16_t, false>(tensors, n_tensors, h, s);
+}
+
+extern "C" int minite_test_adamw_math(unsigned long long* mismatches, minite_stream_t stream) {
+  if (!mismatches) return MINITE_ERR_INVALID_ARG;
+  adamw::math_test_kernel<<<4 * num_sms(), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(mismatches);
+  return cudaGetLastError() == cudaSuccess ? MINITE_OK : MINITE_ERR_CUDA;
 }

@@ -36,7 +36,7 @@ EXPORTS = [
     "minite_swiglu_weighted_quant_keep_h", "minite_grouped_gemm_wgrad_nvfp4",
     "minite_swiglu_backward_quant_keep", "minite_gate_up_swiglu_quant_nvfp4",
     "minite_grouped_gemm_bf16", "minite_grouped_wgrad_bf16", "minite_token_logprobs",
-    "minite_token_logprobs_backward", "minite_adamw_step",
+    "minite_token_logprobs_backward", "minite_adamw_step", "minite_test_adamw_math",
 ]
 
 
@@ -96,6 +96,7 @@ def load(path: str | None = None):
                              [_i64, _vp, _vp],
         "minite_test_convert": [_vp, _i64, _vp, _vp, _vp, _vp],
         "minite_test_div6_exhaustive": [_vp, _vp],
+        "minite_test_adamw_math": [_vp, _vp],
         "minite_test_convert_digest": [ctypes.c_ulonglong, ctypes.c_ulonglong, _vp, _vp],
     }
     for name, args in sig.items():
@@ -528,6 +529,11 @@ def minite_test_convert_digest(first_chunk, n_chunks, digests, stream=None):
 def minite_test_div6_exhaustive(counter, stream=None):
     rc = load().minite_test_div6_exhaustive(_p(counter), _s(stream))
     _check(rc, "minite_test_div6_exhaustive")
+
+
+def minite_test_adamw_math(counters, stream=None):
+    """counters: int64 [2], zeroed by the caller."""
+    _check(load().minite_test_adamw_math(_p(counters), _s(stream)), "minite_test_adamw_math")
 
 
 # ---------------------------------------------------------------- allocation helpers

@@ -187,6 +187,28 @@ def test_another_stream_and_lr_override():
     assert torch.equal(p[0], q[0])
 
 
+def test_roots_and_quotients_are_the_ieee_ones():
+    c = torch.zeros(2, dtype=torch.int64, device=DEV)
+    M.minite_test_adamw_math(c)
+    assert c.tolist() == [0, 0]
+
+
+def test_moments_outside_the_usual_range():
+    """Second moments from 2^-140 to 2^120 and zero, in one block: the same
+    operations as anywhere else (the usual range takes another path)."""
+    n = 512
+    g = torch.ldexp(torch.ones(n), torch.randint(-70, 60, (n,), generator=torch.Generator().manual_seed(3)).float())
+    g[::7] = 0.0
+    g = g.to(DEV)
+    p = torch.zeros(n, device=DEV)
+    opt = M.AdamW([p], state_bits=32, lr=1e-3, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.0)
+    opt.step([g])
+    m, v = g * (1 - 0.9), (g * g) * (1 - 0.95)
+    want = -(m / (v.sqrt() * (1 / math.sqrt(1 - 0.95)) + 1e-8)) * (1e-3 / (1 - 0.9))
+    assert torch.equal(opt.exp_avg[:n], m) and torch.equal(opt.exp_avg_sq[:n], v)
+    assert torch.equal(p, want)
+
+
 def test_refusals():
     p = [torch.zeros(8, device=DEV)]
     opt = M.AdamW(p)
