@@ -575,7 +575,7 @@ def _need(cond, what):
 def _empty(shape, dtype, like, stream):
     """A new tensor that belongs to the stream that the kernel runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
@@ -609,16 +609,27 @@ def token_logprobs(logits, targets=None, temperature=1.0, alternatives=0, status
     temperature), with the row's entropy and its ``alternatives`` most likely
     tokens. Returns dict(logprob (None without targets), entropy, stats,
     alt_ids, alt_logprobs); a negative target marks a row that is skipped."""
-    N, f32 = logits.shape[0], torch.float32
-    r = dict(logprob=None if targets is None else _empty((N,), f32, logits, stream),
-             entropy=_empty((N,), f32, logits, stream), stats=_empty((N, 2), f32, logits, stream),
-             alt_ids=None, alt_logprobs=None)
+    name = "token_logprobs"
+    ld = _rows(logits, name)
+    N, V = logits.shape
+    f32 = torch.float32
+    entropy, stats = _empty((N,), f32, logits, stream), _empty((N, 2), f32, logits, stream)
+    logprob = alt_ids = alt_logprobs = None
+    if targets is not None:
+        logprob = _empty((N,), f32, logits, stream)
     if alternatives:
-        r["alt_ids"] = _empty((N, alternatives), torch.int32, logits, stream)
-        r["alt_logprobs"] = _empty((N, alternatives), f32, logits, stream)
-    minite_token_logprobs(logits, targets, r["logprob"], r["entropy"], r["stats"], temperature,
-                          r["alt_ids"], r["alt_logprobs"], status, stream)
-    return r
+        alt_ids = _empty((N, alternatives), torch.int32, logits, stream)
+        alt_logprobs = _empty((N, alternatives), f32, logits, stream)
+    rc = load().minite_token_logprobs(
+        _ptr(logits), _dtype(logits, name), N, V, ld, _ptr(targets), _targets(targets, N, name),
+        temperature, None if logprob is None else logprob.data_ptr(),
+        entropy.data_ptr(), stats.data_ptr(), alternatives,
+        alt_ids.data_ptr() if alternatives else None,
+        alt_logprobs.data_ptr() if alternatives else None, _ptr(status), _raw(stream, logits))
+    if rc:
+        _check(rc, "minite_token_logprobs")
+    return {"logprob": logprob, "entropy": entropy, "stats": stats, "alt_ids": alt_ids,
+            "alt_logprobs": alt_logprobs}
 
 
 def token_logprobs_backward(logits, targets, forward, grad_logprob=None, grad_entropy=None,
@@ -674,6 +685,7 @@ class AdamW:
                   f"AdamW: state {name} is not {dtype} [{n}]")
             setattr(self, name, t)
         d = self._tensors = np.zeros(len(params), dtype=ADAMW_TENSOR)
+        self._address, self._grads = d.ctypes.data, d["grad"]
         d["param"] = [p.data_ptr() for p in params]
         d["n"] = sizes
         if copies is not None:
@@ -691,12 +703,15 @@ class AdamW:
                 not all([g.is_contiguous() and g.is_cuda for g in grads]):
             raise MiniteError("AdamW.step: gradients are contiguous CUDA tensors of one type, one a "
                               "parameter and of its size")
-        _need(grad_scale is None or (grad_scale.dtype == torch.float32 and grad_scale.numel() == 1),
-              "AdamW.step: grad_scale is one float32")
-        self._tensors["grad"] = [g.data_ptr() for g in grads]
-        minite_adamw_step(self._tensors, self._param_dtype, _dtype(grads[0], "AdamW.step"),
-                          self.state_bits, self.lr if lr is None else lr, *self.betas, self.eps,
-                          self.weight_decay, self.step_count + 1, grad_scale, stream)
+        if grad_scale is not None and (grad_scale.dtype is not torch.float32 or grad_scale.numel() != 1):
+            raise MiniteError("AdamW.step: grad_scale is one float32")
+        self._grads[:] = [g.data_ptr() for g in grads]
+        rc = load().minite_adamw_step(
+            self._address, len(self.params), self._param_dtype, _dtype(grads[0], "AdamW.step"),
+            self.state_bits, self.lr if lr is None else lr, *self.betas, self.eps, self.weight_decay,
+            self.step_count + 1, _ptr(grad_scale), _raw(stream, self.exp_avg))
+        if rc:
+            _check(rc, "minite_adamw_step")
         self.step_count += 1
 
 
