@@ -575,7 +575,7 @@ def _need(cond, what):
 def _empty(shape, dtype, like, stream):
     """A new tensor that belongs to the stream that the kernel runs on."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 
