@@ -73,8 +73,8 @@ constexpr int BOX_BYTES = 64 * 128;               // MN-major box: 64 values x 6
 constexpr int kTokenBoxes = 4;                    // K-major boxes of 16, 32, 64 and 128 tokens
 constexpr int NUM_EPI_WARPS = 16;                 // four per TMEM lane quarter, 64 columns each
 constexpr int EPI_WARP0 = 2;
-constexpr int B_WARP = EPI_WARP0 + NUM_EPI_WARPS;   // the rows' producer
-constexpr int NUM_THREADS = (B_WARP + 1) * 32;
+constexpr int ODD_WARP = EPI_WARP0 + NUM_EPI_WARPS;   // the second producer
+constexpr int NUM_THREADS = (ODD_WARP + 1) * 32;
 constexpr int EPI_COLS = MAX_N / (NUM_EPI_WARPS / 4);
 constexpr int OUT_ROWS = 16;                      // FP32 weight gradients: rows of a staged box
 constexpr int OUT_BOX_BYTES = OUT_ROWS * 512;      // 128 features
@@ -140,6 +140,7 @@ struct Work {
   const int32_t* off;      // [E+1]
   const int32_t* large;    // [E+1] units of the larger experts before e
   const int32_t* small;    // [E+1] units of the experts of at most max_n rows before e
+  const int32_t* size;     // [E] rows of a larger expert's tiles
   int f_tiles;
 };
 
@@ -173,18 +174,25 @@ __device__ __forceinline__ Tile decode(int t, int pair, const Work& w, const Par
     r.len = w.off[r.e + 1] - w.off[r.e];
   } else {
     // the larger experts' units spread evenly over the list
-    const int64_t L = w.large[p.E], all = L + w.small[p.E];
-    const int before = static_cast<int>(div_nonneg(t * L, all));
-    r.by_rows = div_nonneg((t + 1) * L, all) > before;
+    const uint64_t L = static_cast<uint32_t>(w.large[p.E]), all = L + static_cast<uint32_t>(w.small[p.E]);
+    const uint64_t tl = static_cast<uint32_t>(t) * L;
+    int before;
+    uint32_t rest;   // of t L / all: the next one is large if the quotient grows
+    if ((tl >> 32) == 0) {
+      before = static_cast<int>(static_cast<uint32_t>(tl) / static_cast<uint32_t>(all));
+      rest = static_cast<uint32_t>(tl) - static_cast<uint32_t>(before) * static_cast<uint32_t>(all);
+    } else {
+      before = static_cast<int>(tl / all);
+      rest = static_cast<uint32_t>(tl - before * all);
+    }
+    r.by_rows = rest + L >= all;
     int at = 0, size = p.max_n;
     if (r.by_rows) {
       r.e = expert_of(w.large, p.E, before);
-      const int u = before - w.large[r.e];
-      const int twos = (w.large[r.e + 1] - w.large[r.e]) / w.f_tiles;   // pairs of row tiles
-      const int cnt = w.off[r.e + 1] - w.off[r.e];
-      size = ((cnt + 2 * twos - 1) / (2 * twos) + 31) & ~31;            // about equal tiles
-      r.f0 = (u % w.f_tiles) * BF;
-      at = (2 * (u / w.f_tiles) + pair) * size;
+      const uint32_t u = before - w.large[r.e], f_tiles = w.f_tiles, two = u / f_tiles;
+      size = w.size[r.e];
+      r.f0 = static_cast<int>(u - two * f_tiles) * BF;
+      at = (2 * static_cast<int>(two) + pair) * size;
     } else {
       const int u = t - before;
       r.e = expert_of(w.small, p.E, u);
@@ -340,6 +348,7 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
   int32_t* s_off = reinterpret_cast<int32_t*>(&S + 1);   // [E+1] each
   int32_t* s_large = s_off + (p.E + 1);
   int32_t* s_small = s_large + (p.E + 1);
+  int32_t* s_size = s_small + (p.E + 1);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank4 = cluster_ctarank();
@@ -348,7 +357,7 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
   const int pair = static_cast<int>(rank4 >> 1);         // within the cluster
   const int cid = static_cast<int>(cluster_id_x());
   const int ncl = static_cast<int>(num_clusters_x());
-  const Work work = {s_off, s_large, s_small, (p.F + BF - 1) / BF};
+  const Work work = {s_off, s_large, s_small, s_size, (p.F + BF - 1) / BF};
   const uint16_t pair_mask = static_cast<uint16_t>(0x3u << leader);
 
   if (warp == 0 && lane == 0) {
@@ -386,8 +395,12 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
         if (e == 0) s_off[0] = o0;
         if (o1 < o0 || (e == 0 && o0 != 0) || (e == p.E - 1 && o1 > p.M)) bad = true;
         const int cnt = o1 - o0;
-        if (cnt > p.max_n) large = (cnt + 2 * p.max_n - 1) / (2 * p.max_n) * work.f_tiles;
-        else if (cnt > 0) small = (work.f_tiles + 1) >> 1;
+        if (cnt > p.max_n) {
+          // pairs of about equal row tiles
+          const int twos = (cnt + 2 * p.max_n - 1) / (2 * p.max_n);
+          large = twos * work.f_tiles;
+          s_size[e] = ((cnt + 2 * twos - 1) / (2 * twos) + 31) & ~31;
+        } else if (cnt > 0) small = (work.f_tiles + 1) >> 1;
       }
       int il = large, is = small;
 #pragma unroll
@@ -437,16 +450,17 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
     __syncwarp();
   };
 
-  if (warp == 0 || warp == B_WARP) {
-    // ------------------------------------------------------------ producers: features, rows
-    const bool is_a = warp == 0;
+  if (warp == 0 || warp == ODD_WARP) {
+    // ------------------------------------------------------------ producers of every other K block
+    const int which = warp == 0 ? 0 : 1;
     // The whole warp runs the loop and one elected lane issues, so that a
-    // copy's operands are warp-uniform. Each copy costs its warp about 180 cycles,
-    // so the two operands have a warp each and a stage is one or two copies of it.
+    // copy's operands are warp-uniform. Even so each copy costs its warp about
+    // 180 cycles and a block as much again for its barriers, 520 in all where
+    // the tensor cores take 512; so two warps take the blocks in turn.
     const uint16_t both = rank == 0 ? 0x5 : 0xA;   // the CTAs of this rank of both pairs
     const uint32_t leader_full0 = mapa_shared(smem_u32(&S.full[0]), leader);
     uint32_t armed_mask = 0, armed_parity = 0;
-    int stage = 0;
+    int stage = 0, turn = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int t = cid; t < total && ok; t += ncl) {
@@ -477,7 +491,15 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
       const int f_box = tl.by_rows ? f0 + 64 * pair : f0;
       const bool a_two = !tl.by_rows && p.a_two;
       const bool b_two = B_MN && tl.by_rows && box2 >= 0 && p.b_two && b0 % 64 == 0;
-      for (int kt = 0; kt < kt_n; ++kt) {
+      for (int kt = 0; kt < kt_n; ++kt, turn ^= 1) {
+        if (turn != which) {   // the other warp's
+          armed_mask |= 1u << stage;
+          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+          continue;
+        }
+        // the block before this warp's last one has been consumed by then, so
+        // that the barrier cannot be a whole turn of the ring behind
         if (!__all_sync(0xffffffffu, mbar_wait(&S.empty[stage], phase ^ 1u, budget, abort_flag))) {
           ok = false;
           break;
@@ -490,7 +512,7 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
         const int k0 = MODE == WGRAD ? tl.row0 + kt * BK : kt * BK;
         uint8_t* dst = sA + (tl.by_rows ? pair * BOX_BYTES : 0);
         const CUtensorMap* am = a_two ? &maps.a2 : &maps.a1;
-        if (is_a && elect_one()) {
+        if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&S.full[stage], tail ? bytes : 2 * bytes);
           else if (tail) mbar_arrive_expect_tx(&S.tail_full[stage], bytes);
           if constexpr (MODE == FORWARD) {
@@ -507,8 +529,6 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
               tma_load_pair<3>(sA + BOX_BYTES, am, bar, false, both, f_box + 64, k0, tl.e);
             else tma_load_pair<2>(sA + BOX_BYTES, am, bar, false, both, f_box + 64, k0);
           }
-        }
-        if (!is_a && elect_one()) {
           const uint32_t at2 = main_rows * 128;
           if constexpr (B_MN) {
             if (b_two) {
@@ -531,8 +551,8 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
     }
     if (!ok && lane == 0) fail();
     volatile int no_abort = 0;
-    if (is_a && rank == 0) {
-      // every armed stage's copies must have landed before exit
+    if (rank == 0 && which == 0) {
+      // every stage's last copies must have landed before exit
       for (int s = 0; s < p.stages; ++s)
         if (armed_mask & (1u << s))
           mbar_wait(&S.full[s], (armed_parity >> s) & 1u, kDrainBudget, &no_abort);
@@ -793,7 +813,7 @@ int launch_as(const Maps& maps, Params& p, cudaStream_t s) {
   if (attr_err != cudaSuccess) return MINITE_ERR_CUDA;
   p.chunk = F32 ? kChunkBlocks : 1 << 30;
   p.budget_ns = wait_budget_ns();
-  const size_t rest = 1024 + (MODE == WGRAD && F32 ? OUT_BYTES : 0) + sizeof(Smem) + 3 * (static_cast<size_t>(p.E) + 1) * sizeof(int32_t);
+  const size_t rest = 1024 + (MODE == WGRAD && F32 ? OUT_BYTES : 0) + sizeof(Smem) + 4 * (static_cast<size_t>(p.E) + 1) * sizeof(int32_t);
   p.stages = static_cast<int>((kMaxSmem - rest) / STAGE_BYTES);
   if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
   const size_t smem = rest + static_cast<size_t>(p.stages) * STAGE_BYTES;
