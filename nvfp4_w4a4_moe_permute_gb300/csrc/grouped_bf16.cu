@@ -98,6 +98,15 @@ struct Smem {
   int pad_;
 };
 
+// The first units of a cluster's list as every role of its CTAs needs them,
+// looked up by all threads at once: a look-up takes a warp about 1000 cycles,
+// and the ring would wait for it at every unit's start.
+constexpr int kListed = 64;
+struct ListedTile {
+  int row0;
+  uint16_t rows, f, e, by_rows;
+};
+
 struct Params {
   const int32_t* offsets;
   void* out;
@@ -140,7 +149,8 @@ struct Work {
   const int32_t* off;      // [E+1]
   const int32_t* large;    // [E+1] units of the larger experts before e
   const int32_t* small;    // [E+1] units of the experts of at most max_n rows before e
-  const int32_t* size;     // [E] rows of a larger expert's tiles
+  const uint16_t* size;    // [E] rows of a larger expert's tiles
+  const ListedTile* list;  // [kListed]
   int f_tiles;
 };
 
@@ -215,6 +225,24 @@ template <int MODE>
 constexpr uint32_t idesc_base() {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((MODE != FORWARD ? 1u : 0u) << 15) |
          ((MODE == WGRAD ? 1u : 0u) << 16) | (static_cast<uint32_t>(BF >> 4) << 24);
+}
+
+// Unit t, the i-th of this cluster.
+template <int MODE>
+__device__ __forceinline__ Tile unit(int t, int i, int pair, const Work& w, const Params& p) {
+  if (MODE == WGRAD || i >= kListed) return decode<MODE>(t, pair, w, p);
+  const ListedTile l = w.list[i];
+  Tile r;
+  r.e = l.e;
+  r.f0 = l.f * BF;
+  r.by_rows = l.by_rows != 0;
+  r.row0 = l.row0;
+  r.i0 = 0;
+  r.orow0 = l.row0;
+  r.rows = l.rows;
+  r.n = max(32, (r.rows + 31) & ~31);
+  r.len = p.K;
+  return r;
 }
 
 __device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -339,16 +367,18 @@ template <int MODE, bool F32>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
   constexpr bool A_MN = MODE != FORWARD, B_MN = MODE == WGRAD;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* stages = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr bool TMA_OUT = MODE == WGRAD && F32;
-  uint8_t* out_stage = stages + p.stages * STAGE_BYTES;
-  Smem& S = *reinterpret_cast<Smem*>(out_stage + (TMA_OUT ? OUT_BYTES : 0));
-  int32_t* s_off = reinterpret_cast<int32_t*>(&S + 1);   // [E+1] each
+  // barriers and tables, then (1024-byte aligned) the stages and the staged output
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem& S = *reinterpret_cast<Smem*>(smem_raw);
+  int32_t* s_off = reinterpret_cast<int32_t*>(smem_raw + sizeof(Smem));   // [E+1] each
   int32_t* s_large = s_off + (p.E + 1);
   int32_t* s_small = s_large + (p.E + 1);
-  int32_t* s_size = s_small + (p.E + 1);
+  ListedTile* s_list = reinterpret_cast<ListedTile*>(s_small + (p.E + 1));
+  uint16_t* s_size = reinterpret_cast<uint16_t*>(s_list + (MODE == WGRAD ? 0 : kListed));   // [E]
+  uint8_t* stages = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(s_size + p.E) + 1023) & ~uintptr_t(1023));
+  uint8_t* out_stage = stages + p.stages * STAGE_BYTES;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank4 = cluster_ctarank();
@@ -357,7 +387,7 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
   const int pair = static_cast<int>(rank4 >> 1);         // within the cluster
   const int cid = static_cast<int>(cluster_id_x());
   const int ncl = static_cast<int>(num_clusters_x());
-  const Work work = {s_off, s_large, s_small, s_size, (p.F + BF - 1) / BF};
+  const Work work = {s_off, s_large, s_small, s_size, s_list, (p.F + BF - 1) / BF};
   const uint16_t pair_mask = static_cast<uint16_t>(0x3u << leader);
 
   if (warp == 0 && lane == 0) {
@@ -399,7 +429,7 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
           // pairs of about equal row tiles
           const int twos = (cnt + 2 * p.max_n - 1) / (2 * p.max_n);
           large = twos * work.f_tiles;
-          s_size[e] = ((cnt + 2 * twos - 1) / (2 * twos) + 31) & ~31;
+          s_size[e] = static_cast<uint16_t>(((cnt + 2 * twos - 1) / (2 * twos) + 31) & ~31);
         } else if (cnt > 0) small = (work.f_tiles + 1) >> 1;
       }
       int il = large, is = small;
@@ -418,10 +448,23 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
       n_large += __shfl_sync(0xffffffffu, il, 31);
       n_small += __shfl_sync(0xffffffffu, is, 31);
     }
+    // what the launch counted on: the stages start on a 1024-byte boundary within the allocation
+    uint32_t have;
+    asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(have));
+    if (out_stage + (TMA_OUT ? OUT_BYTES : 0) > smem_raw + have) bad = true;
     bad = __any_sync(0xffffffffu, bad);
     if (lane == 0) {
       S.total_tiles = bad ? 0 : MODE == WGRAD ? p.units : n_large + n_small;
       if (bad && blockIdx.x == 0) set_status(p.status, MINITE_ERR_INVALID_ARG);
+    }
+  }
+  if (MODE != WGRAD) {
+    __syncthreads();
+    const int t = cid + static_cast<int>(threadIdx.x) * ncl;
+    if (threadIdx.x < kListed && t < S.total_tiles) {
+      const Tile tl = decode<MODE>(t, pair, work, p);
+      s_list[threadIdx.x] = {tl.row0, static_cast<uint16_t>(tl.rows), static_cast<uint16_t>(tl.f0 / BF),
+                             static_cast<uint16_t>(tl.e), static_cast<uint16_t>(tl.by_rows)};
     }
   }
   // both CTAs' barriers exist and TMEM is allocated before any cross-CTA traffic
@@ -463,8 +506,8 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
     int stage = 0, turn = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int t = cid; t < total && ok; t += ncl) {
-      const Tile tl = decode<MODE>(t, pair, work, p);
+    for (int t = cid, i = 0; t < total && ok; t += ncl, ++i) {
+      const Tile tl = unit<MODE>(t, i, pair, work, p);
       const int kt_n = (tl.len + BK - 1) / BK;
       const int half = tl.n / 2;
       const int f0 = tl.f0 + 128 * static_cast<int>(rank);
@@ -571,8 +614,8 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
     int stage = 0, buf = 0;
     uint32_t phase = 0, acc_phase = 0, tail_parity = 0;
     bool ok = true, issued = false;
-    for (int t = cid; t < total && ok; t += ncl) {
-      const Tile tl = decode<MODE>(t, pair, work, p);
+    for (int t = cid, i = 0; t < total && ok; t += ncl, ++i) {
+      const Tile tl = unit<MODE>(t, i, pair, work, p);
       const uint32_t idesc = idesc_base<MODE>() | (static_cast<uint32_t>(tl.n >> 3) << 17);
       int in_chunk = 0;
       for (int left = tl.len; left > 0; left -= BK) {
@@ -626,8 +669,8 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
       int stage = 0;
       uint32_t tail_parity = 0;
       bool ok = true;
-      for (int t = cid; t < total && ok; t += ncl) {
-        const Tile tl = decode<MODE>(t, pair, work, p);
+      for (int t = cid, i = 0; t < total && ok; t += ncl, ++i) {
+        const Tile tl = unit<MODE>(t, i, pair, work, p);
         const int kt_n = (tl.len + BK - 1) / BK;
         if (kt_n == 0) continue;
         stage = (stage + kt_n - 1) % p.stages;   // the sum's last stage
@@ -651,8 +694,8 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
     int buf = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    for (int t = cid; t < total && ok; t += ncl) {
-      const Tile tl = decode<MODE>(t, pair, work, p);
+    for (int t = cid, i = 0; t < total && ok; t += ncl, ++i) {
+      const Tile tl = unit<MODE>(t, i, pair, work, p);
       const int chunks = ((tl.len + BK - 1) / BK + p.chunk - 1) / p.chunk;
       if (chunks == 0 && p.accumulate) continue;
       const int rows = tl.rows - c0;
@@ -813,7 +856,11 @@ int launch_as(const Maps& maps, Params& p, cudaStream_t s) {
   if (attr_err != cudaSuccess) return MINITE_ERR_CUDA;
   p.chunk = F32 ? kChunkBlocks : 1 << 30;
   p.budget_ns = wait_budget_ns();
-  const size_t rest = 1024 + (MODE == WGRAD && F32 ? OUT_BYTES : 0) + sizeof(Smem) + 4 * (static_cast<size_t>(p.E) + 1) * sizeof(int32_t);
+  // barriers, offsets, list and sizes in front of the stages
+  const size_t head = (sizeof(Smem) + 3 * (static_cast<size_t>(p.E) + 1) * sizeof(int32_t) +
+                       (MODE == WGRAD ? 0 : kListed * sizeof(ListedTile)) + p.E * sizeof(uint16_t) + 1023) /
+                      1024 * 1024;
+  const size_t rest = head + (MODE == WGRAD && F32 ? OUT_BYTES : 0);
   p.stages = static_cast<int>((kMaxSmem - rest) / STAGE_BYTES);
   if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
   const size_t smem = rest + static_cast<size_t>(p.stages) * STAGE_BYTES;
