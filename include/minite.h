@@ -572,8 +572,8 @@ int minite_quantize_tokens_nvfp4(const void* x, int64_t x_rows, const int32_t* r
  * out:      device, [M_total, N] BF16 or FP32 (out_dtype), rows `out_stride`
  *           elements apart; rows at or beyond offsets[E] are not written.
  * Shape rules: N, K, a_stride, out_stride multiples of 8, 8 <= N, K <= 2^20,
- * 1 <= E <= 1024, M_total < 2^31 - 256 (0 is allowed: nothing is enqueued);
- * a, w and out 16-byte aligned. Waits are bounded as in
+ * N K < 2^38, 1 <= E <= 1024, M_total < 2^30 (0 is allowed: nothing is
+ * enqueued); a, w and out 16-byte aligned. Waits are bounded as in
  * minite_grouped_gemm_nvfp4.
  */
 int minite_grouped_gemm_bf16(const void* a, int64_t a_stride, const void* w, int w_layout,

@@ -885,7 +885,7 @@ int launch_as(const Maps& maps, Params& p, cudaStream_t s) {
   const int64_t most = MODE == WGRAD
                            ? units(p.max_n)
                            : (p.M / (2 * p.max_n) + (p.E < p.M ? p.E : p.M)) * f_tiles;
-  if (most > 0x7FFFFFFF) return MINITE_ERR_UNSUPPORTED_SHAPE;
+  if (most >= (int64_t(1) << 30)) return MINITE_ERR_UNSUPPORTED_SHAPE;
   p.units = static_cast<int>(most);
   if (most < clusters) clusters = static_cast<int>(most);
   if (launch_clusters_pdl(grouped_bf16_kernel<MODE, F32>, clusters, 4, NUM_THREADS, smem, s, maps, p) !=
@@ -901,6 +901,9 @@ int launch(const Maps& maps, Params& p, int out_dtype, cudaStream_t s) {
 }
 
 constexpr int64_t kMaxDim = int64_t(1) << 20;
+constexpr int64_t kMaxRows = int64_t(1) << 30;        // row indexes of padded tiles stay within 32 bits
+constexpr int64_t kMaxWeight = int64_t(1) << 38;      // elements of one expert: strides of tensor maps
+                                                      // are below 2^40 bytes
 
 }  // namespace
 }  // namespace gbf16
@@ -916,8 +919,8 @@ extern "C" int minite_grouped_gemm_bf16(const void* a, int64_t a_stride, const v
   using namespace gbf16;
   if (out_dtype != MINITE_OUT_BF16 && out_dtype != MINITE_OUT_FP32) return MINITE_ERR_INVALID_ARG;
   if (w_layout != MINITE_W_NK && w_layout != MINITE_W_KN) return MINITE_ERR_INVALID_ARG;
-  if (M_total < 0 || M_total >= (int64_t(1) << 31) - MAX_N || N < 8 || N % 8 != 0 || N > kMaxDim ||
-      K < 8 || K % 8 != 0 || K > kMaxDim || E < 1 || E > 1024 || a_stride < K || a_stride % 8 != 0 ||
+  if (M_total < 0 || M_total >= kMaxRows || N < 8 || N % 8 != 0 || N > kMaxDim ||
+      K < 8 || K % 8 != 0 || K > kMaxDim || N * K >= kMaxWeight || E < 1 || E > 1024 || a_stride < K || a_stride % 8 != 0 ||
       out_stride < N || out_stride % 8 != 0 || a_stride > (int64_t(1) << 32) ||
       out_stride > (int64_t(1) << 32))
     return MINITE_ERR_UNSUPPORTED_SHAPE;
@@ -962,8 +965,8 @@ extern "C" int minite_grouped_wgrad_bf16(const void* a, int64_t a_stride, const 
   using namespace gbf16;
   if (out_dtype != MINITE_OUT_BF16 && out_dtype != MINITE_OUT_FP32) return MINITE_ERR_INVALID_ARG;
   if (accumulate && out_dtype != MINITE_OUT_FP32) return MINITE_ERR_INVALID_ARG;
-  if (M_total < 0 || M_total >= (int64_t(1) << 31) - MAX_N || Na < 8 || Na % 8 != 0 || Na > kMaxDim ||
-      Nb < 8 || Nb % 8 != 0 || Nb > kMaxDim || E < 1 || E > 1024 || a_stride < Na ||
+  if (M_total < 0 || M_total >= kMaxRows || Na < 8 || Na % 8 != 0 || Na > kMaxDim ||
+      Nb < 8 || Nb % 8 != 0 || Nb > kMaxDim || Na * Nb >= kMaxWeight || E < 1 || E > 1024 || a_stride < Na ||
       a_stride % 8 != 0 || b_stride < Nb || b_stride % 8 != 0 || a_stride > (int64_t(1) << 32) ||
       b_stride > (int64_t(1) << 32))
     return MINITE_ERR_UNSUPPORTED_SHAPE;

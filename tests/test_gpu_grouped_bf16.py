@@ -97,6 +97,57 @@ def test_weight_gradient(counts, N, K, kind):
 
 
 @pytest.mark.parametrize("mode", ["forward", "stored", "wgrad"])
+@pytest.mark.parametrize("E,N,K,seed", [(37, 256, 64, 0), (300, 520, 136, 1), (1024, 72, 72, 2), (5, 1280, 320, 3)])
+def test_random_routings(mode, E, N, K, seed):
+    """Experts of 0 to about 900 rows: every way a cluster's pairs share a tile,
+    every number of rows in a tile, and tables too long for all stages."""
+    g = torch.Generator().manual_seed(seed)
+    counts = (900 * torch.rand(E, generator=g) ** (6 if E > 100 else 1)).long()
+    counts[::5] = 0
+    counts = counts.tolist()
+    off, m = offsets_of(counts), sum(counts)
+    x = randn(seed + 50, m, K)
+    if mode == "wgrad":
+        dy = randn(seed + 51, m, N)
+        got = M.grouped_wgrad_bf16(dy, x, off)
+    else:
+        w = randn(seed + 52, E, K, N) if mode == "stored" else randn(seed + 52, E, N, K)
+        got = M.grouped_gemm_bf16(x, w, off, w_as_stored=mode == "stored", out_dtype=torch.float32)
+    at = 0
+    for e, c in enumerate(counts):
+        r = slice(at, at + c)
+        if mode == "wgrad":
+            a, b, n, res = dy[r].double().t(), x[r].double(), max(c, 1), got[e]
+        else:
+            a, b, n, res = x[r].double(), w[e].double() if mode == "stored" else w[e].double().t(), K, got[r]
+        check(res, a @ b, a.abs() @ b.abs(), n, (torch.float32, e, c))
+        at += c
+
+
+def test_more_units_of_work_than_are_listed():
+    """160000 rows x 2048 features: over 64 units for each cluster."""
+    counts, N, K = [100000, 59993, 7], 2048, 64
+    x, w, off = randn(60, sum(counts), K), randn(61, 3, N, K), offsets_of(counts)
+    out = M.grouped_gemm_bf16(x, w, off, out_dtype=torch.float32)
+    for e, lo, hi in ((0, 0, 100000), (1, 100000, 159993), (2, 159993, 160000)):
+        for a in range(lo, hi, 20000):
+            r = slice(a, min(hi, a + 20000))
+            A, B = x[r].double(), w[e].double().t()
+            check(out[r], A @ B, A.abs() @ B.abs(), K, (torch.float32, e, a))
+
+
+def test_long_sums_of_one_sign():
+    """65536 positive products: what the tensor cores' sums lose at every step all
+    goes one way, and the chunks keep it to a chunk's worth."""
+    n = 65536
+    a, b = randn(62, n, 64).abs(), randn(63, n, 128).abs()
+    exact = a.double().t() @ b.double()
+    check(M.grouped_wgrad_bf16(a, b, offsets_of([n]))[0], exact, exact, n, (torch.float32,))
+    x, w = a.t().contiguous(), b.t().contiguous()[None]
+    check(M.grouped_gemm_bf16(x, w, offsets_of([64]), out_dtype=torch.float32), exact, exact, n, (torch.float32,))
+
+
+@pytest.mark.parametrize("mode", ["forward", "stored", "wgrad"])
 def test_an_experts_values_do_not_reach_another(mode):
     """NaN and infinities in one expert's rows and weight stay with it, also where
     a tile or a sum's tail reads past an expert's end."""

@@ -31,7 +31,8 @@ GEMM = dict(a=FAKE, a_stride=64, w=FAKE, w_layout=0, offsets=FAKE, M=16, N=64, K
     (dict(M=-1), SHAPE), (dict(M=1 << 31), SHAPE), (dict(N=0), SHAPE), (dict(N=12), SHAPE),
     (dict(K=4), SHAPE), (dict(K=20, a_stride=24), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), SHAPE),
     (dict(a_stride=56), SHAPE), (dict(a_stride=68), SHAPE), (dict(out_stride=32), SHAPE),
-    (dict(out_stride=65), SHAPE), (dict(N=1 << 21, out_stride=1 << 21), SHAPE)])
+    (dict(out_stride=65), SHAPE), (dict(N=1 << 21, out_stride=1 << 21), SHAPE), (dict(M=1 << 30), SHAPE),
+    (dict(N=1 << 20, K=1 << 20, a_stride=1 << 20, out_stride=1 << 20), SHAPE)])
 def test_grouped_gemm(lib, change, rc):
     assert lib.minite_grouped_gemm_bf16(*{**GEMM, **change}.values()) == rc
 
