@@ -388,9 +388,9 @@ __device__ __forceinline__ void block_alternatives(Shared& S, const Row<T>& r, c
 // of one CTA, and the segments are joined in order by the cluster's first CTA:
 // the results do not depend on how many CTAs shared a row.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Params p) {
   constexpr int VEC = Elem<T>::kVec;
-  constexpr int UNROLL = 4;
+  constexpr int UNROLL = 8;   // 16-byte loads in flight per thread
   __shared__ Shared S;
   pdl_wait();
   const int tid = threadIdx.x;
@@ -472,7 +472,16 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const Params p) {
 #pragma unroll
         for (int j = 0; j < UNROLL; ++j) add(u[j]);
       }
-      for (; i < v1; i += kThreads) add(r.vec(i));
+#pragma unroll 1
+      for (; i < v1; i += 4 * kThreads) {   // what is left, four in flight
+        uint4 u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i + j * kThreads < v1) u[j] = r.vec(i + j * kThreads);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i + j * kThreads < v1) add(u[j]);
+      }
       float a, b;
       unpair(s2, a, b);
       st.s = a + b;

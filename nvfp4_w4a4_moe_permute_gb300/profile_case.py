@@ -10,6 +10,10 @@ command line, without the memory of a whole layer step.
         --experts 16 --rows 1536 --cols 2048 [--dual]
     python -m nvfp4_w4a4_moe_permute_gb300.profile_case permute_swiglu --tokens 16384
     python -m nvfp4_w4a4_moe_permute_gb300.profile_case gemm --tokens 8192 --gemm gate_up
+    python -m nvfp4_w4a4_moe_permute_gb300.profile_case grouped_bf16 --product wgrad \\
+        --rows 32768 --cols 1536 --inner 2048 --experts 128
+    python -m nvfp4_w4a4_moe_permute_gb300.profile_case logprobs --rows 1024 --cols 131072 [--backward]
+    python -m nvfp4_w4a4_moe_permute_gb300.profile_case adamw --rows 100000000 --bits 8
 
 Expert sizes follow a Zipf(1.5) draw over the experts (a skewed routing);
 every call's device status is checked at the end.
@@ -145,7 +149,64 @@ def gemm(args, M, dev, status):
     M.minite_set_gemm_variant(0)
 
 
-CASES = {"quantize_tokens": quantize_tokens, "quantize_weights": quantize_weights,
+def grouped_bf16(args, M, dev, status):
+    """A BF16 product of `--rows` rows grouped by expert: forward or dgrad to
+    `--cols` columns over `--inner` values, or the weight gradient of a `--cols`
+    x `--inner` projection, added to FP32. `--even`: all experts alike."""
+    rng = np.random.default_rng(args.seed)
+    N, K, E = args.cols, args.inner, args.experts
+    if args.even:
+        off = torch.arange(E + 1, dtype=torch.int32, device=dev) * (args.rows // E)
+    else:
+        off = _expert_offsets(rng, args.rows, E, dev)
+    gen = torch.Generator(device=dev).manual_seed(args.seed)
+
+    def randn(*shape):
+        return torch.randn(shape, device=dev, generator=gen).to(torch.bfloat16)
+
+    if args.product == "wgrad":
+        dy, x = randn(args.rows, N), randn(args.rows, K)
+        out = torch.zeros((E, N, K), dtype=torch.float32, device=dev)
+        for _ in range(args.reps):
+            M.grouped_wgrad_bf16(dy, x, off, out=out, accumulate=True, status=status)
+        return
+    stored = args.product == "dgrad"
+    x, w = randn(args.rows, K), randn(E, K, N) if stored else randn(E, N, K)
+    for _ in range(args.reps):
+        M.grouped_gemm_bf16(x, w, off, w_as_stored=stored, status=status)
+
+
+def logprobs(args, M, dev, status):
+    """Token log probabilities of `--rows` BF16 rows of `--cols` logits with
+    `--alternatives`, or their gradient."""
+    gen = torch.Generator(device=dev).manual_seed(args.seed)
+    x = (torch.randn((args.rows, args.cols), device=dev, generator=gen) * 2).to(torch.bfloat16)
+    y = torch.randint(0, args.cols, (args.rows,), device=dev, generator=gen, dtype=torch.int32)
+    g = torch.ones(args.rows, device=dev)
+    r = M.token_logprobs(x, y, alternatives=args.alternatives, status=status)
+    for _ in range(args.reps):
+        if args.backward:
+            M.token_logprobs_backward(x, y, r, g, g, status=status)
+        else:
+            M.token_logprobs(x, y, alternatives=args.alternatives, status=status)
+
+
+def adamw(args, M, dev, status):
+    """AdamW steps of `--rows` BF16 parameters with 8-bit states, or of FP32 ones
+    with BF16 copies and 32-bit states, in 24 tensors."""
+    gen = torch.Generator(device=dev).manual_seed(args.seed)
+    sizes = [args.rows // 24] * 24
+    dtype = torch.bfloat16 if args.bits == 8 else torch.float32
+    p = [torch.randn(n, device=dev, generator=gen).to(dtype) for n in sizes]
+    grads = [(torch.randn(n, device=dev, generator=gen) * 1e-3).to(torch.bfloat16) for n in sizes]
+    opt = M.AdamW(p, copies=None if args.bits == 8 else [q.to(torch.bfloat16) for q in p],
+                  state_bits=args.bits)
+    for _ in range(args.reps):
+        opt.step(grads)
+
+
+CASES = {"grouped_bf16": grouped_bf16, "logprobs": logprobs, "adamw": adamw,
+         "quantize_tokens": quantize_tokens, "quantize_weights": quantize_weights,
          "permute_swiglu": permute_swiglu, "gemm": gemm}
 
 
@@ -161,6 +222,12 @@ def main(argv=None) -> int:
     ap.add_argument("--gemm", default="gate_up",
                     choices=["gate_up", "gate_up_swiglu", "down", "dgrad"])
     ap.add_argument("--variant", type=int, default=0, help="gemm: grouped-GEMM kernel (0 automatic)")
+    ap.add_argument("--inner", type=int, default=2048, help="grouped_bf16: length of the sums, or columns")
+    ap.add_argument("--product", default="forward", choices=["forward", "dgrad", "wgrad"])
+    ap.add_argument("--even", action="store_true", help="grouped_bf16: as many rows for every expert")
+    ap.add_argument("--alternatives", type=int, default=0)
+    ap.add_argument("--backward", action="store_true", help="logprobs: the gradient")
+    ap.add_argument("--bits", type=int, default=8, choices=[8, 32], help="adamw: the states'")
     ap.add_argument("--reps", type=int, default=3)
     ap.add_argument("--seed", type=int, default=0)
     args = ap.parse_args(argv)
