@@ -53,24 +53,34 @@ struct Params {
   int32_t* status;
 };
 
+// 32 bytes of a row, one load of a thread.
+struct Vec {
+  uint4 lo, hi;
+};
+
 template <typename T> struct Elem;
 template <> struct Elem<float> {
-  static constexpr int kVec = 4;
+  static constexpr int kVec = 8;
   static __device__ __forceinline__ float value(float x) { return x; }
-  static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[4]) {
-    x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
-    x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
+  static __device__ __forceinline__ void unpack(const Vec& u, float (&x)[8]) {
+    x[0] = __uint_as_float(u.lo.x); x[1] = __uint_as_float(u.lo.y);
+    x[2] = __uint_as_float(u.lo.z); x[3] = __uint_as_float(u.lo.w);
+    x[4] = __uint_as_float(u.hi.x); x[5] = __uint_as_float(u.hi.y);
+    x[6] = __uint_as_float(u.hi.z); x[7] = __uint_as_float(u.hi.w);
   }
 };
 template <> struct Elem<uint16_t> {
-  static constexpr int kVec = 8;
+  static constexpr int kVec = 16;
   static __device__ __forceinline__ float value(uint16_t x) {
     return __uint_as_float(static_cast<uint32_t>(x) << 16);
   }
-  static __device__ __forceinline__ void unpack(const uint4& u, float (&x)[8]) { unpack_bf16x8(u, x); }
+  static __device__ __forceinline__ void unpack(const Vec& u, float (&x)[16]) {
+    const uint32_t w[8] = {u.lo.x, u.lo.y, u.lo.z, u.lo.w, u.hi.x, u.hi.y, u.hi.z, u.hi.w};
+    unpack_bf16x16(w, x);
+  }
 };
 
-// A row as an unaligned head, 16-byte vectors and a tail.
+// A row as an unaligned head, 32-byte vectors and a tail.
 template <typename T>
 struct Row {
   const T* x;
@@ -78,14 +88,19 @@ struct Row {
   int head, tail;
   int64_t nv;
   __device__ __forceinline__ Row(const T* row, int64_t V_) : x(row), V(V_) {
-    const uintptr_t off = (16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15;
+    const uintptr_t off = (32 - (reinterpret_cast<uintptr_t>(row) & 31)) & 31;
     head = static_cast<int>(off / sizeof(T));
     if (head > V) head = static_cast<int>(V);
     nv = (V - head) / Elem<T>::kVec;
     tail = static_cast<int>(V - head - nv * Elem<T>::kVec);
   }
-  __device__ __forceinline__ uint4 vec(int64_t i) const {
-    return __ldg(reinterpret_cast<const uint4*>(x + head) + i);
+  __device__ __forceinline__ Vec vec(int64_t i) const {
+    Vec v;
+    asm("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(v.lo.x), "=r"(v.lo.y), "=r"(v.lo.z), "=r"(v.lo.w), "=r"(v.hi.x), "=r"(v.hi.y),
+          "=r"(v.hi.z), "=r"(v.hi.w)
+        : "l"(x + head + i * Elem<T>::kVec));
+    return v;
   }
   __device__ __forceinline__ int64_t tail0() const { return head + nv * Elem<T>::kVec; }
 };
@@ -117,14 +132,14 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
 
 // A vector's logits as float pairs, those below -2^60 (masked ones among
 // them) raised to it, and their maximum.
-__device__ __forceinline__ void pairs_of(const float*, const uint4& u, uint64_t (&x)[2], float& mx) {
+__device__ __forceinline__ void pairs_of(const float*, const uint4& u, uint64_t* x, float& mx) {
   const float a = max_nan(__uint_as_float(u.x), kMask), b = max_nan(__uint_as_float(u.y), kMask);
   const float c = max_nan(__uint_as_float(u.z), kMask), d = max_nan(__uint_as_float(u.w), kMask);
   mx = fmaxf(fmaxf(a, b), fmaxf(c, d));
   x[0] = pair(a, b);
   x[1] = pair(c, d);
 }
-__device__ __forceinline__ void pairs_of(const uint16_t*, const uint4& u, uint64_t (&x)[4], float& mx) {
+__device__ __forceinline__ void pairs_of(const uint16_t*, const uint4& u, uint64_t* x, float& mx) {
   constexpr uint32_t kMask2 = 0xDD80DD80u;   // -2^60 twice
   const uint32_t w0 = max_nan_bf16x2(u.x, kMask2), w1 = max_nan_bf16x2(u.y, kMask2);
   const uint32_t w2 = max_nan_bf16x2(u.z, kMask2), w3 = max_nan_bf16x2(u.w, kMask2);
@@ -244,7 +259,7 @@ struct Shared {
   uint64_t part_best[kMaxSegments][32];   // the cluster's first CTA: the others' best
 };
 
-// A row's segments [s0, s1) of `segs`: segment s holds the 16-byte vectors
+// A row's segments [s0, s1) of `segs`: segment s holds the 32-byte vectors
 // [begin(s), begin(s + 1)), thread t of it the vectors begin(s) + t + i kThreads.
 struct Segments {
   int64_t nv;
@@ -390,7 +405,7 @@ __device__ __forceinline__ void block_alternatives(Shared& S, const Row<T>& r, c
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Params p) {
   constexpr int VEC = Elem<T>::kVec;
-  constexpr int UNROLL = 8;   // 16-byte loads in flight per thread
+  constexpr int UNROLL = 4;   // 32-byte loads in flight per thread
   __shared__ Shared S;
   pdl_wait();
   const int tid = threadIdx.x;
@@ -435,10 +450,12 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Params p) {
         st.m = mx;
         m2 = pair(-mx, -mx);
       };
-      auto add = [&](const uint4& u) {
+      auto add = [&](const Vec& u) {
         uint64_t x[VEC / 2];
-        float mx;
-        pairs_of(static_cast<const T*>(nullptr), u, x, mx);
+        float mx, mx2;
+        pairs_of(static_cast<const T*>(nullptr), u.lo, &x[0], mx);
+        pairs_of(static_cast<const T*>(nullptr), u.hi, &x[VEC / 4], mx2);
+        mx = fmaxf(mx, mx2);
         if (mx > st.m) up(mx);
 #pragma unroll
         for (int q = 0; q < VEC / 2; ++q) {
@@ -466,21 +483,19 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Params p) {
       const int64_t v1 = sg.begin(seg + 1);
       int64_t i = sg.begin(seg) + tid;
       for (; i + (UNROLL - 1) * kThreads < v1; i += UNROLL * kThreads) {
-        uint4 u[UNROLL];
+        Vec u[UNROLL];
 #pragma unroll
         for (int j = 0; j < UNROLL; ++j) u[j] = r.vec(i + j * kThreads);
 #pragma unroll
         for (int j = 0; j < UNROLL; ++j) add(u[j]);
       }
 #pragma unroll 1
-      for (; i < v1; i += 4 * kThreads) {   // what is left, four in flight
-        uint4 u[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (i + j * kThreads < v1) u[j] = r.vec(i + j * kThreads);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (i + j * kThreads < v1) add(u[j]);
+      for (; i < v1; i += 2 * kThreads) {   // what is left, two in flight
+        Vec u[2];
+        u[0] = r.vec(i);
+        if (i + kThreads < v1) u[1] = r.vec(i + kThreads);
+        add(u[0]);
+        if (i + kThreads < v1) add(u[1]);
       }
       float a, b;
       unpair(s2, a, b);
@@ -600,7 +615,7 @@ constexpr int kBackChunk = 8192;   // elements of a row per CTA
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) logprobs_backward_kernel(const BackParams p) {
-  constexpr int VEC = Elem<T>::kVec;
+  constexpr int VEC = 16 / sizeof(T);
   pdl_wait();
   // last rows first: the forward read them last, so L2 still holds some
   const int64_t row = gridDim.y - 1 - blockIdx.y;
