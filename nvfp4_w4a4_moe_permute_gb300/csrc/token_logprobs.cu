@@ -275,14 +275,38 @@ __device__ __forceinline__ Stat join_warp(Stat st, float k) {
   for (int o = 16; o > 0; o >>= 1) st.merge(shfl_xor(st, o), k);
   return st;
 }
-// S.stat of n segments to S.part[s0 ...], one thread a segment. Block-wide, a
+// S.stat of n segments to S.part[s0 ...], one thread a segment, and, for the
+// alternatives, the largest of the groups' maxima that at least k of them reach
+// to S.thr. `mine` is the largest logit that this thread saw. Block-wide, with a
 // barrier at both ends.
-__device__ __forceinline__ void join_segments(Shared& S, int s0, int n, float k) {
+__device__ __forceinline__ void join_segments(Shared& S, int s0, int n, float k2, float mine, int k) {
+  const int tid = threadIdx.x;
+  if (k > 0) {
+    float g = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
+    g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
+    if ((tid & 3) == 0) S.group_max[tid >> 2] = g;
+    if (tid == 0) {
+      S.thr = 0;
+      S.n_sets = 0;
+      S.n_cand = 0;
+    }
+    if (tid < 32) S.best[tid] = 0;
+  }
   __syncthreads();
-  if (threadIdx.x < n) {
-    Stat st = S.stat[threadIdx.x][0];
-    for (int w = 1; w < kWarps; ++w) st.merge(S.stat[threadIdx.x][w], k);
-    S.part[s0 + threadIdx.x] = st;
+  if (tid < n) {
+    Stat st = S.stat[tid][0];
+    for (int w = 1; w < kWarps; ++w) st.merge(S.stat[tid][w], k2);
+    S.part[s0 + tid] = st;
+  }
+  if (k > 0 && tid >= kThreads - kGroups) {
+    const float own = S.group_max[tid - (kThreads - kGroups)];
+    int reach = 0;
+#pragma unroll
+    for (int j = 0; j < kGroups / 4; ++j) {
+      const float4 o = reinterpret_cast<const float4*>(S.group_max)[j];
+      reach += (o.x >= own) + (o.y >= own) + (o.z >= own) + (o.w >= own);
+    }
+    if (reach >= k) atomicMax(&S.thr, static_cast<uint32_t>(rank_key(own, 0) >> 32));
   }
   __syncthreads();
 }
@@ -300,7 +324,8 @@ __device__ __forceinline__ void rank_keys(const uint64_t* keys, int n, uint64_t*
 
 // The k best of some segments (with the row's head if they are the first, its
 // tail if the last) to S.best. `mine` is the largest logit that this thread saw
-// in them: its vectors, head element tid, tail element tid. Ends with a barrier.
+// in them: its vectors, head element tid, tail element tid. After join_segments;
+// ends with a barrier.
 template <typename T>
 __device__ __forceinline__ void block_alternatives(Shared& S, const Row<T>& r, const Segments& sg,
                                                    float mine, int k) {
@@ -308,27 +333,6 @@ __device__ __forceinline__ void block_alternatives(Shared& S, const Row<T>& r, c
   const float inf = __int_as_float(0x7F800000);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool first = sg.first(), last = sg.last();
-  float g = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
-  g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
-  if ((tid & 3) == 0) S.group_max[tid >> 2] = g;
-  if (tid == 0) {
-    S.thr = 0;
-    S.n_sets = 0;
-    S.n_cand = 0;
-  }
-  if (tid < 32) S.best[tid] = 0;
-  __syncthreads();
-  if (tid < kGroups) {   // the largest of the groups' maxima that at least k of them reach
-    const float own = S.group_max[tid];
-    int reach = 0;
-#pragma unroll
-    for (int j = 0; j < kGroups / 4; ++j) {
-      const float4 o = reinterpret_cast<const float4*>(S.group_max)[j];
-      reach += (o.x >= own) + (o.y >= own) + (o.z >= own) + (o.w >= own);
-    }
-    if (reach >= k) atomicMax(&S.thr, static_cast<uint32_t>(rank_key(own, 0) >> 32));
-  }
-  __syncthreads();
   float thr = key_value(static_cast<uint64_t>(S.thr) << 32);
   if (thr <= kMask) thr = -inf;   // what threads with masked logits only hold, or none
   auto offer = [&](float x, int64_t i) {
@@ -506,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Params p) {
       st = join_warp(st, k2);
       if ((tid & 31) == 0) S.stat[seg - sg.s0][tid >> 5] = st;
     }
-    join_segments(S, sg.s0, sg.s1 - sg.s0, k2);
+    join_segments(S, sg.s0, sg.s1 - sg.s0, k2, mine, p.k);
     if (p.k > 0) block_alternatives<T>(S, r, sg, mine, p.k);
     if (C > 1) {
       cluster_wait();   // all CTAs run: their shared memory can be written
@@ -564,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const Params p) {
     __syncthreads();   // S is written again
     st = join_warp(st, k2);
     if ((tid & 31) == 0) S.stat[0][tid >> 5] = st;
-    join_segments(S, 0, 1, k2);
+    join_segments(S, 0, 1, k2, mine, p.k);
     st = S.part[0];
     if (p.k > 0) block_alternatives<T>(S, r, all, mine, p.k);
   }
