@@ -208,6 +208,18 @@ def test_gradient_against_differences():
         assert ((slope - (d.double() * u.double()).sum(1)).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("v", [4099, 32000, 50001, 100003])
+def test_a_rows_results_do_not_depend_on_the_batch(v):
+    """Alone (a cluster for a row), among 40 rows and among 1000: the same bits."""
+    x = logits_of(31, 1000, v, torch.bfloat16, pad=3)
+    y = torch.arange(1000, dtype=torch.int32, device=DEV) % v
+    many = M.token_logprobs(x, y, temperature=0.9, alternatives=7)
+    for n in (1, 40):
+        few = M.token_logprobs(x[960:960 + n], y[960:960 + n], temperature=0.9, alternatives=7)
+        for key in ("logprob", "entropy", "stats", "alt_ids", "alt_logprobs"):
+            assert torch.equal(few[key], many[key][960:960 + n]), key
+
+
 def test_no_targets_and_no_rows():
     x = logits_of(11, 9, 700, torch.bfloat16)
     r = M.token_logprobs(x)
