@@ -20,7 +20,7 @@
 //
 // Bound by HBM. FP32 states (28 bytes an element with a BF16 copy): plain 16-byte
 // loads, 604M elements in 2.41 ms, 7.0 TB/s. 8-bit states (10 bytes an element
-// with BF16 parameters and gradients, 55 instructions): asynchronous copies three
+// with BF16 parameters and gradients, 50 instructions): asynchronous copies three
 // reads ahead, the scales of 64 blocks read and written at once; 400M elements
 // in 0.65 ms, 6.2 TB/s (1.11 ms with plain loads and IEEE roots and quotients).
 // Up to 440 tensors' pointers travel as kernel parameters (48 in a small set),

@@ -12,11 +12,19 @@
 // new one when it grows (s <- c s, t <- c (t + d s) for a shift d, c = exp d).
 //
 // The top alternatives cost the streaming loop nothing. Every thread's running
-// maximum is the largest of the values it saw, so the k-th largest of these
-// maxima is a lower bound of the row's k-th largest logit, and only threads
-// whose maximum reaches it can hold one of the top k (about k of them): a warp
-// then reads those threads' elements again, from L2, and keeps its k best in
-// its lanes. Equal logits rank by the lower index.
+// maximum is the largest of the values it saw, so the k-th largest of the
+// maxima of groups of four threads is a lower bound of the row's k-th largest
+// logit, and only threads whose maximum reaches it can hold one of the top k:
+// those threads' elements are read again, mostly from L2, and the few at or
+// above the bound are ranked by counting (more than kCandidates of them by
+// sorted lists in the lanes of warps). Equal logits rank by the lower index.
+//
+// Bound by HBM for learner batches: 4096 rows of 131072 BF16 171 us forward (161
+// at the copy rate), 336 to 341 backward (321); the forward executes 8.5
+// instructions an element (issue slots 59% busy). With 20 alternatives 225 us:
+// the second reading fetches 16% more from HBM. A single row takes a cluster:
+// 10.6 us for 131072 FP32 logits with 20 alternatives, 7.5 without, most of it
+// latency.
 #include <cmath>
 
 #include "common.cuh"
