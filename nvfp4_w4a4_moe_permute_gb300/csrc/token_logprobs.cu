@@ -5,11 +5,15 @@
 // With y = x / T over a row's V logits, M = max y, s = sum exp(y - M) and
 // t = sum (y - M) exp(y - M):
 //   log p_j = y_j - M - log s,  logprob = log p_i,  H = log s - t / s
+// s is kept as r = s - 1, the sum without the maximum's own term, and log s =
+// log1p(r): a token that is almost certain has a log probability of -r, which
+// would be lost beside the 1 (r = 1e-4 to three digits).
 //   dx_j = (1/T) (g_lp ([j = i] - p_j) - g_H p_j (log p_j + H))
 // M (as a logit) and log s are kept apart for the backward: their sum would
 // lose log s beside a large M.
-// M, s and t come from one pass: a running maximum, with s and t moved to the
-// new one when it grows (s <- c s, t <- c (t + d s) for a shift d, c = exp d).
+// M, r and t come from one pass: a running maximum, with r and t moved to the
+// new one when it grows (t <- c (t + d (r + 1)), r <- c (r + 1) for a shift d,
+// c = exp d).
 //
 // The top alternatives cost the streaming loop nothing. Every thread's running
 // maximum is the largest of the values it saw, so the k-th largest of the
@@ -160,32 +164,41 @@ __device__ __forceinline__ void pairs_of(const uint16_t*, const uint4& u, uint64
 }
 
 // Running (maximum, sum, weighted sum) of a set of logits in powers of two,
-// with k = log2(e) / T and y = (x - m) k:  s = sum 2^y,  t = sum y 2^y. The
-// difference is taken before the product, so that y is exactly 0 at the
-// maximum (a row with one token left has logprob 0 and entropy 0).
+// with k = log2(e) / T and y = (x - m) k:  r = sum 2^y without one element at the
+// maximum, t = sum y 2^y. The difference is taken before the product, so that y
+// is exactly 0 at the maximum (a row with one token left has logprob 0 and
+// entropy 0).
 struct Stat {
-  float m, s, t;
+  float m, r, t;
   __device__ __forceinline__ void raise(float nm, float k) {
     const float d = (m - nm) * k;
     const float c = ex2(d);
+    const float s = r + 1.0f;
     t = c > 0.0f ? c * (t + d * s) : 0.0f;   // d * s may be infinite where c is 0
-    s = c * s;
+    r = c * s;
     m = nm;
   }
   __device__ __forceinline__ void merge(Stat o, float k) {
     if (o.m > m) raise(o.m, k);
     else if (o.m < m) o.raise(m, k);
-    s += o.s;
+    else o.r += 1.0f;   // one maximum of the two counts
+    r += o.r;
     t += o.t;
   }
   // One logit, every special value looked at: for a row whose maximum lies
   // beyond +-2^59 (all of it masked, or infinite) or an extreme temperature.
+  // m is -inf until there is a logit above it.
   __device__ __forceinline__ void add_any(float x, float k) {
-    if (x > m) raise(x, k);
+    if (x > m) {
+      raise(x, k);
+      r += x - x;   // +inf: no probabilities
+      return;
+    }
+    if (x == __int_as_float(0xFF800000)) return;   // masked: adds 0
     const float y = (x - m) * k;
     const float e = ex2(y);
-    s += e;
-    t += fmaxf(y, -1e30f) * e;   // a masked logit (-inf) adds 0, not -inf * 0
+    r += e;
+    t += fmaxf(y, -1e30f) * e;   // y may be -inf, which adds 0, not -inf * 0
   }
 };
 // k in (2^-40, 2^13): a logit of -2^60 then has probability zero beside any
@@ -197,7 +210,7 @@ __device__ __forceinline__ bool fast_row(float m) { return fabsf(m) < 5.76460752
 __device__ __forceinline__ Stat shfl_xor(const Stat& a, int o) {
   Stat r;
   r.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-  r.s = __shfl_xor_sync(0xffffffffu, a.s, o);
+  r.r = __shfl_xor_sync(0xffffffffu, a.r, o);
   r.t = __shfl_xor_sync(0xffffffffu, a.t, o);
   return r;
 }
@@ -451,37 +464,58 @@ __global__ void __launch_bounds__(kThreads, CTAS) logprobs_kernel(const Params p
     const uint64_t kk = pair(k2, k2);
     float mine = kMask;
     for (int seg = sg.s0; seg < sg.s1; ++seg) {
+      // s2 sums all vectors but the one that holds the maximum; that one's sum
+      // is `top` (with the maximum's 1), its index `at`.
       st = Stat{kMask, 0.0f, 0.0f};
       uint64_t s2 = 0, t2 = 0, m2 = pair(-kMask, -kMask);
+      float top = 1.0f;
+      int at = -1;
       auto up = [&](float mx) {   // a new maximum: rare after the first few vectors
         const float d = (st.m - mx) * k2;
         const float c = ex2(d);
         const uint64_t cc = pair(c, c), dd = pair(d, d);
+        s2 = add2(s2, pair(top, 0.0f));
         t2 = c > 0.0f ? mul2(cc, fma2(dd, s2, t2)) : 0;
         s2 = mul2(cc, s2);
         st.m = mx;
         m2 = pair(-mx, -mx);
       };
-      auto add = [&](const Vec& u) {
+      auto add = [&](const Vec& u, int64_t i) {
         uint64_t x[VEC / 2];
         float mx, mx2;
         pairs_of(static_cast<const T*>(nullptr), u.lo, &x[0], mx);
         pairs_of(static_cast<const T*>(nullptr), u.hi, &x[VEC / 4], mx2);
         mx = fmaxf(mx, mx2);
-        if (mx > st.m) up(mx);
+        const bool higher = mx > st.m;
+        if (higher) {
+          up(mx);
+          at = static_cast<int>(i);
+        }
+        uint64_t v2 = 0;
 #pragma unroll
         for (int q = 0; q < VEC / 2; ++q) {
           const uint64_t y = mul2(add2(x[q], m2), kk);
           float a, b;
           unpair(y, a, b);
           const uint64_t e = pair(ex2(a), ex2(b));
-          s2 = add2(s2, e);
+          v2 = add2(v2, e);
           t2 = fma2(y, e, t2);
+        }
+        if (higher) {
+          float a, b;
+          unpair(v2, a, b);
+          top = a + b;
+        } else {
+          s2 = add2(s2, v2);
         }
       };
       auto single = [&](float x) {
         x = max_nan(x, kMask);
-        if (x > st.m) up(x);
+        if (x > st.m) {
+          up(x);
+          top = 1.0f;
+          return;
+        }
         float s, s1, t, t1;
         unpair(s2, s, s1);
         unpair(t2, t, t1);
@@ -499,19 +533,37 @@ __global__ void __launch_bounds__(kThreads, CTAS) logprobs_kernel(const Params p
 #pragma unroll
         for (int j = 0; j < UNROLL; ++j) u[j] = r.vec(i + j * kThreads);
 #pragma unroll
-        for (int j = 0; j < UNROLL; ++j) add(u[j]);
+        for (int j = 0; j < UNROLL; ++j) add(u[j], i + j * kThreads);
       }
 #pragma unroll 1
       for (; i < v1; i += 2 * kThreads) {   // what is left, two in flight
         Vec u[2];
         u[0] = r.vec(i);
         if (i + kThreads < v1) u[1] = r.vec(i + kThreads);
-        add(u[0]);
-        if (i + kThreads < v1) add(u[1]);
+        add(u[0], i);
+        if (i + kThreads < v1) add(u[1], i + kThreads);
       }
       float a, b;
       unpair(s2, a, b);
-      st.s = a + b;
+      const float others = a + b;
+      float rest = top - 1.0f;   // of the maximum's vector
+      // Up to 16 roundings beside the 1 are 2^-20: where that is not small beside
+      // the sum, the vector is summed again without its (first) maximum. Rare in
+      // long rows, where one lane of a row whose token is almost certain does it.
+      if (others + rest < 0.25f && at >= 0) {
+        float v[VEC];
+        Elem<T>::unpack(r.vec(at), v);
+        rest = 0.0f;
+        bool found = false;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float x = max_nan(v[j], kMask);
+          const bool is = !found && x == st.m;
+          found |= is;
+          rest += is ? 0.0f : ex2((x - st.m) * k2);
+        }
+      }
+      st.r = others + rest;
       unpair(t2, a, b);
       st.t = a + b;
       mine = fmaxf(mine, st.m);
@@ -527,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) logprobs_kernel(const Params p
           const Stat& o = S.part[sg.s0 + tid];
           const uint32_t to = mapa_shared(smem_u32(&o), 0);
           st_shared_cluster(to, __float_as_uint(o.m));
-          st_shared_cluster(to + 4, __float_as_uint(o.s));
+          st_shared_cluster(to + 4, __float_as_uint(o.r));
           st_shared_cluster(to + 8, __float_as_uint(o.t));
         }
         if (tid < p.k) {
@@ -563,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) logprobs_kernel(const Params p
   }
   if (!p.fast || !fast_row(st.m)) {   // the first CTA does the whole row
     const Segments all = {r.nv, 1, 0, 1};
-    st = Stat{kLowest, 0.0f, 0.0f};
+    st = Stat{__int_as_float(0xFF800000), 0.0f, 0.0f};
     if (tid < r.head) st.add_any(Elem<T>::value(r.x[tid]), k2);
     if (tid < r.tail) st.add_any(Elem<T>::value(r.x[r.tail0() + tid]), k2);
     for (int64_t i = tid; i < r.nv; i += kThreads) {
@@ -581,9 +633,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) logprobs_kernel(const Params p
     if (p.k > 0) block_alternatives<T>(S, r, all, mine, p.k);
   }
   const float inf = __int_as_float(0x7F800000);
-  const bool none = st.s == 0.0f;   // every logit is -inf
-  const float log2_s = log2f(st.s);
-  const float log_s = log2_s * kLn2;
+  const bool none = st.m == -inf && st.r == st.r;   // every logit is -inf
+  const float log_s = log1pf(st.r);
   if (tid == 0) {
     if (p.targets) {
       float lp;
@@ -595,15 +646,15 @@ __global__ void __launch_bounds__(kThreads, CTAS) logprobs_kernel(const Params p
       }
       p.logprob[row] = lp;
     }
-    if (p.entropy) p.entropy[row] = none ? 0.0f : (log2_s - st.t / st.s) * kLn2;
-    if (p.stats) p.stats[row] = make_float2(none ? -inf : st.m, none ? 0.0f : log_s);
+    if (p.entropy) p.entropy[row] = none ? 0.0f : fmaf(-kLn2, st.t / (1.0f + st.r), log_s);
+    if (p.stats) p.stats[row] = none ? make_float2(-inf, 0.0f) : make_float2(fmaxf(st.m, kLowest), log_s);
   }
   if (tid < p.k) {
     const uint64_t key = S.best[tid];
-    const bool ok = key != 0 && st.s == st.s;   // a NaN or +inf logit: no ranking
+    const bool ok = key != 0 && st.r == st.r;   // a NaN or +inf logit: no ranking
     p.alt_ids[row * p.k + tid] = ok ? key_index(key) : -1;
     p.alt_lp[row * p.k + tid] =
-        st.s != st.s ? st.s : (ok ? fmaf(key_value(key) - st.m, p.inv_t, -log_s) : -inf);
+        st.r != st.r ? st.r : (ok ? fmaf(key_value(key) - st.m, p.inv_t, -log_s) : -inf);
   }
 }
 
