@@ -79,3 +79,37 @@ def test_tied_maxima_share_the_probability(dtype):
     bound = (8 + 5003 / 256 + 64) * 2.0 ** -24
     assert ((got["logprob"].double() + n.log()).abs() <= bound * n.log()).all()
     assert ((got["entropy"].double() - n.log()).abs() <= 2 * bound * n.log()).all()
+
+
+@pytest.mark.parametrize("vocab", [33, 1000, 32003, 131072])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_gradient_at_confident_tokens_keeps_relative_accuracy(vocab, offset):
+    """At the target, d = (g_lp (1 - p) - g_H p (log p + H)) / T: each of the three
+    numbers 1 - p, log p and H carries the bound above (H twice), and the result
+    one rounding."""
+    dtype, temperature = torch.float32, 0.8
+    x, y = _rows(dtype, vocab, temperature, False, 3 * vocab)
+    n = x.shape[0]
+    if offset:   # rows that start off a 16-byte boundary
+        wide = torch.zeros(n, vocab + 1, device="cuda", dtype=dtype)
+        wide[:, 1:] = x
+        x = wide[:, 1:]
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    gl = torch.randn(n, generator=g, device="cuda")
+    ge = 0.1 * torch.randn(n, generator=g, device="cuda")
+    fwd = M.token_logprobs(x, y, temperature=temperature)
+    d = torch.empty(n, vocab, device="cuda", dtype=dtype)
+    M.token_logprobs_backward(x, y, fwd, gl, ge, temperature=temperature, out=d)
+    got = d.gather(1, y.long()[:, None])[:, 0].double()
+    z = (x.double() - x.double().amax(1, keepdim=True)) / temperature
+    e = torch.where(z == 0, 0.0, z.exp())
+    r = e.sum(1)
+    lp, q = -torch.log1p(r), r / (1 + r)
+    h = torch.log1p(r) - (z * e).sum(1) / (1 + r)
+    one, two = gl.double() * q, ge.double() * (1 - q)
+    exact = (one - two * (lp + h)) / temperature
+    far = -z.amin(1)
+    bound = (3 * far + 4 + vocab / 256 + 64 + 16) * 2.0 ** -24
+    slack = bound * (one.abs() + two.abs() * (lp.abs() + 2 * h)) / temperature
+    unit = 2.0 ** -24
+    assert ((got - exact).abs() <= slack * (1 + unit) + unit * exact.abs() + vocab * 2.0 ** -120).all()
