@@ -23,11 +23,11 @@
 // above the bound are ranked by counting (more than kCandidates of them by
 // sorted lists in the lanes of warps). Equal logits rank by the lower index.
 //
-// Bound by HBM for learner batches: 4096 rows of 131072 BF16 171 us forward (161
-// at the copy rate), 336 to 341 backward (321); the forward executes 8.5
-// instructions an element (issue slots 59% busy). With 20 alternatives 225 us:
+// Bound by HBM for learner batches: 4096 rows of 131072 BF16 175 us forward (161
+// at the copy rate), 313 backward (321); the forward executes 9.1
+// instructions an element (issue slots 61% busy). With 20 alternatives 229 us:
 // the second reading fetches 16% more from HBM. A single row takes a cluster:
-// 10.6 us for 131072 FP32 logits with 20 alternatives, 7.5 without, most of it
+// 10.9 us for 131072 FP32 logits with 20 alternatives, 7.5 without, most of it
 // latency.
 #include <cmath>
 
@@ -803,9 +803,9 @@ cudaError_t launch_forward(Params& p, int64_t N, cudaStream_t s) {
   cfg.numAttrs = c > 1 ? 2 : 1;
   // Short rows: a CTA's time is latency (its start, the joins, the second look),
   // so eight CTAs an SM with one load in flight each; long ones, and few: four
-  // with four. 4096 rows of 32000 BF16 with 20 alternatives: 70 us against 85; of
-  // 131072: 226 against 225 (without alternatives 177 against 171). 512 rows of
-  // 131072: 42 against 38.
+  // with four. 4096 rows of 32000 BF16: 58 us against 66, with 20 alternatives 78
+  // against 90; of 131072: 189 against 175, 237 against 229. 512 rows of 131072
+  // with 20 alternatives: 45 against 39.
   if (p.V * static_cast<int64_t>(sizeof(T)) <= 65536 && N > 4 * num_sms())
     return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, 1, 8>, p);
   return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, 4, 4>, p);
