@@ -541,8 +541,7 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
       const bool b_two = B_MN && tl.by_rows && box2 >= 0 && p.b_two && b0 % 64 == 0;
       for (int kt = 0; kt < kt_n; ++kt, turn ^= 1) {
         if (turn != which) {   // the other warp's
-          armed_mask |= 1u << stage;
-          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+          armed_mask &= ~(1u << stage);
           if (++stage == p.stages) { stage = 0; phase ^= 1u; }
           continue;
         }
@@ -598,12 +597,19 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
       }
     }
     if (!ok && lane == 0) fail();
+    // No copy may be in flight when a CTA exits: each stage's last ones are waited
+    // for by the warp that issued them. After a wait that ran out the two warps
+    // stop at different blocks, and a stage may hold one CTA's copies alone: each
+    // producer then gives its own time to land before it comes to the last barrier.
     volatile int no_abort = 0;
-    if (rank == 0 && which == 0) {
-      // every stage's last copies must have landed before exit
+    if (rank == 0) {
       for (int s = 0; s < p.stages; ++s)
         if (armed_mask & (1u << s))
           mbar_wait(&S.full[s], (armed_parity >> s) & 1u, kDrainBudget, &no_abort);
+    }
+    if (*abort_flag) {
+      const uint64_t t0 = globaltimer();
+      while (globaltimer() - t0 < 100000ull) {}
     }
   } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------------------ MMA issuer (even CTA)
@@ -800,12 +806,6 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
     if (!ok && lane == 0) fail();
   }
 
-  // after a wait that ran out, copies of a stage that was not armed may still be
-  // in flight: give them time to land before a CTA can exit
-  if (warp == 0 && *abort_flag) {
-    const uint64_t t0 = globaltimer();
-    while (globaltimer() - t0 < 100000ull) {}
-  }
   __syncwarp();
   tc_fence_before();
   cluster_sync_all();
