@@ -825,6 +825,17 @@ __device__ __forceinline__ void bar_sync_named(uint32_t id, uint32_t count) {
   asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(count) : "memory");
 }
 
+// The same, and whether `ok` holds for all `count` threads.
+__device__ __forceinline__ bool bar_all_named(uint32_t id, uint32_t count, bool ok) {
+  uint32_t all;
+  asm volatile("{\n\t.reg .pred p, q;\n\t"
+               "setp.ne.u32 p, %3, 0;\n\t"
+               "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+               "selp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(all) : "r"(id), "r"(count), "r"(static_cast<uint32_t>(ok)) : "memory");
+  return all != 0;
+}
+
 // Device-scope stores and loads of global words (served by L2, not L1).
 __device__ __forceinline__ void st_relaxed_gpu(uint32_t* p, uint32_t v) {
   asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" :: "l"(p), "r"(v) : "memory");

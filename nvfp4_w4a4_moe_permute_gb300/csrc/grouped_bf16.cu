@@ -755,12 +755,16 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
             }
           release();
         }
+        // The four warps that meet at a named barrier below, which has no bound, go
+        // on or leave together: one alone may have given up. All four come here
+        // once a tile, since every wait above is bounded.
+        const uint32_t bar_id = 1 + c0 / EPI_COLS;
+        if constexpr (TMA_OUT) ok = bar_all_named(bar_id, 128, ok);
         if (!ok) break;
         if constexpr (TMA_OUT) {
           // the four warps of the same rows stage 128 features together: a copy
           // out costs about as much as one in
           uint8_t* box = out_stage + (c0 / EPI_COLS) * OUT_BOX_BYTES;
-          const uint32_t bar_id = 1 + c0 / EPI_COLS;
           const int x = tl.f0 + 128 * static_cast<int>(rank), y = tl.i0 + c0;
           if (x < p.F) {
 #pragma unroll

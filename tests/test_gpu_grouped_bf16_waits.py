@@ -59,3 +59,22 @@ def test_products(counts, stored, out_dtype):
     w = randn(2, e, K, N) if stored else randn(2, e, N, K)
     out_of_time(lambda st: M.grouped_gemm_bf16(x, w, off, w_as_stored=stored, out_dtype=out_dtype, status=st),
                 surely=out_dtype == torch.bfloat16)
+
+
+@pytest.mark.parametrize("counts", [[4101], [3000, 0, 33, 2057, 5], [2048, 2048]])
+@pytest.mark.parametrize("kind", ["bfloat16", "float32", "accumulate"])
+def test_weight_gradients(kind, counts):
+    """The odd CTA's tail waits for all of an expert's sum where that does not end
+    on a step of 16 rows (64 blocks take at least 16 microseconds), and so does a
+    BF16 result's epilogue."""
+    N, K, e = 520, 1032, len(counts)
+    dy, x, off = randn(3, sum(counts), N), randn(4, sum(counts), K), offsets_of(counts)
+    before = torch.randn(e, N, K, generator=torch.Generator().manual_seed(5)).to(DEV)
+    dtype = torch.bfloat16 if kind == "bfloat16" else torch.float32
+
+    def call(st):
+        out = before.clone() if kind == "accumulate" else None
+        return M.grouped_wgrad_bf16(dy, x, off, out=out, out_dtype=dtype, accumulate=kind == "accumulate",
+                                    status=st)
+
+    out_of_time(call, surely=kind == "bfloat16" or any(c % 16 for c in counts))
