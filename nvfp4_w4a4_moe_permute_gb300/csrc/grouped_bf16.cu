@@ -17,23 +17,18 @@
 //    tile, one token costs 32, and the tile's width is chosen per launch. A
 //    TMEM lane then holds one feature and a warp writes 32 neighbouring
 //    features of a row, without a transposition.
-//  * Two CTAs on the SMs of a cluster work on one 256 (features) x N tile with
+//  * The two CTAs of a cluster work on one 256 (features) x N tile with
 //    tcgen05.mma.cta_group::2: each loads 128 features and half the rows, K
 //    consumed 64 values (128 bytes) a stage, and holds 128 x N sums in TMEM,
-//    twice, so that a tile's epilogue runs under the next one's products.
-//  * Two such pairs share a cluster of four and one of their operands, each
-//    box of which is loaded once and multicast to both pairs: an expert of up
-//    to 256 rows gives them two feature tiles of the same rows, a larger one
-//    two tiles of rows of the same features. What bounds pairs that share
-//    nothing is the traffic from L2, about 44 bytes a cycle and SM (32 KB for
-//    the 512 cycles of a full stage are 64; shared, 48): 8 experts of 8192 rows,
-//    2048 x 1536, took 255 us before, 221 to 226 now (1866 to 1823 TFLOP/s, 97
-//    to 95% of the measured burst rate). Two tiles of rows on separate clusters also fetched part of
-//    the weight twice from DRAM.
-//  * Large experts (bound by the tensor cores) and small ones (bound by DRAM)
-//    are interleaved, so that both are busy: 65536 rows in Zipf shares, 2048 x
-//    1536, 312 us (floors: tensor 214, HBM 191). 128 experts of 256 rows, 1536 x
-//    2048: 160 us, 97% of the copy rate; of 16 rows 127.
+//    twice, so that a tile's epilogue runs under the next one's products. Every
+//    copy is a CTA's own: no load is multicast, so that no call can make one
+//    read memory of another GPU.
+//    8 experts of 8192 rows, 2048 x 1536, take 232 us (1778 TFLOP/s, 92% of the
+//    measured burst rate).
+//  * Large experts (bound by the tensor cores and L2) and small ones (bound by
+//    DRAM) are interleaved, so that all are busy: 65536 rows in Zipf shares, 2048
+//    x 1536, 327 us (floors: tensor 214, HBM 191). 128 experts of 256 rows, 1536 x
+//    2048: 168 us, 93% of the copy rate; of 16 rows 131.
 //  * Operands come by TMA with the 128-byte swizzle, K-major (rows of 64 K
 //    values) or, where memory has the other dimension contiguous (dgrad's
 //    weight, both operands of the weight gradient), MN-major: boxes of 64 such
@@ -52,7 +47,7 @@
 //    the chunks are added in FP32 registers (round to nearest) by the
 //    epilogue warps. For BF16 outputs the final rounding hides that loss.
 //    Weight gradients in FP32 leave by bulk copies that store or add in L2:
-//    561 us for 128 experts of 256 rows, 1536 x 2048, added (floor 517).
+//    606 us for 128 experts of 256 rows, 1536 x 2048, added (floor 517).
 //  * Fixed K order, no split over CTAs: results do not depend on the launch.
 //  * Every mbarrier wait is bounded; on expiry the CTA records
 //    MINITE_ERR_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
@@ -91,7 +86,7 @@ enum Mode { FORWARD = 0, DGRAD = 1, WGRAD = 2 };
 
 struct Smem {
   uint64_t full[MAX_STAGES];        // even CTA: all copies to both CTAs have landed
-  uint64_t empty[MAX_STAGES];       // every pair of the cluster is done with the stage
+  uint64_t empty[MAX_STAGES];       // the products of the stage are done
   uint64_t tail_full[MAX_STAGES];   // odd CTA: its copies of a stage with rows to zero
   uint64_t tail_ready[MAX_STAGES];  // even CTA: the odd CTA has zeroed them
   uint64_t acc_full[2];
@@ -109,7 +104,7 @@ struct Smem {
 constexpr int kListed = 64;
 struct ListedTile {
   int row0;
-  uint16_t rows, f, e, by_rows;
+  uint16_t rows, f, e, pad;
 };
 
 struct Params {
@@ -123,7 +118,6 @@ struct Params {
   int E;
   int units;       // wgrad: length of the list of work
   int max_n;       // rows of a tile at most, a multiple of 32
-  int by_rows;     // wgrad: the cluster's pairs take two row tiles, not two feature tiles
   int a_two, b_two;  // the maps of two boxes of features (wgrad: of output rows) serve
   int stages;
   int chunk;       // K blocks summed in TMEM before the epilogue takes them
@@ -131,7 +125,7 @@ struct Params {
   uint64_t budget_ns;
 };
 
-// Boxes of every size that a stage can need: a stage is two copies a CTA.
+// Boxes of every size that a stage can need: a stage is two to four copies a CTA.
 struct Maps {
   CUtensorMap a1, a2;           // 64 and 128 features
   CUtensorMap b[kTokenBoxes];   // tokens; wgrad: b[0], b[1] are 64 and 128 output rows
@@ -140,20 +134,19 @@ struct Maps {
 
 struct Tile {
   int e, f0;
-  bool by_rows;    // the cluster's pairs share the features, not the rows
   int row0;        // forward, dgrad: first token; wgrad: first of the rows summed over
   int i0;          // wgrad: first output row within the expert
   int64_t orow0;   // first output row
-  int rows;        // output rows of the tile (none in a pair that ran out of them)
+  int rows;        // output rows of the tile
   int n;           // rows the matrix instruction covers: `rows` rounded up to 32
   int len;         // length of the sums
 };
 
-// The list of a cluster's work: for each expert the tiles of its two pairs.
+// The list of work, one tile a unit.
 struct Work {
   const int32_t* off;      // [E+1]
-  const int32_t* large;    // [E+1] units of the larger experts before e
-  const int32_t* small;    // [E+1] units of the experts of at most max_n rows before e
+  const int32_t* large;    // [E+1] tiles of the larger experts before e
+  const int32_t* small;    // [E+1] tiles of the experts of at most max_n rows before e
   const uint16_t* size;    // [E] rows of a larger expert's tiles
   const ListedTile* list;  // [kListed]
   int f_tiles;
@@ -168,24 +161,19 @@ __device__ __forceinline__ int expert_of(const int32_t* prefix, int E, int u) {
   return lo;
 }
 
-// Unit t of the list, for one of the cluster's pairs.
+// Unit t of the list.
 template <int MODE>
-__device__ __forceinline__ Tile decode(int t, int pair, const Work& w, const Params& p) {
+__device__ __forceinline__ Tile decode(int t, const Work& w, const Params& p) {
   Tile r;
-  const int f_groups = (w.f_tiles + 1) >> 1;
+  const uint32_t f_tiles = w.f_tiles;
   if constexpr (MODE == WGRAD) {
-    r.by_rows = p.by_rows;
-    const int per_row = r.by_rows ? w.f_tiles : f_groups;
-    const int bt = t / per_row, f = t - bt * per_row;
-    const int i_tiles = (p.K + p.max_n - 1) / p.max_n;
-    const int per_e = r.by_rows ? (i_tiles + 1) >> 1 : i_tiles;
-    r.e = bt / per_e;
-    const int it = bt - r.e * per_e;
-    r.f0 = (r.by_rows ? f : 2 * f + pair) * BF;
-    r.i0 = (r.by_rows ? 2 * it + pair : it) * p.max_n;
+    const int it = t / w.f_tiles, i_tiles = (p.K + p.max_n - 1) / p.max_n;
+    r.e = it / i_tiles;
+    r.f0 = (t - it * w.f_tiles) * BF;
+    r.i0 = (it - r.e * i_tiles) * p.max_n;
     r.row0 = w.off[r.e];
     r.orow0 = static_cast<int64_t>(r.e) * p.K + r.i0;
-    r.rows = max(0, min(p.max_n, p.K - r.i0));
+    r.rows = min(p.max_n, p.K - r.i0);
     r.len = w.off[r.e + 1] - w.off[r.e];
   } else {
     // the larger experts' units spread evenly over the list
@@ -200,18 +188,17 @@ __device__ __forceinline__ Tile decode(int t, int pair, const Work& w, const Par
       before = static_cast<int>(tl / all);
       rest = static_cast<uint32_t>(tl - before * all);
     }
-    r.by_rows = rest + L >= all;
     int at = 0, size = p.max_n;
-    if (r.by_rows) {
+    if (rest + L >= all) {
       r.e = expert_of(w.large, p.E, before);
-      const uint32_t u = before - w.large[r.e], f_tiles = w.f_tiles, two = u / f_tiles;
+      const uint32_t u = before - w.large[r.e], row_tile = u / f_tiles;
       size = w.size[r.e];
-      r.f0 = static_cast<int>(u - two * f_tiles) * BF;
-      at = (2 * static_cast<int>(two) + pair) * size;
+      r.f0 = static_cast<int>(u - row_tile * f_tiles) * BF;
+      at = static_cast<int>(row_tile) * size;
     } else {
       const int u = t - before;
       r.e = expert_of(w.small, p.E, u);
-      r.f0 = (2 * (u - w.small[r.e]) + pair) * BF;   // may lie past the last feature
+      r.f0 = (u - w.small[r.e]) * BF;
     }
     r.i0 = 0;
     r.row0 = w.off[r.e] + at;
@@ -234,13 +221,12 @@ constexpr uint32_t idesc_base() {
 
 // Unit t, the i-th of this cluster.
 template <int MODE>
-__device__ __forceinline__ Tile unit(int t, int i, int pair, const Work& w, const Params& p) {
-  if (MODE == WGRAD || i >= kListed) return decode<MODE>(t, pair, w, p);
+__device__ __forceinline__ Tile unit(int t, int i, const Work& w, const Params& p) {
+  if (MODE == WGRAD || i >= kListed) return decode<MODE>(t, w, p);
   const ListedTile l = w.list[i];
   Tile r;
   r.e = l.e;
   r.f0 = l.f * BF;
-  r.by_rows = l.by_rows != 0;
   r.row0 = l.row0;
   r.i0 = 0;
   r.orow0 = l.row0;
@@ -259,29 +245,19 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d, uint64_t a, uint64_t b
       :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// TMA loads for the pairs of a cluster. Plain: into this CTA, counted on an
-// mbarrier of either CTA of its pair. Multicast: into the same place of every
-// CTA in `mask`, counted there on the barrier at mbar's place of that CTA or of
-// the other one of its pair, whichever has the parity of mbar's CTA.
+// TMA loads into this CTA, counted on an mbarrier of either CTA of the pair.
 template <int D>
-__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, uint32_t mbar, bool mc,
-                                              uint16_t mask, int x, int y, int z = 0, int w = 0) {
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, uint32_t mbar, int x, int y,
+                                              int z = 0, int w = 0) {
   const uint32_t d = smem_u32(dst);
   const uint64_t m = reinterpret_cast<uint64_t>(map);
-#define MINITE_TMA(dim, mcast, coords, ...)                                                        \
+#define MINITE_TMA(dim, coords)                                                                   \
   asm volatile("cp.async.bulk.tensor." dim ".cta_group::2.shared::cluster.global.tile"             \
-               ".mbarrier::complete_tx::bytes" mcast " [%0], [%1, " coords "], [%2]" __VA_ARGS__    \
-               :: "r"(d), "l"(m), "r"(mbar), "h"(mask), "r"(x), "r"(y), "r"(z), "r"(w) : "memory")
-  if constexpr (D == 2) {
-    if (mc) MINITE_TMA("2d", ".multicast::cluster", "{%4, %5}", ", %3;");
-    else MINITE_TMA("2d", "", "{%4, %5}", ";");
-  } else if constexpr (D == 3) {
-    if (mc) MINITE_TMA("3d", ".multicast::cluster", "{%4, %5, %6}", ", %3;");
-    else MINITE_TMA("3d", "", "{%4, %5, %6}", ";");
-  } else {
-    if (mc) MINITE_TMA("4d", ".multicast::cluster", "{%4, %5, %6, %7}", ", %3;");
-    else MINITE_TMA("4d", "", "{%4, %5, %6, %7}", ";");
-  }
+               ".mbarrier::complete_tx::bytes [%0], [%1, " coords "], [%2];"                       \
+               :: "r"(d), "l"(m), "r"(mbar), "r"(x), "r"(y), "r"(z), "r"(w) : "memory")
+  if constexpr (D == 2) MINITE_TMA("2d", "{%3, %4}");
+  else if constexpr (D == 3) MINITE_TMA("3d", "{%3, %4, %5}");
+  else MINITE_TMA("4d", "{%3, %4, %5, %6}");
 #undef MINITE_TMA
 }
 
@@ -386,21 +362,18 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
   uint8_t* out_stage = stages + p.stages * STAGE_BYTES;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank4 = cluster_ctarank();
-  const uint32_t rank = rank4 & 1u;                      // within the pair
-  const uint32_t leader = rank4 & ~1u;                   // the pair's even CTA
-  const int pair = static_cast<int>(rank4 >> 1);         // within the cluster
+  const uint32_t rank = cluster_ctarank();
   const int cid = static_cast<int>(cluster_id_x());
   const int ncl = static_cast<int>(num_clusters_x());
   const Work work = {s_off, s_large, s_small, s_size, s_list, (p.F + BF - 1) / BF};
-  const uint16_t pair_mask = static_cast<uint16_t>(0x3u << leader);
+  constexpr uint16_t kBoth = 0x3;
 
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&maps.a1);
     tma_prefetch_desc(&maps.a2);
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&S.full[s], 1);
-      mbar_init(&S.empty[s], 2);
+      mbar_init(&S.empty[s], 1);
       mbar_init(&S.tail_full[s], 1);
       mbar_init(&S.tail_ready[s], 1);
     }
@@ -431,11 +404,11 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
         if (o1 < o0 || (e == 0 && o0 != 0) || (e == p.E - 1 && o1 > p.M)) bad = true;
         const int cnt = o1 - o0;
         if (cnt > p.max_n) {
-          // pairs of about equal row tiles
-          const int twos = (cnt + 2 * p.max_n - 1) / (2 * p.max_n);
-          large = twos * work.f_tiles;
-          s_size[e] = static_cast<uint16_t>(((cnt + 2 * twos - 1) / (2 * twos) + 31) & ~31);
-        } else if (cnt > 0) small = (work.f_tiles + 1) >> 1;
+          // row tiles of about equal size
+          const int tiles = (cnt + p.max_n - 1) / p.max_n;
+          large = tiles * work.f_tiles;
+          s_size[e] = static_cast<uint16_t>(((cnt + tiles - 1) / tiles + 31) & ~31);
+        } else if (cnt > 0) small = work.f_tiles;
       }
       int il = large, is = small;
 #pragma unroll
@@ -467,9 +440,9 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
     __syncthreads();
     const int t = cid + static_cast<int>(threadIdx.x) * ncl;
     if (threadIdx.x < kListed && t < S.total_tiles) {
-      const Tile tl = decode<MODE>(t, pair, work, p);
+      const Tile tl = decode<MODE>(t, work, p);
       s_list[threadIdx.x] = {tl.row0, static_cast<uint16_t>(tl.rows), static_cast<uint16_t>(tl.f0 / BF),
-                             static_cast<uint16_t>(tl.e), static_cast<uint16_t>(tl.by_rows)};
+                             static_cast<uint16_t>(tl.e), 0};
     }
   }
   // both CTAs' barriers exist and TMEM is allocated before any cross-CTA traffic
@@ -483,7 +456,7 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
   const uint64_t budget = p.budget_ns;
   constexpr uint64_t kDrainBudget = 200000000ull;
   auto fail = [&]() {
-    for (int c = 0; c < 4; ++c)
+    for (int c = 0; c < 2; ++c)
       st_shared_cluster(mapa_shared(smem_u32(&S.abort_flag), c), 1u);
     set_status(p.status, MINITE_ERR_TIMEOUT);
   };
@@ -505,40 +478,32 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
     // copy's operands are warp-uniform. Even so each copy costs its warp about
     // 180 cycles and a block as much again for its barriers, 520 in all where
     // the tensor cores take 512; so two warps take the blocks in turn.
-    const uint16_t both = rank == 0 ? 0x5 : 0xA;   // the CTAs of this rank of both pairs
-    const uint32_t leader_full0 = mapa_shared(smem_u32(&S.full[0]), leader);
+    const uint32_t leader_full0 = mapa_shared(smem_u32(&S.full[0]), 0);
     uint32_t armed_mask = 0, armed_parity = 0;
     int stage = 0, turn = 0;
     uint32_t phase = 0;
     bool ok = true;
     for (int t = cid, i = 0; t < total && ok; t += ncl, ++i) {
-      const Tile tl = unit<MODE>(t, i, pair, work, p);
+      const Tile tl = unit<MODE>(t, i, work, p);
       const int kt_n = (tl.len + BK - 1) / BK;
       const int half = tl.n / 2;
       const int f0 = tl.f0 + 128 * static_cast<int>(rank);
-      // Features: 128 of its own, or 64 from each pair to both. Rows: its half
-      // of them in a main box and a second one, both its own, or one from each
-      // pair to both. Boxes hold 2^i 16 rows (wgrad: 64), the main one at least
-      // half of them: rows that nobody needs cost traffic from L2.
+      // Half of the tile's rows come in a main box and, if need be, a second one.
+      // Boxes hold 2^i 16 rows (wgrad: 64), the main one at least half of them: rows
+      // that nobody needs cost traffic from L2.
       int box, box2;   // index of the main box and of the second, -1 if there is none
       if constexpr (B_MN) {
         box = 0;
         box2 = half > 64 ? 0 : -1;
-      } else if (tl.by_rows && half == 128) {
-        box = 3;
-        box2 = -1;
       } else {
-        box = 28 - __clz((half / 2 - 1) | 15);
+        box = 27 - __clz(half);
         box2 = half > 16 << box ? 28 - __clz((half - (16 << box) - 1) | 15) : -1;
       }
       const int main_rows = (B_MN ? 64 : 16) << box;
       const int b0 = (B_MN ? tl.i0 : tl.row0) + half * static_cast<int>(rank);
       const uint32_t bytes =
           A_BYTES + 128 * (main_rows + (box2 >= 0 ? (B_MN ? 64 : 16) << box2 : 0));
-      const bool first_box = tl.by_rows || pair == 0, second_box = box2 >= 0 && (tl.by_rows || pair == 1);
-      const int f_box = tl.by_rows ? f0 + 64 * pair : f0;
-      const bool a_two = !tl.by_rows && p.a_two;
-      const bool b_two = B_MN && tl.by_rows && box2 >= 0 && p.b_two && b0 % 64 == 0;
+      const bool b_two = B_MN && box2 >= 0 && p.b_two && b0 % 64 == 0;
       for (int kt = 0; kt < kt_n; ++kt, turn ^= 1) {
         if (turn != which) {   // the other warp's
           armed_mask &= ~(1u << stage);
@@ -557,37 +522,33 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
         const bool tail = MODE == WGRAD && left < BK && left % 16 != 0;
         const uint32_t bar = rank != 0 && tail ? smem_u32(&S.tail_full[stage]) : leader_full0 + 8u * stage;
         const int k0 = MODE == WGRAD ? tl.row0 + kt * BK : kt * BK;
-        uint8_t* dst = sA + (tl.by_rows ? pair * BOX_BYTES : 0);
-        const CUtensorMap* am = a_two ? &maps.a2 : &maps.a1;
         if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&S.full[stage], tail ? bytes : 2 * bytes);
           else if (tail) mbar_arrive_expect_tx(&S.tail_full[stage], bytes);
           if constexpr (MODE == FORWARD) {
-            tma_load_pair<3>(dst, am, bar, tl.by_rows, both, k0, f_box, tl.e);
-          } else if constexpr (MODE == DGRAD) {
-            if (a_two) tma_load_pair<4>(dst, am, bar, false, both, 0, k0, f_box / 64, tl.e);
-            else tma_load_pair<3>(dst, am, bar, tl.by_rows, both, f_box, k0, tl.e);
-          } else {
-            if (a_two) tma_load_pair<3>(dst, am, bar, false, both, 0, k0, f_box / 64);
-            else tma_load_pair<2>(dst, am, bar, tl.by_rows, both, f_box, k0);
-          }
-          if (A_MN && !tl.by_rows && !a_two) {   // features that do not come in whole boxes
-            if constexpr (MODE == DGRAD)
-              tma_load_pair<3>(sA + BOX_BYTES, am, bar, false, both, f_box + 64, k0, tl.e);
-            else tma_load_pair<2>(sA + BOX_BYTES, am, bar, false, both, f_box + 64, k0);
+            tma_load_pair<3>(sA, &maps.a2, bar, k0, f0, tl.e);
+          } else if (p.a_two) {
+            if constexpr (MODE == DGRAD) tma_load_pair<4>(sA, &maps.a2, bar, 0, k0, f0 / 64, tl.e);
+            else tma_load_pair<3>(sA, &maps.a2, bar, 0, k0, f0 / 64);
+          } else {   // features that do not come in whole boxes
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              if constexpr (MODE == DGRAD)
+                tma_load_pair<3>(sA + j * BOX_BYTES, &maps.a1, bar, f0 + 64 * j, k0, tl.e);
+              else tma_load_pair<2>(sA + j * BOX_BYTES, &maps.a1, bar, f0 + 64 * j, k0);
+            }
           }
           const uint32_t at2 = main_rows * 128;
           if constexpr (B_MN) {
             if (b_two) {
-              tma_load_pair<3>(sB, &maps.b[1], bar, false, both, 0, k0, b0 / 64);
+              tma_load_pair<3>(sB, &maps.b[1], bar, 0, k0, b0 / 64);
             } else {
-              if (first_box) tma_load_pair<2>(sB, &maps.b[0], bar, !tl.by_rows, both, b0, k0);
-              if (second_box) tma_load_pair<2>(sB + at2, &maps.b[0], bar, !tl.by_rows, both, b0 + 64, k0);
+              tma_load_pair<2>(sB, &maps.b[0], bar, b0, k0);
+              if (box2 >= 0) tma_load_pair<2>(sB + at2, &maps.b[0], bar, b0 + 64, k0);
             }
           } else {
-            if (first_box) tma_load_pair<2>(sB, &maps.b[box], bar, !tl.by_rows, both, k0, b0);
-            if (second_box)
-              tma_load_pair<2>(sB + at2, &maps.b[box2], bar, !tl.by_rows, both, k0, b0 + main_rows);
+            tma_load_pair<2>(sB, &maps.b[box], bar, k0, b0);
+            if (box2 >= 0) tma_load_pair<2>(sB + at2, &maps.b[box2], bar, k0, b0 + main_rows);
           }
         }
         __syncwarp();
@@ -626,7 +587,7 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
     uint32_t phase = 0, acc_phase = 0, tail_parity = 0;
     bool ok = true, issued = false;
     for (int t = cid, i = 0; t < total && ok; t += ncl, ++i) {
-      const Tile tl = unit<MODE>(t, i, pair, work, p);
+      const Tile tl = unit<MODE>(t, i, work, p);
       const uint32_t idesc = idesc_base<MODE>() | (static_cast<uint32_t>(tl.n >> 3) << 17);
       int in_chunk = 0;
       for (int left = tl.len; left > 0; left -= BK) {
@@ -651,8 +612,8 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
             if (s < ks)
               mma_bf16_pair(acc, adesc0 + soff + a_step * s, bdesc0 + soff + b_step * s, idesc,
                             (in_chunk | s) != 0);
-          tc_commit_pair_mc(&S.empty[stage], 0xF);
-          if (last) tc_commit_pair_mc(&S.acc_full[buf], pair_mask);
+          tc_commit_pair_mc(&S.empty[stage], kBoth);
+          if (last) tc_commit_pair_mc(&S.acc_full[buf], kBoth);
         }
         __syncwarp();
         issued = true;
@@ -668,7 +629,7 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
     if (!ok && lane == 0) fail();
     if (issued) {
       // all MMAs complete before TMEM is freed
-      if (elect_one()) tc_commit_pair_mc(&S.drain, static_cast<uint16_t>(1u << leader));
+      if (elect_one()) tc_commit_pair_mc(&S.drain, 0x1);
       __syncwarp();
       volatile int no_abort = 0;
       mbar_wait(&S.drain, 0, kDrainBudget, &no_abort);
@@ -676,12 +637,12 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
   } else if (warp == 1) {
     // ------------------------------------------------------------ tail rows of the odd CTA
     if constexpr (MODE == WGRAD) {
-      const uint32_t leader_ready0 = mapa_shared(smem_u32(&S.tail_ready[0]), leader);
+      const uint32_t leader_ready0 = mapa_shared(smem_u32(&S.tail_ready[0]), 0);
       int stage = 0;
       uint32_t tail_parity = 0;
       bool ok = true;
       for (int t = cid, i = 0; t < total && ok; t += ncl, ++i) {
-        const Tile tl = unit<MODE>(t, i, pair, work, p);
+        const Tile tl = unit<MODE>(t, i, work, p);
         const int kt_n = (tl.len + BK - 1) / BK;
         if (kt_n == 0) continue;
         stage = (stage + kt_n - 1) % p.stages;   // the sum's last stage
@@ -699,14 +660,14 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    const uint32_t leader_acc_empty0 = mapa_shared(smem_u32(&S.acc_empty[0]), leader);
+    const uint32_t leader_acc_empty0 = mapa_shared(smem_u32(&S.acc_empty[0]), 0);
     const int quarter = warp & 3;
     const int c0 = ((warp - EPI_WARP0) >> 2) * EPI_COLS;   // this warp's rows of a tile
     int buf = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
     for (int t = cid, i = 0; t < total && ok; t += ncl, ++i) {
-      const Tile tl = unit<MODE>(t, i, pair, work, p);
+      const Tile tl = unit<MODE>(t, i, work, p);
       const int chunks = ((tl.len + BK - 1) / BK + p.chunk - 1) / p.chunk;
       if (chunks == 0 && p.accumulate) continue;
       const int rows = tl.rows - c0;
@@ -873,31 +834,26 @@ int launch_as(const Maps& maps, Params& p, cudaStream_t s) {
   p.stages = static_cast<int>((kMaxSmem - rest) / STAGE_BYTES);
   if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
   const size_t smem = rest + static_cast<size_t>(p.stages) * STAGE_BYTES;
-  int clusters = resident_clusters<10 + 2 * MODE + F32>(grouped_bf16_kernel<MODE, F32>, 4, NUM_THREADS, smem);
+  int clusters = resident_pairs<10 + 2 * MODE + F32>(grouped_bf16_kernel<MODE, F32>, NUM_THREADS, smem);
   if (clusters <= 0) return MINITE_ERR_CUDA;
-  const int64_t f_tiles = (p.F + BF - 1) / BF, f_groups = (f_tiles + 1) / 2;
-  // units of work with tiles of n rows (forward and dgrad: if all experts had as many rows)
+  const int64_t f_tiles = (p.F + BF - 1) / BF;
+  // tiles of n rows (forward and dgrad: if all experts had as many rows)
   auto units = [&](int64_t n) -> int64_t {
-    if (MODE == WGRAD) {
-      const int64_t i_tiles = (p.K + n - 1) / n;
-      return p.E * (p.by_rows ? (i_tiles + 1) / 2 * f_tiles : i_tiles * f_groups);
-    }
+    if (MODE == WGRAD) return p.E * ((p.K + n - 1) / n) * f_tiles;
     const int64_t experts = p.E < p.M ? p.E : p.M;
     const int64_t rows = (p.M + experts - 1) / experts;
-    return experts * (rows > n ? (rows + 2 * n - 1) / (2 * n) * f_tiles : f_groups);
+    return experts * ((rows + n - 1) / n) * f_tiles;
   };
-  // tiles of 256 rows, narrower ones where those would leave most clusters idle
-  p.by_rows = f_tiles % 2 != 0;
+  // tiles of 256 rows, narrower ones where those would leave most pairs idle
   p.max_n = MAX_N;
   while (p.max_n > 64 && units(p.max_n) * 2 <= clusters) p.max_n /= 2;
-  // at most (forward and dgrad): every expert's last unit may be nearly empty
-  const int64_t most = MODE == WGRAD
-                           ? units(p.max_n)
-                           : (p.M / (2 * p.max_n) + (p.E < p.M ? p.E : p.M)) * f_tiles;
+  // at most (forward and dgrad): every expert's last tile may be nearly empty
+  const int64_t most =
+      MODE == WGRAD ? units(p.max_n) : (p.M / p.max_n + (p.E < p.M ? p.E : p.M)) * f_tiles;
   if (most >= (int64_t(1) << 30)) return MINITE_ERR_UNSUPPORTED_SHAPE;
   p.units = static_cast<int>(most);
   if (most < clusters) clusters = static_cast<int>(most);
-  if (launch_clusters_pdl(grouped_bf16_kernel<MODE, F32>, clusters, 4, NUM_THREADS, smem, s, maps, p) !=
+  if (launch_pair_pdl(grouped_bf16_kernel<MODE, F32>, clusters, NUM_THREADS, smem, s, maps, p) !=
       cudaSuccess)
     return MINITE_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MINITE_OK : MINITE_ERR_CUDA;
@@ -943,9 +899,7 @@ extern "C" int minite_grouped_gemm_bf16(const void* a, int64_t a_stride, const v
   const cuuint64_t un = N, uk = K, ue = E, um = M_total, us = a_stride;
   bool ok = true;
   if (nk) {
-    p.a_two = 1;
-    ok = make_map(&maps.a1, w, 3, {uk, un, ue}, {uk, un * uk}, 64) &&
-         make_map(&maps.a2, w, 3, {uk, un, ue}, {uk, un * uk}, 128);
+    ok = make_map(&maps.a2, w, 3, {uk, un, ue}, {uk, un * uk}, 128);
   } else {
     p.a_two = N % 64 == 0;   // else a box of two could reach past the last row's end
     ok = make_map(&maps.a1, w, 3, {un, uk, ue}, {un, un * uk}, 64) &&

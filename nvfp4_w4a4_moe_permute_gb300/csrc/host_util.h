@@ -48,51 +48,46 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-// Clusters of `size` CTAs of `kernel` that can be resident at once on the
-// current device (queried once per device and Tag; kernels of one type share a
-// type, so a tag names one kernel and launch shape).
+// Clusters of two CTAs of `kernel` that can be resident at once on the current
+// device (queried once per device and Tag; kernels of one type share a type, so
+// a tag names one kernel and launch shape).
 template <int Tag, typename Kernel>
-inline int resident_clusters(Kernel kernel, int size, int threads, size_t smem) {
+inline int resident_pairs(Kernel kernel, int threads, size_t smem) {
   static std::atomic<int> cache[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   int v = cache[dev].load();
   if (v > 0) return v;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(size * (num_sms() / size)));
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(num_sms() / 2));
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+  attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) return 0;
-  if (n > num_sms() / size) n = num_sms() / size;
+  if (n > num_sms() / 2) n = num_sms() / 2;
   cache[dev].store(n);
   return n;
 }
 
-template <int Tag, typename Kernel>
-inline int resident_pairs(Kernel kernel, int threads, size_t smem) {
-  return resident_clusters<Tag>(kernel, 2, threads, smem);
-}
-
-// Launch `clusters` clusters of `size` CTAs with programmatic stream serialization.
+// Launch `pairs` clusters of two CTAs with programmatic stream serialization.
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_clusters_pdl(void (*kernel)(KArgs...), int clusters, int size, int threads,
-                                       size_t smem, cudaStream_t s, Args... args) {
+inline cudaError_t launch_pair_pdl(void (*kernel)(KArgs...), int pairs, int threads, size_t smem,
+                                   cudaStream_t s, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(size * clusters));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+  attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -100,12 +95,6 @@ inline cudaError_t launch_clusters_pdl(void (*kernel)(KArgs...), int clusters, i
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
-}
-
-template <typename... KArgs, typename... Args>
-inline cudaError_t launch_pair_pdl(void (*kernel)(KArgs...), int pairs, int threads, size_t smem,
-                                   cudaStream_t s, Args... args) {
-  return launch_clusters_pdl(kernel, pairs, 2, threads, smem, s, args...);
 }
 
 }  // namespace minite
