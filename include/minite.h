@@ -19,6 +19,10 @@
  *  - Pointers named *device* are CUDA device pointers owned by the caller.
  *    The library allocates no memory and keeps no pointer after a call
  *    returns. Buffers must not overlap unless stated.
+ *  - A call launches on the device that is current: every device pointer has
+ *    to be memory of that device, and `stream` a stream of it. The library
+ *    does not check this (the Python binding does); no load of it is a
+ *    multicast one.
  *  - Every call is asynchronous on `stream` (0 = legacy default stream) and
  *    never synchronizes the host. Host-detectable errors (null pointers, bad
  *    shapes, bad alignment) are returned before anything is enqueued.

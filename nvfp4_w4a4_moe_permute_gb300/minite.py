@@ -117,17 +117,32 @@ def load(path: str | None = None):
     return lib
 
 
+def _current_device():
+    """Index of the device that kernels are launched on."""
+    return torch._C._cuda_getDevice()
+
+
+def _elsewhere(what, index, dev):
+    return MiniteError(f"expected a CUDA {what} on cuda:{dev}, the current device, got one on "
+                       f"{'the CPU' if index < 0 else f'cuda:{index}'}")
+
+
 def _p(t):
     if t is None:
         return None
     if not t.is_cuda:
         raise MiniteError("expected a CUDA tensor")
+    if t.get_device() != _current_device():
+        raise _elsewhere("tensor", t.get_device(), _current_device())
     return ctypes.c_void_p(t.data_ptr())
 
 
 def _s(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    elif stream.device_index != _current_device():
+        raise _elsewhere("stream", stream.device_index, _current_device())
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _check(rc: int, name: str):
@@ -371,20 +386,33 @@ def _dtype(t, name):
     return d
 
 
-def _ptr(t):
-    """Device address of a tensor, None for None."""
+def _device(t):
+    """Index of the device of a call's first operand: it has to be the current one,
+    where the kernel is launched, and every other operand has to be there too."""
+    d = t.get_device()
+    if d < 0:
+        raise MiniteError("expected a CUDA tensor")
+    if d != _current_device():
+        raise _elsewhere("tensor", d, _current_device())
+    return d
+
+
+def _ptr(t, dev):
+    """Address of a tensor on this device, None for None."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise MiniteError("expected a CUDA tensor")
+    if t.get_device() != dev:
+        raise _elsewhere("tensor", t.get_device(), dev)
     return t.data_ptr()
 
 
-def _raw(stream, t):
-    """The stream's handle: t's device's current stream when none is given."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+def _raw(stream, dev):
+    """The stream's handle: the device's current stream when none is given."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
+        raise _elsewhere("stream", stream.device_index, dev)
+    return stream.cuda_stream
 
 
 def _rows(t, name):
@@ -396,10 +424,10 @@ def _rows(t, name):
     return rs if n > 1 else (c + 7) // 8 * 8
 
 
-def _offsets(t, E, name):
+def _offsets(t, E, name, dev):
     if t.dtype is not torch.int32 or t.shape != (E + 1,) or not t.is_contiguous():
         raise MiniteError(f"{name}: expert_offsets is int32 [E + 1], contiguous")
-    return _ptr(t)
+    return _ptr(t, dev)
 
 
 def minite_grouped_gemm_bf16(a, w, expert_offsets, out, w_layout=W_NK, status=None, stream=None):
@@ -413,10 +441,11 @@ def minite_grouped_gemm_bf16(a, w, expert_offsets, out, w_layout=W_NK, status=No
     M, Ka = a.shape
     if Ka != K or out.shape != (M, N):
         raise MiniteError(f"{name}: shapes of a, w and out do not match")
-    rc = load().minite_grouped_gemm_bf16(_ptr(a), _rows(a, name), _ptr(w), w_layout,
-                                         _offsets(expert_offsets, E, name), M, N, K, E, _ptr(out),
-                                         _rows(out, name), _dtype(out, name), _ptr(status),
-                                         _raw(stream, a))
+    d = _device(a)
+    rc = load().minite_grouped_gemm_bf16(a.data_ptr(), _rows(a, name), _ptr(w, d), w_layout,
+                                         _offsets(expert_offsets, E, name, d), M, N, K, E,
+                                         _ptr(out, d), _rows(out, name), _dtype(out, name),
+                                         _ptr(status, d), _raw(stream, d))
     if rc:
         _check(rc, name)
 
@@ -430,10 +459,11 @@ def minite_grouped_wgrad_bf16(a, b, expert_offsets, out, accumulate=False, statu
     M = a.shape[0]
     if a.shape != (M, Na) or b.shape != (M, Nb):
         raise MiniteError(f"{name}: shapes of a, b and out do not match")
-    rc = load().minite_grouped_wgrad_bf16(_ptr(a), _rows(a, name), _ptr(b), _rows(b, name),
-                                          _offsets(expert_offsets, E, name), M, Na, Nb, E, _ptr(out),
-                                          _dtype(out, name), 1 if accumulate else 0, _ptr(status),
-                                          _raw(stream, out))
+    d = _device(a)
+    rc = load().minite_grouped_wgrad_bf16(a.data_ptr(), _rows(a, name), _ptr(b, d), _rows(b, name),
+                                          _offsets(expert_offsets, E, name, d), M, Na, Nb, E,
+                                          _ptr(out, d), _dtype(out, name), 1 if accumulate else 0,
+                                          _ptr(status, d), _raw(stream, d))
     if rc:
         _check(rc, name)
 
@@ -447,13 +477,13 @@ def _targets(targets, N, name):
     return 1 if targets.dtype is torch.int64 else 0
 
 
-def _f32(t, shape, name, what):
-    """Device address of an FP32 tensor of this shape, None for None."""
+def _f32(t, shape, name, what, dev):
+    """Address of an FP32 tensor of this shape on this device, None for None."""
     if t is None:
         return None
     if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous():
         raise MiniteError(f"{name}: {what} is float32 {list(shape)}, contiguous")
-    return _ptr(t)
+    return _ptr(t, dev)
 
 
 def minite_token_logprobs(logits, targets, logprob, entropy=None, stats=None, temperature=1.0,
@@ -468,13 +498,14 @@ def minite_token_logprobs(logits, targets, logprob, entropy=None, stats=None, te
         k = alt_ids.shape[1]
         if alt_ids.dtype is not torch.int32 or alt_ids.shape[0] != N or not alt_ids.is_contiguous():
             raise MiniteError(f"{name}: alt_ids is int32 [N, k], contiguous")
-    rc = load().minite_token_logprobs(_ptr(logits), _dtype(logits, name), N, V, ld,
-                                      _ptr(targets), _targets(targets, N, name), temperature,
-                                      _f32(logprob, (N,), name, "logprob"),
-                                      _f32(entropy, (N,), name, "entropy"),
-                                      _f32(stats, (N, 2), name, "stats"), k, _ptr(alt_ids),
-                                      _f32(alt_logprobs, (N, k), name, "alt_logprobs"),
-                                      _ptr(status), _raw(stream, logits))
+    d = _device(logits)
+    rc = load().minite_token_logprobs(logits.data_ptr(), _dtype(logits, name), N, V, ld,
+                                      _ptr(targets, d), _targets(targets, N, name), temperature,
+                                      _f32(logprob, (N,), name, "logprob", d),
+                                      _f32(entropy, (N,), name, "entropy", d),
+                                      _f32(stats, (N, 2), name, "stats", d), k, _ptr(alt_ids, d),
+                                      _f32(alt_logprobs, (N, k), name, "alt_logprobs", d),
+                                      _ptr(status, d), _raw(stream, d))
     if rc:
         _check(rc, name)
 
@@ -487,11 +518,13 @@ def minite_token_logprobs_backward(logits, targets, stats, entropy, grad_logprob
     N, V = logits.shape
     if dlogits.dtype is not logits.dtype or dlogits.shape != logits.shape or stats is None:
         raise MiniteError(f"{name}: needs the forward's stats, and dlogits of the type and shape of logits")
+    d = _device(logits)
     rc = load().minite_token_logprobs_backward(
-        _ptr(logits), _dtype(logits, name), N, V, ld, _ptr(targets), _targets(targets, N, name),
-        temperature, _f32(stats, (N, 2), name, "stats"), _f32(entropy, (N,), name, "entropy"),
-        _f32(grad_logprob, (N,), name, "grad_logprob"), _f32(grad_entropy, (N,), name, "grad_entropy"),
-        _ptr(dlogits), _rows(dlogits, name), _ptr(status), _raw(stream, logits))
+        logits.data_ptr(), _dtype(logits, name), N, V, ld, _ptr(targets, d), _targets(targets, N, name),
+        temperature, _f32(stats, (N, 2), name, "stats", d), _f32(entropy, (N,), name, "entropy", d),
+        _f32(grad_logprob, (N,), name, "grad_logprob", d),
+        _f32(grad_entropy, (N,), name, "grad_entropy", d),
+        _ptr(dlogits, d), _rows(dlogits, name), _ptr(status, d), _raw(stream, d))
     if rc:
         _check(rc, name)
 
@@ -504,12 +537,13 @@ ADAMW_TENSOR = np.dtype([("param", "u8"), ("grad", "u8"), ("exp_avg", "u8"), ("e
 
 def minite_adamw_step(tensors, param_dtype, grad_dtype, state_bits, lr, beta1, beta2, eps,
                       weight_decay, step, grad_scale=None, stream=None):
-    """tensors: numpy array of ADAMW_TENSOR on the host, one descriptor a tensor."""
+    """tensors: numpy array of ADAMW_TENSOR on the host, one descriptor a tensor, with
+    addresses on the current device."""
     if tensors.dtype != ADAMW_TENSOR or not tensors.flags.c_contiguous:
         raise MiniteError("minite_adamw_step: tensors is a contiguous array of ADAMW_TENSOR")
     rc = load().minite_adamw_step(tensors.ctypes.data, len(tensors), param_dtype, grad_dtype,
                                   state_bits, lr, beta1, beta2, eps, weight_decay, step,
-                                  _ptr(grad_scale), _s(stream))
+                                  _p(grad_scale), _s(stream))
     _check(rc, "minite_adamw_step")
 
 
@@ -612,6 +646,7 @@ def token_logprobs(logits, targets=None, temperature=1.0, alternatives=0, status
     name = "token_logprobs"
     ld = _rows(logits, name)
     N, V = logits.shape
+    d = _device(logits)
     f32 = torch.float32
     entropy, stats = _empty((N,), f32, logits, stream), _empty((N, 2), f32, logits, stream)
     logprob = alt_ids = alt_logprobs = None
@@ -621,11 +656,11 @@ def token_logprobs(logits, targets=None, temperature=1.0, alternatives=0, status
         alt_ids = _empty((N, alternatives), torch.int32, logits, stream)
         alt_logprobs = _empty((N, alternatives), f32, logits, stream)
     rc = load().minite_token_logprobs(
-        _ptr(logits), _dtype(logits, name), N, V, ld, _ptr(targets), _targets(targets, N, name),
+        logits.data_ptr(), _dtype(logits, name), N, V, ld, _ptr(targets, d), _targets(targets, N, name),
         temperature, None if logprob is None else logprob.data_ptr(),
         entropy.data_ptr(), stats.data_ptr(), alternatives,
         alt_ids.data_ptr() if alternatives else None,
-        alt_logprobs.data_ptr() if alternatives else None, _ptr(status), _raw(stream, logits))
+        alt_logprobs.data_ptr() if alternatives else None, _ptr(status, d), _raw(stream, d))
     if rc:
         _check(rc, "minite_token_logprobs")
     return {"logprob": logprob, "entropy": entropy, "stats": stats, "alt_ids": alt_ids,
@@ -699,17 +734,18 @@ class AdamW:
     def step(self, grads, grad_scale=None, lr=None, stream=None):
         """One step with grads[i] (bf16 or fp32, all one type) for tensor i, each
         times the device scalar ``grad_scale``."""
+        d = _device(self.exp_avg)
         if [g.numel() for g in grads] != self._numel or len({g.dtype for g in grads}) != 1 or \
-                not all([g.is_contiguous() and g.is_cuda for g in grads]):
-            raise MiniteError("AdamW.step: gradients are contiguous CUDA tensors of one type, one a "
-                              "parameter and of its size")
+                not all([g.is_contiguous() and g.get_device() == d for g in grads]):
+            raise MiniteError("AdamW.step: gradients are contiguous tensors of one type on the parameters' "
+                              "device, one a parameter and of its size")
         if grad_scale is not None and (grad_scale.dtype is not torch.float32 or grad_scale.numel() != 1):
             raise MiniteError("AdamW.step: grad_scale is one float32")
         self._grads[:] = [g.data_ptr() for g in grads]
         rc = load().minite_adamw_step(
             self._address, len(self.params), self._param_dtype, _dtype(grads[0], "AdamW.step"),
             self.state_bits, self.lr if lr is None else lr, *self.betas, self.eps, self.weight_decay,
-            self.step_count + 1, _ptr(grad_scale), _raw(stream, self.exp_avg))
+            self.step_count + 1, _ptr(grad_scale, d), _raw(stream, d))
         if rc:
             _check(rc, "minite_adamw_step")
         self.step_count += 1
