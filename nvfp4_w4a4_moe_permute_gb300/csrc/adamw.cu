@@ -26,7 +26,6 @@
 // Up to 440 tensors' pointers travel as kernel parameters (48 in a small set),
 // so that a step is one launch and nothing is copied to the device first.
 #include <cmath>
-#include <mutex>
 #include <type_traits>
 
 #include "common.cuh"
@@ -483,12 +482,8 @@ cudaError_t launch_batch(const minite_adamw_tensor* t, int64_t count, const Hype
   if (chunks == 0) return cudaSuccess;
   constexpr size_t kSmem = EIGHT ? kDepth * sizeof(Stage<P, G>) : 0;
   if constexpr (kSmem + 1024 > 48 * 1024) {   // with the static part
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-      attr_err = cudaFuncSetAttribute(adamw_kernel<P, G, EIGHT, CAP>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem));
-    });
+    static std::atomic<uint64_t> devices{0};
+    const cudaError_t attr_err = allow_smem(devices, adamw_kernel<P, G, EIGHT, CAP>, kSmem);
     if (attr_err != cudaSuccess) return attr_err;
   }
   return launch_pdl(adamw_kernel<P, G, EIGHT, CAP>, dim3(static_cast<unsigned>(chunks)),

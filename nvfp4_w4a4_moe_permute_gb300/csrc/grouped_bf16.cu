@@ -54,8 +54,6 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include <mutex>
-
 #include "common.cuh"
 #include "host_util.h"
 
@@ -816,13 +814,8 @@ bool make_out_map(CUtensorMap* m, void* out, cuuint64_t E, cuuint64_t rows, cuui
 
 template <int MODE, bool F32>
 int launch_as(const Maps& maps, Params& p, cudaStream_t s) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(grouped_bf16_kernel<MODE, F32>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(kMaxSmem));
-  });
+  static std::atomic<uint64_t> devices{0};
+  const cudaError_t attr_err = allow_smem(devices, grouped_bf16_kernel<MODE, F32>, kMaxSmem);
   if (attr_err != cudaSuccess) return MINITE_ERR_CUDA;
   p.chunk = F32 ? kChunkBlocks : 1 << 30;
   p.budget_ns = wait_budget_ns();

@@ -1778,12 +1778,8 @@ extern "C" int minite_grouped_gemm_nvfp4(const uint8_t* a_codes, const uint8_t* 
   const int64_t n_tiles = (N + BN - 1) / BN;
   if (variant == 1) {
     const size_t smem = 1024 + STAGES * STAGE_BYTES + sizeof(Smem) + 2 * (E + 1) * sizeof(int32_t);
-    static std::once_flag attr_once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(attr_once, [] {
-      attr_err = cudaFuncSetAttribute(grouped_gemm_kernel,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
-    });
+    static std::atomic<uint64_t> devices{0};
+    const cudaError_t attr_err = allow_smem(devices, grouped_gemm_kernel, 232448);
     if (attr_err != cudaSuccess || smem > 232448) return MINITE_ERR_CUDA;
     // one CTA per SM, never more CTAs than the largest possible tile count
     const int64_t max_tiles = (M_total / BM + E) * n_tiles;
@@ -1791,12 +1787,8 @@ extern "C" int minite_grouped_gemm_nvfp4(const uint8_t* a_codes, const uint8_t* 
     if (max_tiles < grid) grid = static_cast<int>(max_tiles);
     grouped_gemm_kernel<<<grid, NUM_THREADS, smem, s>>>(ta, tb, p);
   } else if (variant == 5) {
-    static std::once_flag attr_once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(attr_once, [] {
-      attr_err = cudaFuncSetAttribute(grouped_gemm_dc_kernel<false>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
-    });
+    static std::atomic<uint64_t> devices{0};
+    const cudaError_t attr_err = allow_smem(devices, grouped_gemm_dc_kernel<false>, 232448);
     if (attr_err != cudaSuccess) return MINITE_ERR_CUDA;
     const int64_t max_tiles = (M_total / BM + E) * n_tiles;
     int grid = num_sms();
@@ -1805,12 +1797,8 @@ extern "C" int minite_grouped_gemm_nvfp4(const uint8_t* a_codes, const uint8_t* 
                    p) != cudaSuccess)
       return MINITE_ERR_CUDA;
   } else if (variant == 6) {
-    static std::once_flag attr_once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(attr_once, [] {
-      attr_err = cudaFuncSetAttribute(grouped_gemm_pair_deep_kernel<false>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
-    });
+    static std::atomic<uint64_t> devices{0};
+    const cudaError_t attr_err = allow_smem(devices, grouped_gemm_pair_deep_kernel<false>, 232448);
     if (attr_err != cudaSuccess) return MINITE_ERR_CUDA;
     // one CTA per SM in clusters of two: as many pairs as can be resident at
     // once (a GPC with an odd SM count leaves one SM out), never more pairs
@@ -1854,12 +1842,8 @@ extern "C" int minite_gate_up_swiglu_quant_nvfp4(
                       3 * (E + 1) * sizeof(int32_t) + 16 + kLut24Entries * sizeof(float) +
                       2 * 512 * sizeof(float);
   if (smem > 232448) return MINITE_ERR_UNSUPPORTED_SHAPE;
-  static std::once_flag attr_once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(attr_once, [] {
-    attr_err = cudaFuncSetAttribute(grouped_gemm_pair_deep_kernel<true>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
-  });
+  static std::atomic<uint64_t> devices{0};
+  const cudaError_t attr_err = allow_smem(devices, grouped_gemm_pair_deep_kernel<true>, 232448);
   if (attr_err != cudaSuccess) return MINITE_ERR_CUDA;
   // every m-block's I/128 tiles run at once on I/128 clusters (consecutive
   // cluster ids): launch a multiple of I/128 clusters, all resident together
@@ -1945,12 +1929,8 @@ extern "C" int minite_grouped_gemm_wgrad_nvfp4(const uint8_t* a_codes, const uin
   p.E = E;
   p.out_fp32 = out_dtype == MINITE_OUT_FP32;
   p.budget_ns = wait_budget_ns();
-  static std::once_flag attr_once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(attr_once, [] {
-    attr_err = cudaFuncSetAttribute(grouped_gemm_dc_kernel<true>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
-  });
+  static std::atomic<uint64_t> devices{0};
+  const cudaError_t attr_err = allow_smem(devices, grouped_gemm_dc_kernel<true>, 232448);
   if (attr_err != cudaSuccess) return MINITE_ERR_CUDA;
   const int64_t max_tiles = int64_t(E) * ((M + BM - 1) / BM) * ((N + BN - 1) / BN);
   int grid = num_sms();

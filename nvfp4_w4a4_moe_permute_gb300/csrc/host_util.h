@@ -29,6 +29,23 @@ inline int permute_chunk_tokens(int k) {
   return ct < 1 ? 1 : ct;
 }
 
+// Allow `kernel` dynamic shared memory of `bytes`, once on each device (the
+// attribute belongs to one): `devices` is the call site's own, a bit a device.
+inline cudaError_t allow_smem(std::atomic<uint64_t>& devices, const void* kernel, size_t bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t(1) << dev : 0;
+  if (devices.load() & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (e == cudaSuccess) devices.fetch_or(bit);
+  return e;
+}
+template <typename... KArgs>
+inline cudaError_t allow_smem(std::atomic<uint64_t>& devices, void (*kernel)(KArgs...), size_t bytes) {
+  return allow_smem(devices, reinterpret_cast<const void*>(kernel), bytes);
+}
+
 // Launch with programmatic stream serialization: the kernel may start while
 // the previous kernel on the stream finishes; it must call pdl_wait() before
 // touching global memory (every kernel launched this way does).

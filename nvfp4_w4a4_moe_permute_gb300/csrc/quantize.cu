@@ -23,7 +23,6 @@
 //                          optionally the forward copy from the same read:
 //                          128 x 128 tiles staged through shared memory with
 //                          per-thread asynchronous copies (two buffers).
-#include <mutex>
 
 #include "common.cuh"
 #include "host_util.h"
@@ -444,13 +443,8 @@ template <bool FWD>
 static int launch_tiles(const uint16_t* x, int64_t groups, int64_t rows, int64_t cols,
                         const float* g_in, const uint32_t* amax, uint8_t* codes_k, uint8_t* sf_k,
                         uint8_t* codes_n, uint8_t* sf_n, float* g_out, cudaStream_t s) {
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(quantize_tiles_kernel<FWD>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(kDualSmem));
-  });
+  static std::atomic<uint64_t> devices{0};
+  const cudaError_t attr = allow_smem(devices, quantize_tiles_kernel<FWD>, kDualSmem);
   if (attr != cudaSuccess) return MINITE_ERR_CUDA;
   const int64_t tiles = groups * ((rows + kDR - 1) / kDR) * ((cols + kDC - 1) / kDC);
   int64_t blocks = static_cast<int64_t>(num_sms()) * 3;

@@ -36,7 +36,6 @@
 //                        quantizes channel c's four 16-token blocks and
 //                        writes 32 code bytes and 4 scale bytes, all
 //                        contiguous.
-#include <mutex>
 
 #include "common.cuh"
 #include "host_util.h"
@@ -434,13 +433,10 @@ extern "C" int minite_quantize_tokens_nvfp4(const void* x, int64_t x_rows, const
   }
   const size_t smem = 2 * kTokT * kTokPitch * sizeof(uint16_t) +
                       2 * (E + 1) * sizeof(int64_t) + (E + 1) * sizeof(int32_t);
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(tokens_quant_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(2 * kTokT * kTokPitch * sizeof(uint16_t) +
-                                                 2 * 1025 * sizeof(int64_t) + 1025 * 4));
-  });
+  static std::atomic<uint64_t> devices{0};
+  const cudaError_t attr = allow_smem(
+      devices, tokens_quant_kernel,
+      2 * kTokT * kTokPitch * sizeof(uint16_t) + 2 * 1025 * sizeof(int64_t) + 1025 * 4);
   if (attr != cudaSuccess) return MINITE_ERR_CUDA;
   const int64_t qblocks = static_cast<int64_t>(num_sms()) * kTokCtasPerSm;
   tokens_quant_kernel<<<static_cast<unsigned>(qblocks), kTokThreads, smem, s>>>(

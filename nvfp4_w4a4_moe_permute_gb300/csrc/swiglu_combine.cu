@@ -4,7 +4,6 @@
 // writes NVFP4 codes plus swizzled scales directly (miniTE report summary,
 // section "Two complementary interventions"); the combine sums each token's
 // k expert rows back into token order.
-#include <mutex>
 
 #include "common.cuh"
 #include "host_util.h"
@@ -414,14 +413,9 @@ __global__ void __launch_bounds__(bwd_threads<NCH>(), 1) swiglu_bwd_quant_kernel
 
 template <int NCH, bool KEEP>
 static cudaError_t bwd_smem_attr() {
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(swiglu_bwd_quant_kernel<NCH, KEEP>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(2 * kLutEntries * sizeof(float) + 2 * 1025 * 4));
-  });
-  return attr;
+  static std::atomic<uint64_t> devices{0};
+  return allow_smem(devices, swiglu_bwd_quant_kernel<NCH, KEEP>,
+                    2 * kLutEntries * sizeof(float) + 2 * 1025 * 4);
 }
 
 template <int NCH>
