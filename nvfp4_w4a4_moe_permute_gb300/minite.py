@@ -685,7 +685,9 @@ class AdamW:
     256 elements). ``copies``: bf16 tensors that receive the rounded parameters
     (for fp32 parameters). The states are flat buffers in which each tensor
     starts at a multiple of 256 elements (``starts``); ``state`` takes buffers
-    of this layout and a step count to continue from."""
+    of this layout and a step count to continue from. A step uses ``params``,
+    ``copies`` and the states as they are then: their storage may be replaced
+    between steps, by some of the same type and size."""
 
     BLOCK = 256
 
@@ -694,12 +696,7 @@ class AdamW:
         _need(len(params) > 0 and state_bits in (8, 32), "AdamW: needs tensors and state_bits 8 or 32")
         dev = params[0].device
         self._param_dtype = _dtype(params[0], "AdamW")
-        for i, p in enumerate(params):
-            _need(p.is_cuda and p.device == dev and p.dtype == params[0].dtype and p.is_contiguous(),
-                  f"AdamW: parameter {i} is not a contiguous {params[0].dtype} CUDA tensor")
-        _need(copies is None or (len(copies) == len(params) and all(
-            c.dtype == torch.bfloat16 and c.shape == p.shape and c.is_contiguous() and c.device == dev
-            for c, p in zip(copies, params))), "AdamW: copies are bfloat16 tensors like the parameters")
+        self._dtype = params[0].dtype
         self.params, self.copies = list(params), None if copies is None else list(copies)
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
         self.state_bits = state_bits
@@ -709,27 +706,48 @@ class AdamW:
         first = np.concatenate([[0], np.cumsum(blocks)[:-1]]).astype(np.int64)
         self.starts = (first * self.BLOCK).tolist()
         n_blocks = int(blocks.sum())
-        kinds = dict(exp_avg=(n_blocks * self.BLOCK, torch.float8_e4m3fn if state_bits == 8 else torch.float32))
-        kinds["exp_avg_sq"] = kinds["exp_avg"]
+        # each state's type, size, and elements in front of every tensor's part
+        codes = (torch.float8_e4m3fn if state_bits == 8 else torch.float32, n_blocks * self.BLOCK, first * self.BLOCK)
+        self._states = dict(exp_avg=codes, exp_avg_sq=codes)
         if state_bits == 8:
-            kinds["exp_avg_scale"] = kinds["exp_avg_sq_scale"] = (n_blocks, torch.float32)
+            self._states["exp_avg_scale"] = self._states["exp_avg_sq_scale"] = (torch.float32, n_blocks, first)
+        _need(all(p.is_cuda for p in params), "AdamW: parameters are CUDA tensors")
         self.step_count = 0 if state is None else int(state["step"])
-        for name, (n, dtype) in kinds.items():
-            t = torch.zeros(n, dtype=dtype, device=dev) if state is None else state[name]
-            _need(t.numel() == n and t.dtype == dtype and t.is_contiguous() and t.device == dev,
-                  f"AdamW: state {name} is not {dtype} [{n}]")
-            setattr(self, name, t)
+        for name, (dtype, n, _) in self._states.items():
+            setattr(self, name, torch.zeros(n, dtype=dtype, device=dev) if state is None else state[name])
         d = self._tensors = np.zeros(len(params), dtype=ADAMW_TENSOR)
         self._address, self._grads = d.ctypes.data, d["grad"]
-        d["param"] = [p.data_ptr() for p in params]
         d["n"] = sizes
-        if copies is not None:
-            d["param_bf16"] = [c.data_ptr() for c in copies]
-        for name in ("exp_avg", "exp_avg_sq"):
+        self._bind(self._kept())
+
+    def _kept(self):
+        """What a step works on besides gradients, as it lies now."""
+        t = [*self.params, self.exp_avg, self.exp_avg_sq]
+        if self.state_bits == 8:
+            t += (self.exp_avg_scale, self.exp_avg_sq_scale)
+        if self.copies is not None:
+            t += self.copies
+        return [(x.data_ptr(), x.numel(), x.dtype, x.is_contiguous()) for x in t]
+
+    def _bind(self, kept):
+        """Checks all of that and writes its addresses into the descriptors."""
+        d, dev = self._tensors, self.exp_avg.device
+        _need(len(self.params) == len(self._numel), "AdamW: a parameter was added or taken away")
+        for i, p in enumerate(self.params):
+            _need(p.is_cuda and p.device == dev and p.dtype == self._dtype and p.is_contiguous() and
+                  p.numel() == self._numel[i],
+                  f"AdamW: parameter {i} is not a contiguous {self._dtype} tensor of {self._numel[i]} elements on {dev}")
+        _need(self.copies is None or (len(self.copies) == len(self.params) and all(
+            c.dtype == torch.bfloat16 and c.shape == p.shape and c.is_contiguous() and c.device == dev
+            for c, p in zip(self.copies, self.params))), "AdamW: copies are bfloat16 tensors like the parameters")
+        for name, (dtype, n, first) in self._states.items():
             t = getattr(self, name)
-            d[name] = t.data_ptr() + first * (self.BLOCK * t.element_size())
-            if state_bits == 8:
-                d[name + "_scale"] = getattr(self, name + "_scale").data_ptr() + first * 4
+            _need(t.numel() == n and t.dtype == dtype and t.is_contiguous() and t.device == dev,
+                  f"AdamW: state {name} is not {dtype} [{n}] on {dev}")
+            d[name] = t.data_ptr() + first * t.element_size()
+        d["param"] = [p.data_ptr() for p in self.params]
+        d["param_bf16"] = 0 if self.copies is None else [c.data_ptr() for c in self.copies]
+        self._bound = kept
 
     def step(self, grads, grad_scale=None, lr=None, stream=None):
         """One step with grads[i] (bf16 or fp32, all one type) for tensor i, each
@@ -741,6 +759,9 @@ class AdamW:
                               "device, one a parameter and of its size")
         if grad_scale is not None and (grad_scale.dtype is not torch.float32 or grad_scale.numel() != 1):
             raise MiniteError("AdamW.step: grad_scale is one float32")
+        kept = self._kept()
+        if kept != self._bound:   # storage was replaced
+            self._bind(kept)
         self._grads[:] = [g.data_ptr() for g in grads]
         rc = load().minite_adamw_step(
             self._address, len(self.params), self._param_dtype, _dtype(grads[0], "AdamW.step"),
