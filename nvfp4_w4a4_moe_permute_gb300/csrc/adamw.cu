@@ -12,6 +12,17 @@
 // zero code: it takes the smallest one instead, since a v of 0 beside an m
 // that is not would divide the step by eps alone.
 //
+// Codes round to nearest where one step, together with the change of the block's
+// scale, moves a moment far enough: beta1 <= 0.9, beta2 <= 0.95. A larger beta takes
+// a moment down by much less than half a code's distance (3 to 6%) a step, and
+// rounding to nearest would give the old code back for ever: with beta2 0.99 and gradients that fall to a hundredth, sqrt(v) stayed
+// 87 to 137 times too large (5th and 95th percentile over elements, 2000 steps),
+// with beta1 0.95 and gradients that stop, parameters moved 22 times too far. Such
+// a moment's code is drawn from its two neighbours so that it is right on average,
+// by a hash of step and element, hence repeatable: 0.79 to 1.30 times, and as far
+// as with 32 bits. At the limits nearest is the closer one: 0.88 to 1.15 at beta2
+// 0.95, drawn 0.85 to 1.21.
+//
 // Every operation is rounded to nearest on its own in the order written above
 // (no contraction), so that the codes do not depend on how a compiler fuses
 // them. Where the moments lie in the usual range, two elements go through the
@@ -22,7 +33,9 @@
 // loads, 604M elements in 2.41 ms, 7.0 TB/s. 8-bit states (10 bytes an element
 // with BF16 parameters and gradients, 50 instructions): asynchronous copies three
 // reads ahead, the scales of 64 blocks read and written at once; 400M elements
-// in 0.65 ms, 6.2 TB/s (1.11 ms with plain loads and IEEE roots and quotients).
+// in 0.65 ms, 6.2 TB/s (1.11 ms with plain loads and IEEE roots and quotients), in
+// 0.87 ms where the second moment's codes are drawn, 1.04 where both are: some 15
+// instructions more for each.
 // Up to 440 tensors' pointers travel as kernel parameters (48 in a small set),
 // so that a step is one launch and nothing is copied to the device first.
 #include <cmath>
@@ -56,6 +69,8 @@ struct Hyper {
   float b1, c1, b2, c2;      // beta1, 1 - beta1, beta2, 1 - beta2
   float keep, rate, isq, eps;  // 1 - lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
   float minus_zero;          // -0
+  uint32_t key;              // of the step's draws
+  bool draw_m, draw_v;       // 8-bit states: which moment's codes are drawn
   const float* scale;        // device factor of the gradients, or null
 };
 
@@ -66,6 +81,14 @@ struct Batch {
   int32_t chunk0[CAP];       // chunks of the tensors before this one
   Tensor t[CAP];
 };
+
+// Finaliser of SplitMix64 (Steele, Lea and Flood, 2014).
+__host__ __device__ inline uint64_t split_mix(uint64_t x) {
+  uint64_t z = x + 0x9E3779B97F4A7C15ull;
+  z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+  z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+  return z ^ (z >> 31);
+}
 
 __device__ __forceinline__ uint64_t twice(float x) { return pair(x, x); }
 
@@ -216,6 +239,21 @@ __device__ __forceinline__ void store_codes(uint8_t* a, int64_t i, int64_t n, bo
   }
 }
 
+// One of the two E4M3 values around x, drawn by the upper 20 bits of `bits` so that
+// it is right on average: they are added to the part of x's fraction that the
+// format has no room for, and what is left of that part is cut off. Below 2^-6 the
+// values lie 2^-9 apart, as they do from there to 2^-5: x is moved there and back.
+__device__ __forceinline__ float drawn(float x, uint32_t bits) {
+  const float to = fabsf(x) < 0.015625f ? copysignf(0.015625f, x) : 0.0f;
+  return __uint_as_float((__float_as_uint(x + to) + (bits >> 12)) & 0xFFF00000u) - to;
+}
+// Mixed bits, the upper ones of use: multiplications by odd numbers (bits of the
+// roots of 2 and 3) and shifts, so that every bit of x reaches them.
+__device__ __forceinline__ uint32_t mixed(uint32_t x) {
+  x = (x ^ (x >> 16)) * 0x6A09E667u;
+  return (x ^ (x >> 15)) * 0xBB67AE85u;
+}
+
 // Scale of a block whose largest magnitude is a.
 __device__ __forceinline__ float block_scale_of(float a) {
   const float s = __fmul_rn(a, kInvMax);
@@ -298,7 +336,7 @@ struct Stage {
   }
 };
 
-template <typename P, typename G, bool EIGHT, int CAP>
+template <typename P, typename G, bool EIGHT, bool DRAW, int CAP>
 __global__ void __launch_bounds__(kThreads)
 adamw_kernel(const __grid_constant__ Batch<CAP> b) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -431,6 +469,15 @@ adamw_kernel(const __grid_constant__ Batch<CAP> b) {
         }
       }
     }
+    if constexpr (DRAW) {
+      const uint32_t first = static_cast<uint32_t>(i) + static_cast<uint32_t>(i >> 32) * 0x3C6EF373u;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t bits = mixed((first + j) * 0x9E3779B1u + h.key);
+        if (h.draw_m) m[j] = drawn(m[j], bits * 0xA54FF53Bu);
+        if (h.draw_v) r[j] = r[j] > 0.0f ? fmaxf(drawn(r[j], bits), kSmallest) : r[j];
+      }
+    }
     if constexpr (EIGHT) {
       // everything that the slot held has been worked on
       ask(i + kDepth * kStep, stage);
@@ -457,7 +504,7 @@ adamw_kernel(const __grid_constant__ Batch<CAP> b) {
   }
 }
 
-template <typename P, typename G, bool EIGHT, int CAP>
+template <typename P, typename G, bool EIGHT, bool DRAW, int CAP>
 cudaError_t launch_batch(const minite_adamw_tensor* t, int64_t count, const Hyper& h,
                          cudaStream_t s) {
   constexpr int64_t kChunk = chunk_elements(EIGHT);
@@ -483,15 +530,15 @@ cudaError_t launch_batch(const minite_adamw_tensor* t, int64_t count, const Hype
   constexpr size_t kSmem = EIGHT ? kDepth * sizeof(Stage<P, G>) : 0;
   if constexpr (kSmem + 1024 > 48 * 1024) {   // with the static part
     static std::atomic<uint64_t> devices{0};
-    const cudaError_t attr_err = allow_smem(devices, adamw_kernel<P, G, EIGHT, CAP>, kSmem);
+    const cudaError_t attr_err = allow_smem(devices, adamw_kernel<P, G, EIGHT, DRAW, CAP>, kSmem);
     if (attr_err != cudaSuccess) return attr_err;
   }
-  return launch_pdl(adamw_kernel<P, G, EIGHT, CAP>, dim3(static_cast<unsigned>(chunks)),
+  return launch_pdl(adamw_kernel<P, G, EIGHT, DRAW, CAP>, dim3(static_cast<unsigned>(chunks)),
                     dim3(kThreads), kSmem, s, b);
 }
 
-template <typename P, typename G, bool EIGHT>
-int step(const minite_adamw_tensor* t, int64_t n, const Hyper& h, cudaStream_t s) {
+template <typename P, typename G, bool EIGHT, bool DRAW>
+int step_as(const minite_adamw_tensor* t, int64_t n, const Hyper& h, cudaStream_t s) {
   // kernel parameters carry the tensors' pointers (4 KB or 32 KB of them)
   constexpr int kSmall = 48, kLarge = 440;
   constexpr int64_t kChunk = chunk_elements(EIGHT);
@@ -505,12 +552,20 @@ int step(const minite_adamw_tensor* t, int64_t n, const Hyper& h, cudaStream_t s
       if (c > 0 && chunks > 0x7FFFFFFF) break;
       ++c;
     }
-    const cudaError_t e = cap == kSmall ? launch_batch<P, G, EIGHT, kSmall>(t + i, c, h, s)
-                                        : launch_batch<P, G, EIGHT, kLarge>(t + i, c, h, s);
+    const cudaError_t e = cap == kSmall ? launch_batch<P, G, EIGHT, DRAW, kSmall>(t + i, c, h, s)
+                                        : launch_batch<P, G, EIGHT, DRAW, kLarge>(t + i, c, h, s);
     if (e != cudaSuccess) return MINITE_ERR_CUDA;
     i += c;
   }
   return MINITE_OK;
+}
+
+template <typename P, typename G, bool EIGHT>
+int step(const minite_adamw_tensor* t, int64_t n, const Hyper& h, cudaStream_t s) {
+  if constexpr (EIGHT) {
+    if (h.draw_m || h.draw_v) return step_as<P, G, true, true>(t, n, h, s);
+  }
+  return step_as<P, G, EIGHT, false>(t, n, h, s);
 }
 
 // Roots of every significand at the even and the odd exponents of `scale`, and
@@ -527,11 +582,7 @@ __global__ void math_test_kernel(unsigned long long* mismatches) {
     roots += (a != __fsqrt_rn(v * 0x1p96f)) + (b != __fsqrt_rn(v * 0x1p-40f));
   }
   for (uint32_t i = first; i < (1u << 30); i += stride) {
-    // SplitMix64 finaliser (Steele, Lea and Flood, 2014)
-    unsigned long long z = i + 0x9E3779B97F4A7C15ull;
-    z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
-    z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
-    z ^= z >> 31;
+    const uint64_t z = split_mix(i);
     // m in +-[2^-60, 2^60), d in [2^-27, 2^51)
     const uint32_t me = 67 + static_cast<uint32_t>((z >> 23) % 120), de = 100 + static_cast<uint32_t>((z >> 55) % 78);
     const float m = __uint_as_float(static_cast<uint32_t>(z & 0x807FFFFFu) | (me << 23));
@@ -590,6 +641,9 @@ extern "C" int minite_adamw_step(const minite_adamw_tensor* tensors, int64_t n_t
   h.isq = static_cast<float>(1.0 / std::sqrt(bc2));
   h.eps = static_cast<float>(eps);
   h.minus_zero = -0.0f;
+  h.key = static_cast<uint32_t>(split_mix(static_cast<uint64_t>(step)));
+  h.draw_m = beta1 > 0.9;
+  h.draw_v = beta2 > 0.95;
   h.scale = grad_scale;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool pf = param_dtype == MINITE_OUT_FP32, gf = grad_dtype == MINITE_OUT_FP32;
