@@ -254,9 +254,11 @@ __device__ __forceinline__ uint32_t mixed(uint32_t x) {
   return (x ^ (x >> 15)) * 0xBB67AE85u;
 }
 
-// Scale of a block whose largest magnitude is a.
+// Scale of a block whose largest magnitude is a, NaN if a is not finite: with an
+// infinite one the block's other moments would read back as infinite too and its
+// parameters stand still without a sign of it.
 __device__ __forceinline__ float block_scale_of(float a) {
-  const float s = __fmul_rn(a, kInvMax);
+  const float s = __fadd_rn(__fmul_rn(a, kInvMax), __fsub_rn(a, a));
   return s < kTiny ? kTiny : s;
 }
 // The warp's largest non-negative float: their bits order as integers, NaN
