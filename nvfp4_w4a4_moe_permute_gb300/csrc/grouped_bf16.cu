@@ -41,11 +41,13 @@
 //    the end are zeroed in shared memory in both operands (a NaN there would
 //    survive a product with zero). For such a stage the odd CTA's copies count
 //    on its own barrier; its second warp zeroes and reports to the even CTA.
-//  * FP32 outputs: the tensor cores' FP32 sums lose about 2^-24 of the running
+//  * FP32 outputs: the tensor cores' FP32 sums lose up to 2^-22 of the running
 //    sum at every K = 16 step, always towards zero. Sums longer than
 //    kChunkBlocks blocks are therefore split: each chunk is summed in TMEM and
 //    the chunks are added in FP32 registers (round to nearest) by the
-//    epilogue warps. For BF16 outputs the final rounding hides that loss.
+//    epilogue warps. BF16 outputs are split after 16384
+//    values, where 2^-12 beside their last rounding of 2^-8 may be lost (sums of
+//    65536 values of one sign lost 3.3e-4, of 2^25 more than that rounding).
 //    Weight gradients in FP32 leave by bulk copies that store or add in L2:
 //    606 us for 128 experts of 256 rows, 1536 x 2048, added (floor 517).
 //  * Fixed K order, no split over CTAs: results do not depend on the launch.
@@ -78,6 +80,7 @@ constexpr int OUT_ROWS = 16;                      // FP32 weight gradients: rows
 constexpr int OUT_BOX_BYTES = OUT_ROWS * 512;      // 128 features
 constexpr int OUT_BYTES = NUM_EPI_WARPS / 4 * OUT_BOX_BYTES;
 constexpr int kChunkBlocks = 4;                   // FP32 outputs: K blocks summed in TMEM at a time
+constexpr int kChunkBlocksBf16 = 256;             // BF16 outputs
 constexpr size_t kMaxSmem = 232448;
 
 enum Mode { FORWARD = 0, DGRAD = 1, WGRAD = 2 };
@@ -300,18 +303,20 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&r)[8]) {
       : "memory");
 }
 
-// 16 rows of the lane's feature, `out` at the first, `rows` of them in the
+// 16 rows of the lane's feature, v[first ...], `out` at the first, `rows` of them in the
 // output. Even lanes take the even rows of both lanes' features and odd lanes
 // the odd rows, so that a lane writes four bytes and the warp 64 of each of
 // two rows.
+template <int N>
 __device__ __forceinline__ void store_16rows(uint16_t* out, int64_t ldo, int rows, bool ok,
-                                             const float (&v)[16]) {
+                                             const float (&v)[N], int first = 0) {
   const int odd = threadIdx.x & 1;
   uint16_t* o = out + (odd ? ldo - 1 : 0);
 #pragma unroll
   for (int j = 0; j < 16; j += 2) {
-    const float other = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
-    const uint32_t w = odd ? pack_bf16x2_rn(other, v[j + 1]) : pack_bf16x2_rn(v[j], other);
+    const float a = v[first + j], b = v[first + j + 1];
+    const float other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+    const uint32_t w = odd ? pack_bf16x2_rn(other, b) : pack_bf16x2_rn(a, other);
     if (ok && j + odd < rows) *reinterpret_cast<uint32_t*>(o) = w;
     o += 2 * ldo;
   }
@@ -342,7 +347,11 @@ __device__ __forceinline__ void tma_out_3d(const CUtensorMap* map, const void* s
                  :: "l"(m), "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z) : "memory");
 }
 
-template <int MODE, bool F32>
+// SPLIT: sums may have several chunks, always so with FP32 outputs. With BF16 ones
+// the kernel without costs less where tiles are short (weight gradients of 128
+// experts of 256 rows, 1536 x 2048: 186 us, split 210), so the host takes it if no
+// sum can be longer than a chunk.
+template <int MODE, bool F32, bool SPLIT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
   constexpr bool A_MN = MODE != FORWARD, B_MN = MODE == WGRAD;
@@ -696,7 +705,7 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
         buf ^= 1;
         if (buf == 0) acc_phase ^= 1u;
       };
-      if constexpr (F32) {
+      if constexpr (SPLIT) {
         float acc[EPI_COLS];
 #pragma unroll
         for (int j = 0; j < EPI_COLS; ++j) acc[j] = 0.0f;
@@ -742,8 +751,13 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
                 }
               }
           }
-        } else {
+        } else if constexpr (F32) {
           store_64rows(static_cast<float*>(p.out) + at, p.ldo, rows, f_ok, acc);
+        } else {
+          uint16_t* out = static_cast<uint16_t*>(p.out) + at;
+#pragma unroll
+          for (int g = 0; g < EPI_COLS; g += 16)
+            if (g < rows) store_16rows(out + g * p.ldo, p.ldo, rows - g, f_ok, acc, g);
         }
       } else {
         // one chunk, or none: an expert without rows
@@ -812,12 +826,12 @@ bool make_out_map(CUtensorMap* m, void* out, cuuint64_t E, cuuint64_t rows, cuui
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, bool F32>
+template <int MODE, bool F32, bool SPLIT>
 int launch_as(const Maps& maps, Params& p, cudaStream_t s) {
   static std::atomic<uint64_t> devices{0};
-  const cudaError_t attr_err = allow_smem(devices, grouped_bf16_kernel<MODE, F32>, kMaxSmem);
+  const cudaError_t attr_err = allow_smem(devices, grouped_bf16_kernel<MODE, F32, SPLIT>, kMaxSmem);
   if (attr_err != cudaSuccess) return MINITE_ERR_CUDA;
-  p.chunk = F32 ? kChunkBlocks : 1 << 30;
+  p.chunk = F32 ? kChunkBlocks : kChunkBlocksBf16;
   p.budget_ns = wait_budget_ns();
   // barriers, offsets, list and sizes in front of the stages
   const size_t head = (sizeof(Smem) + 3 * (static_cast<size_t>(p.E) + 1) * sizeof(int32_t) +
@@ -827,7 +841,7 @@ int launch_as(const Maps& maps, Params& p, cudaStream_t s) {
   p.stages = static_cast<int>((kMaxSmem - rest) / STAGE_BYTES);
   if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
   const size_t smem = rest + static_cast<size_t>(p.stages) * STAGE_BYTES;
-  int clusters = resident_pairs<10 + 2 * MODE + F32>(grouped_bf16_kernel<MODE, F32>, NUM_THREADS, smem);
+  int clusters = resident_pairs<10 + 4 * MODE + 2 * F32 + SPLIT>(grouped_bf16_kernel<MODE, F32, SPLIT>, NUM_THREADS, smem);
   if (clusters <= 0) return MINITE_ERR_CUDA;
   const int64_t f_tiles = (p.F + BF - 1) / BF;
   // tiles of n rows (forward and dgrad: if all experts had as many rows)
@@ -846,7 +860,7 @@ int launch_as(const Maps& maps, Params& p, cudaStream_t s) {
   if (most >= (int64_t(1) << 30)) return MINITE_ERR_UNSUPPORTED_SHAPE;
   p.units = static_cast<int>(most);
   if (most < clusters) clusters = static_cast<int>(most);
-  if (launch_pair_pdl(grouped_bf16_kernel<MODE, F32>, clusters, NUM_THREADS, smem, s, maps, p) !=
+  if (launch_pair_pdl(grouped_bf16_kernel<MODE, F32, SPLIT>, clusters, NUM_THREADS, smem, s, maps, p) !=
       cudaSuccess)
     return MINITE_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? MINITE_OK : MINITE_ERR_CUDA;
@@ -854,8 +868,11 @@ int launch_as(const Maps& maps, Params& p, cudaStream_t s) {
 
 template <int MODE>
 int launch(const Maps& maps, Params& p, int out_dtype, cudaStream_t s) {
-  return out_dtype == MINITE_OUT_FP32 ? launch_as<MODE, true>(maps, p, s)
-                                      : launch_as<MODE, false>(maps, p, s);
+  if (out_dtype == MINITE_OUT_FP32) return launch_as<MODE, true, true>(maps, p, s);
+  // the longest sum that there can be
+  const int64_t longest = MODE == WGRAD ? p.M : p.K;
+  return longest > kChunkBlocksBf16 * BK ? launch_as<MODE, false, true>(maps, p, s)
+                                         : launch_as<MODE, false, false>(maps, p, s);
 }
 
 constexpr int64_t kMaxDim = int64_t(1) << 20;
