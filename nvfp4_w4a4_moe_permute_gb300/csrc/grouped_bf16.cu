@@ -655,7 +655,11 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
         stage = (stage + kt_n - 1) % p.stages;   // the sum's last stage
         const int left = tl.len - (kt_n - 1) * BK;
         if (left < BK && left % 16 != 0) {
-          const bool w_ok = mbar_wait(&S.tail_full[stage], (tail_parity >> stage) & 1u, budget, abort_flag);
+          // over in time for the whole sum: a budget for each 1024 blocks (they take
+          // 0.3 ms or more). Where the pipeline stands still another role's wait for
+          // one block runs out first and raises the abort flag.
+          const uint64_t all = budget < (uint64_t(1) << 40) ? budget * (1 + kt_n / 1024) : budget;
+          const bool w_ok = mbar_wait(&S.tail_full[stage], (tail_parity >> stage) & 1u, all, abort_flag);
           if (!__all_sync(0xffffffffu, w_ok)) { ok = false; break; }
           tail_parity ^= 1u << stage;
           zero_tail(stage, left, 2 + (tl.n / 2 + 63) / 64);

@@ -78,3 +78,22 @@ def test_weight_gradients(kind, counts):
                                     status=st)
 
     out_of_time(call, surely=kind == "bfloat16" or any(c % 16 for c in counts))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_the_length_of_a_sum_uses_up_no_budget(dtype):
+    """2^25 - 7 rows in one sum, 0.1 s at least, with 20 ms for each wait: no wait is
+    for more than some blocks, but for the odd CTA's tail, which has more time."""
+    n = (1 << 25) - 7
+    a = torch.ones(n, 8, device=DEV, dtype=torch.bfloat16)
+    b = torch.ones(n, 16, device=DEV, dtype=torch.bfloat16)
+    a[::3], b[1::2] = 0.5, 0.25
+    off, status = offsets_of([n]), torch.zeros(1, dtype=torch.int32, device=DEV)
+    want = M.grouped_wgrad_bf16(a, b, off, out_dtype=dtype)
+    M.minite_set_wait_budget_ns(20_000_000)
+    try:
+        got = M.grouped_wgrad_bf16(a, b, off, out_dtype=dtype, status=status)
+        torch.cuda.synchronize()
+    finally:
+        M.minite_set_wait_budget_ns(0)
+    assert int(status.item()) == 0 and torch.equal(got, want)
