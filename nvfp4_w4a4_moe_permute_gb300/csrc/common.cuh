@@ -198,12 +198,13 @@ __device__ __forceinline__ int64_t sf_offset(int64_t r, int64_t c, int64_t kc) {
 // 256 bytes of codes).
 // ----------------------------------------------------------------------------
 
-// 16 BF16 values from a 32-byte aligned address, streaming (read once).
+// 16 BF16 values from a 32-byte aligned address, streaming (read once). Volatile
+// and with a memory clobber, so that it stays behind pdl_wait().
 __device__ __forceinline__ void ld_bf16x16(const uint16_t* p, uint32_t (&w)[8]) {
-  asm("ld.global.cs.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+  asm volatile("ld.global.cs.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
                  "=r"(w[6]), "=r"(w[7])
-               : "l"(p));
+               : "l"(p) : "memory");
 }
 
 // Same values from a 16-byte aligned address (two 16-byte loads).

@@ -108,10 +108,12 @@ struct Row {
   }
   __device__ __forceinline__ Vec vec(int64_t i) const {
     Vec v;
-    asm("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-        : "=r"(v.lo.x), "=r"(v.lo.y), "=r"(v.lo.z), "=r"(v.lo.w), "=r"(v.hi.x), "=r"(v.hi.y),
-          "=r"(v.hi.z), "=r"(v.hi.w)
-        : "l"(x + head + i * Elem<T>::kVec));
+    // volatile and a memory clobber: to the compiler the load would else be a
+    // function of its address alone, free to move ahead of pdl_wait()
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v.lo.x), "=r"(v.lo.y), "=r"(v.lo.z), "=r"(v.lo.w), "=r"(v.hi.x), "=r"(v.hi.y),
+                   "=r"(v.hi.z), "=r"(v.hi.w)
+                 : "l"(x + head + i * Elem<T>::kVec) : "memory");
     return v;
   }
   __device__ __forceinline__ int64_t tail0() const { return head + nv * Elem<T>::kVec; }
