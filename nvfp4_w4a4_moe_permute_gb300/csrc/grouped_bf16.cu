@@ -905,7 +905,8 @@ extern "C" int minite_grouped_gemm_bf16(const void* a, int64_t a_stride, const v
     return MINITE_ERR_UNSUPPORTED_SHAPE;
   if (M_total == 0) return MINITE_OK;
   if (!a || !w || !expert_offsets || !out) return MINITE_ERR_INVALID_ARG;
-  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(expert_offsets, 4))
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(expert_offsets, 4) ||
+      !aligned(status, 4))
     return MINITE_ERR_INVALID_ARG;
   const bool nk = w_layout == MINITE_W_NK;
   Maps maps = {};
@@ -948,7 +949,8 @@ extern "C" int minite_grouped_wgrad_bf16(const void* a, int64_t a_stride, const 
       b_stride > (int64_t(1) << 32))
     return MINITE_ERR_UNSUPPORTED_SHAPE;
   if (!expert_offsets || !out || (M_total > 0 && (!a || !b))) return MINITE_ERR_INVALID_ARG;
-  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(out, 16) || !aligned(expert_offsets, 4))
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(out, 16) || !aligned(expert_offsets, 4) ||
+      !aligned(status, 4))
     return MINITE_ERR_INVALID_ARG;
   Maps maps = {};   // without rows no copy is issued
   Params p = {};

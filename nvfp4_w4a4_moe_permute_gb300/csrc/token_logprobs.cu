@@ -833,7 +833,7 @@ extern "C" int minite_token_logprobs(const void* logits, int dtype, int64_t N, i
     return MINITE_ERR_UNSUPPORTED_SHAPE;
   if (!aligned(logits, dtype == MINITE_OUT_FP32 ? 4 : 2) ||
       !aligned(targets, targets_int64 ? 8 : 4) || !aligned(logprob, 4) || !aligned(entropy, 4) ||
-      !aligned(stats, 8) || !aligned(alt_ids, 4) || !aligned(alt_logprobs, 4))
+      !aligned(stats, 8) || !aligned(alt_ids, 4) || !aligned(alt_logprobs, 4) || !aligned(status, 4))
     return MINITE_ERR_INVALID_ARG;
   Params p = {};
   p.logits = logits;
@@ -875,7 +875,7 @@ extern "C" int minite_token_logprobs_backward(const void* logits, int dtype, int
   const uintptr_t ea = dtype == MINITE_OUT_FP32 ? 4 : 2;
   if (!aligned(logits, ea) || !aligned(dlogits, ea) || !aligned(targets, targets_int64 ? 8 : 4) ||
       !aligned(stats, 8) || !aligned(entropy, 4) || !aligned(grad_logprob, 4) ||
-      !aligned(grad_entropy, 4))
+      !aligned(grad_entropy, 4) || !aligned(status, 4))
     return MINITE_ERR_INVALID_ARG;
   if (dlogits == logits && dlogits_stride != row_stride) return MINITE_ERR_INVALID_ARG;
   BackParams p = {};

@@ -415,9 +415,25 @@ def _raw(stream, dev):
     return stream.cuda_stream
 
 
+def _shape(t, dims, name, what):
+    """A tensor's sizes, of which there have to be so many."""
+    if len(t.shape) != dims:
+        raise MiniteError(f"{name}: expected {what} with {dims} dimensions, got {list(t.shape)}")
+    return t.shape
+
+
+def _status(t, name, dev):
+    """Address of the word that device errors are OR-ed into, None for None."""
+    if t is None:
+        return None
+    if t.dtype is not torch.int32 or t.numel() < 1:
+        raise MiniteError(f"{name}: status is int32, one element")
+    return _ptr(t, dev)
+
+
 def _rows(t, name):
     """Row stride of a 2-D tensor whose rows are contiguous and do not overlap."""
-    n, c = t.shape
+    n, c = _shape(t, 2, name, "a matrix")
     rs, cs = t.stride()
     if (c > 1 and cs != 1) or (n > 1 and rs < c):
         raise MiniteError(f"{name}: expected 2-D with contiguous rows that do not overlap")
@@ -435,17 +451,17 @@ def minite_grouped_gemm_bf16(a, w, expert_offsets, out, w_layout=W_NK, status=No
     name = "minite_grouped_gemm_bf16"
     if a.dtype is not torch.bfloat16 or w.dtype is not torch.bfloat16 or not w.is_contiguous():
         raise MiniteError(f"{name}: a and w are bfloat16, w contiguous")
-    E, N, K = w.shape
+    E, N, K = _shape(w, 3, name, "w")
     if w_layout == W_KN:
         N, K = K, N
-    M, Ka = a.shape
+    M, Ka = _shape(a, 2, name, "a")
     if Ka != K or out.shape != (M, N):
         raise MiniteError(f"{name}: shapes of a, w and out do not match")
     d = _device(a)
     rc = load().minite_grouped_gemm_bf16(a.data_ptr(), _rows(a, name), _ptr(w, d), w_layout,
                                          _offsets(expert_offsets, E, name, d), M, N, K, E,
                                          _ptr(out, d), _rows(out, name), _dtype(out, name),
-                                         _ptr(status, d), _raw(stream, d))
+                                         _status(status, name, d), _raw(stream, d))
     if rc:
         _check(rc, name)
 
@@ -455,15 +471,15 @@ def minite_grouped_wgrad_bf16(a, b, expert_offsets, out, accumulate=False, statu
     name = "minite_grouped_wgrad_bf16"
     if a.dtype is not torch.bfloat16 or b.dtype is not torch.bfloat16 or not out.is_contiguous():
         raise MiniteError(f"{name}: a and b are bfloat16, out contiguous")
-    E, Na, Nb = out.shape
-    M = a.shape[0]
+    E, Na, Nb = _shape(out, 3, name, "out")
+    M = _shape(a, 2, name, "a")[0]
     if a.shape != (M, Na) or b.shape != (M, Nb):
         raise MiniteError(f"{name}: shapes of a, b and out do not match")
     d = _device(a)
     rc = load().minite_grouped_wgrad_bf16(a.data_ptr(), _rows(a, name), _ptr(b, d), _rows(b, name),
                                           _offsets(expert_offsets, E, name, d), M, Na, Nb, E,
                                           _ptr(out, d), _dtype(out, name), 1 if accumulate else 0,
-                                          _ptr(status, d), _raw(stream, d))
+                                          _status(status, name, d), _raw(stream, d))
     if rc:
         _check(rc, name)
 
@@ -495,7 +511,7 @@ def minite_token_logprobs(logits, targets, logprob, entropy=None, stats=None, te
     N, V = logits.shape
     k = 0
     if alt_ids is not None:
-        k = alt_ids.shape[1]
+        k = _shape(alt_ids, 2, name, "alt_ids")[1]
         if alt_ids.dtype is not torch.int32 or alt_ids.shape[0] != N or not alt_ids.is_contiguous():
             raise MiniteError(f"{name}: alt_ids is int32 [N, k], contiguous")
     d = _device(logits)
@@ -505,7 +521,7 @@ def minite_token_logprobs(logits, targets, logprob, entropy=None, stats=None, te
                                       _f32(entropy, (N,), name, "entropy", d),
                                       _f32(stats, (N, 2), name, "stats", d), k, _ptr(alt_ids, d),
                                       _f32(alt_logprobs, (N, k), name, "alt_logprobs", d),
-                                      _ptr(status, d), _raw(stream, d))
+                                      _status(status, name, d), _raw(stream, d))
     if rc:
         _check(rc, name)
 
@@ -524,7 +540,7 @@ def minite_token_logprobs_backward(logits, targets, stats, entropy, grad_logprob
         temperature, _f32(stats, (N, 2), name, "stats", d), _f32(entropy, (N,), name, "entropy", d),
         _f32(grad_logprob, (N,), name, "grad_logprob", d),
         _f32(grad_entropy, (N,), name, "grad_entropy", d),
-        _ptr(dlogits, d), _rows(dlogits, name), _ptr(status, d), _raw(stream, d))
+        _ptr(dlogits, d), _rows(dlogits, name), _status(status, name, d), _raw(stream, d))
     if rc:
         _check(rc, name)
 
@@ -621,7 +637,9 @@ def grouped_gemm_bf16(x, w, expert_offsets, w_as_stored=False, out=None, out_dty
     (the activation gradient of that forward, x its output's gradient).
     Returns [M, N]."""
     if out is None:
-        out = _empty((x.shape[0], w.shape[2 if w_as_stored else 1]), out_dtype, x, stream)
+        name = "grouped_gemm_bf16"
+        rows, cols = _shape(x, 2, name, "x")[0], _shape(w, 3, name, "w")[2 if w_as_stored else 1]
+        out = _empty((rows, cols), out_dtype, x, stream)
     minite_grouped_gemm_bf16(x, w, expert_offsets, out, W_KN if w_as_stored else W_NK, status, stream)
     return out
 
@@ -633,7 +651,11 @@ def grouped_wgrad_bf16(dy, x, expert_offsets, out=None, out_dtype=torch.float32,
     if out is None:
         if accumulate:
             raise MiniteError("grouped_wgrad_bf16: accumulate needs out")
-        out = _empty((expert_offsets.numel() - 1, dy.shape[1], x.shape[1]), out_dtype, x, stream)
+        name = "grouped_wgrad_bf16"
+        if expert_offsets.numel() < 2:
+            raise MiniteError(f"{name}: expert_offsets is int32 [E + 1], contiguous")
+        out = _empty((expert_offsets.numel() - 1, _shape(dy, 2, name, "dy")[1], _shape(x, 2, name, "x")[1]),
+                     out_dtype, x, stream)
     minite_grouped_wgrad_bf16(dy, x, expert_offsets, out, accumulate, status, stream)
     return out
 
@@ -645,6 +667,8 @@ def token_logprobs(logits, targets=None, temperature=1.0, alternatives=0, status
     alt_ids, alt_logprobs); a negative target marks a row that is skipped."""
     name = "token_logprobs"
     ld = _rows(logits, name)
+    if alternatives < 0:
+        raise MiniteError(f"{name}: alternatives is {alternatives}")
     N, V = logits.shape
     d = _device(logits)
     f32 = torch.float32
@@ -660,7 +684,7 @@ def token_logprobs(logits, targets=None, temperature=1.0, alternatives=0, status
         temperature, None if logprob is None else logprob.data_ptr(),
         entropy.data_ptr(), stats.data_ptr(), alternatives,
         alt_ids.data_ptr() if alternatives else None,
-        alt_logprobs.data_ptr() if alternatives else None, _ptr(status, d), _raw(stream, d))
+        alt_logprobs.data_ptr() if alternatives else None, _status(status, name, d), _raw(stream, d))
     if rc:
         _check(rc, "minite_token_logprobs")
     return {"logprob": logprob, "entropy": entropy, "stats": stats, "alt_ids": alt_ids,
