@@ -771,7 +771,8 @@ int minite_test_div6_exhaustive(unsigned long long* mismatches, minite_stream_t 
  * Test hook: the optimizer computes roots and quotients of pairs from the
  * hardware's approximations with a correction. This adds, into the device
  * counters mismatches[2] (caller zeroes them), how many of 4 * 2^24 roots and
- * of 2^31 quotients differ from the IEEE ones (expected: 0).
+ * of 2^31 quotients (m / d and -m / d of 2^30 pairs, 2^-100 <= |m| < 2^60, 2^-51 <=
+ * d < 2^65, those below 2^-126 left out) differ from the IEEE ones (expected: 0).
  */
 int minite_test_adamw_math(unsigned long long* mismatches, minite_stream_t stream);
 
