@@ -617,10 +617,11 @@ int minite_grouped_wgrad_bf16(const void* a, int64_t a_stride, const void* b, in
  *   logprob = log p[target],  entropy = -sum_j p_j log p_j,
  *   alternatives: the k largest logits' ids and log p, largest first, equal
  *   logits by the lower id.
- * All sums in FP32. -inf logits are masked tokens: probability 0, never an
- * alternative (missing alternatives have id -1 and -inf). A row whose every
- * logit is -inf has logprob -inf, entropy 0 and no alternatives. A NaN or
- * +inf logit makes the row's results NaN (ids -1).
+ * All sums in FP32, in an order that depends on V and on the remainder of the
+ * row's address by 32 bytes alone, not on N or on other rows. -inf logits are
+ * masked tokens: probability 0, never an alternative (missing alternatives have
+ * id -1 and -inf). A row whose every logit is -inf has logprob -inf, entropy 0
+ * and no alternatives. A NaN or +inf logit makes the row's results NaN (ids -1).
  *
  * logits:  device, BF16 or FP32 (dtype) [N, V], rows `row_stride` elements
  *          apart, aligned to the element only. x / temperature must fit FP32.

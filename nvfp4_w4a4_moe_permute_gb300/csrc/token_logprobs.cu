@@ -428,7 +428,9 @@ __device__ __forceinline__ void block_alternatives(Shared& S, const Row<T>& r, c
 // One row per cluster of CTAs (of one CTA where there are rows enough). A row is
 // cut into segments by its length alone, a segment is summed by the 256 threads
 // of one CTA, and the segments are joined in order by the cluster's first CTA:
-// the results do not depend on how many CTAs shared a row.
+// the results do not depend on how many CTAs shared a row. They do depend, in the
+// last places, on the remainder of the row's address by 32 bytes: its vectors, and
+// with them the threads' shares, start at a multiple of that.
 // UNROLL 32-byte loads in flight per thread, CTAS CTAs per SM.
 template <typename T, int UNROLL, int CTAS>
 __global__ void __launch_bounds__(kThreads, CTAS) logprobs_kernel(const Params p) {
