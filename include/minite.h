@@ -702,6 +702,12 @@ int minite_token_logprobs_backward(const void* logits, int dtype, int64_t N, int
  *   coefficient or an inverse loss scale that the host never reads).
  * step: 1 for the first step; with hyper-parameters outside 0 <= beta < 1,
  *   eps >= 0 or not finite, MINITE_ERR_INVALID_ARG and nothing is enqueued.
+ * All hyper-parameters and `step` are host values of the call, the same for all
+ *   of its tensors: groups with rates or decays of their own take a call each,
+ *   and a graph that captured a call replays that step's bias corrections (and
+ *   draws) at every replay; capture a call again, or update its node, for each
+ *   step. A step with non-finite gradients is not skipped: they reach the
+ *   moments, whatever grad_scale is.
  */
 typedef struct minite_adamw_tensor {
   void* param;

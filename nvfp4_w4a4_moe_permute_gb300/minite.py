@@ -711,7 +711,12 @@ class AdamW:
     starts at a multiple of 256 elements (``starts``); ``state`` takes buffers
     of this layout and a step count to continue from. A step uses ``params``,
     ``copies`` and the states as they are then: their storage may be replaced
-    between steps, by some of the same type and size."""
+    between steps, by some of the same type and size.
+
+    One learning rate and one weight decay for all tensors (an optimizer for each
+    group that has its own). Step count and rates are host values: a captured
+    graph replays one step's bias corrections. Non-finite gradients are not
+    skipped."""
 
     BLOCK = 256
 
