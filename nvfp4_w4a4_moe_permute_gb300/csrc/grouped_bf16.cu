@@ -23,12 +23,12 @@
 //    twice, so that a tile's epilogue runs under the next one's products. Every
 //    copy is a CTA's own: no load is multicast, so that no call can make one
 //    read memory of another GPU.
-//    8 experts of 8192 rows, 2048 x 1536, take 232 us (1778 TFLOP/s, 92% of the
-//    measured burst rate).
+//    8 experts of 8192 rows, 2048 x 1536, take 226 to 232 us (1827 to 1778
+//    TFLOP/s, 95 to 92% of the measured burst rate), with FP32 results 271.
 //  * Large experts (bound by the tensor cores and L2) and small ones (bound by
 //    DRAM) are interleaved, so that all are busy: 65536 rows in Zipf shares, 2048
-//    x 1536, 327 us (floors: tensor 214, HBM 191). 128 experts of 256 rows, 1536 x
-//    2048: 168 us, 93% of the copy rate; of 16 rows 131.
+//    x 1536, 315 to 327 us (floors: tensor 214, HBM 191). 128 experts of 256 rows,
+//    1536 x 2048: 165 to 168 us, 95 to 93% of the copy rate; of 16 rows 129 to 131.
 //  * Operands come by TMA with the 128-byte swizzle, K-major (rows of 64 K
 //    values) or, where memory has the other dimension contiguous (dgrad's
 //    weight, both operands of the weight gradient), MN-major: boxes of 64 such
@@ -49,7 +49,7 @@
 //    values, where 2^-12 beside their last rounding of 2^-8 may be lost (sums of
 //    65536 values of one sign lost 3.3e-4, of 2^25 more than that rounding).
 //    Weight gradients in FP32 leave by bulk copies that store or add in L2:
-//    606 us for 128 experts of 256 rows, 1536 x 2048, added (floor 517).
+//    589 to 606 us for 128 experts of 256 rows, 1536 x 2048, added (floor 517).
 //  * Fixed K order, no split over CTAs: results do not depend on the launch.
 //  * Every mbarrier wait is bounded; on expiry the CTA records
 //    MINITE_ERR_TIMEOUT, drains its copies and MMAs, frees TMEM and exits.
@@ -349,8 +349,8 @@ __device__ __forceinline__ void tma_out_3d(const CUtensorMap* map, const void* s
 
 // SPLIT: sums may have several chunks, always so with FP32 outputs. With BF16 ones
 // the kernel without costs less where tiles are short (weight gradients of 128
-// experts of 256 rows, 1536 x 2048: 186 us, split 210), so the host takes it if no
-// sum can be longer than a chunk.
+// experts of 256 rows, 1536 x 2048: 187 us, split 210 to 235), so the host takes it
+// if no sum can be longer than a chunk.
 template <int MODE, bool F32, bool SPLIT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {

@@ -200,7 +200,7 @@ def adamw(args, M, dev, status):
     p = [torch.randn(n, device=dev, generator=gen).to(dtype) for n in sizes]
     grads = [(torch.randn(n, device=dev, generator=gen) * 1e-3).to(torch.bfloat16) for n in sizes]
     opt = M.AdamW(p, copies=None if args.bits == 8 else [q.to(torch.bfloat16) for q in p],
-                  state_bits=args.bits)
+                  betas=(0.9, args.beta2), state_bits=args.bits)
     for _ in range(args.reps):
         opt.step(grads)
 
@@ -228,6 +228,7 @@ def main(argv=None) -> int:
     ap.add_argument("--alternatives", type=int, default=0)
     ap.add_argument("--backward", action="store_true", help="logprobs: the gradient")
     ap.add_argument("--bits", type=int, default=8, choices=[8, 32], help="adamw: the states'")
+    ap.add_argument("--beta2", type=float, default=0.95, help="adamw: above 0.95 8-bit codes are drawn")
     ap.add_argument("--reps", type=int, default=3)
     ap.add_argument("--seed", type=int, default=0)
     args = ap.parse_args(argv)
