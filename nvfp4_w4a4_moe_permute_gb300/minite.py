@@ -759,8 +759,8 @@ class AdamW:
         return [(x.data_ptr(), x.numel(), x.dtype, x.is_contiguous()) for x in t]
 
     def _bind(self, kept):
-        """Checks all of that and writes its addresses into the descriptors."""
-        d, dev = self._tensors, self.exp_avg.device
+        """Checks all of that, then writes its addresses into the descriptors."""
+        dev, places = self.exp_avg.device, {}
         _need(len(self.params) == len(self._numel), "AdamW: a parameter was added or taken away")
         for i, p in enumerate(self.params):
             _need(p.is_cuda and p.device == dev and p.dtype == self._dtype and p.is_contiguous() and
@@ -773,9 +773,11 @@ class AdamW:
             t = getattr(self, name)
             _need(t.numel() == n and t.dtype == dtype and t.is_contiguous() and t.device == dev,
                   f"AdamW: state {name} is not {dtype} [{n}] on {dev}")
-            d[name] = t.data_ptr() + first * t.element_size()
-        d["param"] = [p.data_ptr() for p in self.params]
-        d["param_bf16"] = 0 if self.copies is None else [c.data_ptr() for c in self.copies]
+            places[name] = t.data_ptr() + first * t.element_size()
+        places["param"] = [p.data_ptr() for p in self.params]
+        places["param_bf16"] = 0 if self.copies is None else [c.data_ptr() for c in self.copies]
+        for name, address in places.items():
+            self._tensors[name] = address
         self._bound = kept
 
     def step(self, grads, grad_scale=None, lr=None, stream=None):

@@ -117,6 +117,21 @@ def test_storage_that_does_not_fit_is_refused(given, bits):
         step(opt)
 
 
+@pytest.mark.parametrize("bits", [8, 32])
+def test_a_refused_step_leaves_no_address_behind(given, bits):
+    """One state is replaced by a good tensor and another by a bad one: refused. With
+    the old ones put back, a step uses the old ones."""
+    opt = optimizer(bits)
+    step(opt)
+    old = opt.exp_avg.t, opt.exp_avg_sq.t
+    opt.exp_avg.t, opt.exp_avg_sq.t = old[0].clone(), torch.zeros(3)
+    with pytest.raises(M.MiniteError):
+        step(opt)
+    opt.exp_avg.t, opt.exp_avg_sq.t = old
+    step(opt)
+    check(opt, given[-1], bits)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("bits", [8, 32])
 def test_a_run_with_replaced_storage_equals_one_without(bits):
