@@ -281,19 +281,22 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   }
 }
 
-// Warp: 16 / 8 consecutive FP32 columns of this warp's 32 TMEM lanes.
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&r)[16]) {
+// Warp: 16 / 8 consecutive FP32 columns of this warp's 32 TMEM lanes, the 16 to
+// r[first ...].
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols16(uint32_t taddr, float (&r)[N], int first = 0) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32"
       " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
-        "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
-        "=f"(r[14]), "=f"(r[15])
+      : "=f"(r[first]), "=f"(r[first + 1]), "=f"(r[first + 2]), "=f"(r[first + 3]), "=f"(r[first + 4]),
+        "=f"(r[first + 5]), "=f"(r[first + 6]), "=f"(r[first + 7]), "=f"(r[first + 8]),
+        "=f"(r[first + 9]), "=f"(r[first + 10]), "=f"(r[first + 11]), "=f"(r[first + 12]),
+        "=f"(r[first + 13]), "=f"(r[first + 14]), "=f"(r[first + 15])
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, float (&r)[8]) {
+__device__ __forceinline__ void tmem_ld_cols8(uint32_t taddr, float (&r)[8]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
@@ -349,7 +352,7 @@ __device__ __forceinline__ void tma_out_3d(const CUtensorMap* map, const void* s
 
 // SPLIT: sums may have several chunks, always so with FP32 outputs. With BF16 ones
 // the kernel without costs less where tiles are short (weight gradients of 128
-// experts of 256 rows, 1536 x 2048: 187 us, split 210 to 235), so the host takes it
+// experts of 256 rows, 1536 x 2048: 187 us, split 197), so the host takes it
 // if no sum can be longer than a chunk.
 template <int MODE, bool F32, bool SPLIT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
@@ -717,14 +720,20 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
         for (int c = 0; c < chunks; ++c) {
           if (!wait_acc()) break;
           const uint32_t tb = tb0 + buf * MAX_N;
+          if (!F32 && c == 0) {   // often the only one (FP32 results of short sums lost 6% by it)
 #pragma unroll
-          for (int g = 0; g < EPI_COLS; g += 8)
-            if (g < rows) {
-              float r[8];
-              tmem_ld_cols(tb + g, r);
+            for (int g = 0; g < EPI_COLS; g += 16)
+              if (g < rows) tmem_ld_cols16(tb + g, acc, g);
+          } else {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) acc[g + j] += r[j];
-            }
+            for (int g = 0; g < EPI_COLS; g += 8)
+              if (g < rows) {
+                float r[8];
+                tmem_ld_cols8(tb + g, r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[g + j] += r[j];
+              }
+          }
           release();
         }
         // The four warps that meet at a named barrier below, which has no bound, go
@@ -777,7 +786,7 @@ grouped_bf16_kernel(const __grid_constant__ Maps maps, const Params p) {
 #pragma unroll
         for (int g = 0; g < EPI_COLS; g += 16) {
           float r[16];
-          if (g < rows) tmem_ld_cols(tb + g, r);
+          if (g < rows) tmem_ld_cols16(tb + g, r);
           if (g == EPI_COLS - 16) release();
           if (g < rows) store_16rows(out + g * p.ldo, p.ldo, rows - g, f_ok, r);
         }
