@@ -75,8 +75,12 @@ enum {
   MINITE_OP_PERMUTE_QUANT = 1,
   MINITE_OP_COMBINE_BACKWARD_QUANT = 2,
   MINITE_OP_QUANTIZE_TOKENS = 3,
-  MINITE_OP_GATE_UP_SWIGLU = 4
+  MINITE_OP_GATE_UP_SWIGLU = 4,
+  MINITE_OP_PERMUTE_ROWS = 5,
+  MINITE_OP_GRAD_NORM = 6,
+  MINITE_OP_VERIFY_DRAFTS = 7
 };
+enum { MINITE_NORM_2 = 0, MINITE_NORM_MAX = 1 };
 
 /*
  * minite_quantize_nvfp4 -- NVFP4 quantization of `groups` BF16 matrices.
@@ -725,11 +729,178 @@ int minite_adamw_step(const minite_adamw_tensor* tensors, int64_t n_tensors, int
                       double eps, double weight_decay, int64_t step, const float* grad_scale,
                       minite_stream_t stream);
 
+/*
+ * minite_moe_permute_rows -- tokens sorted by expert, in BF16 or FP32: the
+ * counterpart of minite_moe_permute_quant for the products that stay in BF16.
+ *
+ * Cites: miniTE report summary, "Two complementary interventions" (contiguous
+ * expert buffers, device-side metadata) and "Respect the timing boundaries" (the
+ * measured learner paths run the backward in BF16).
+ *
+ * Rows are ordered by (expert, token, slot): rows[dest_row[t, j]] = x[t], as bits.
+ * A negative id is a slot that is not used (a dropped token, an expert of another
+ * rank): its dest_row is -1. An id at or above E is treated the same way and sets
+ * bit 1<<MINITE_ERR_BAD_ROUTING. The same expert may appear twice in a token's
+ * slots. Used rows are [0, expert_offsets[E]); later ones are left as they were,
+ * their perm_src is -1.
+ *
+ * x:        device, BF16 or FP32 (dtype) [T, H], rows `x_stride` elements apart.
+ * topk_ids: device, int32 [T, k].
+ * rows:     device, the type of x, [T*k, H], rows `rows_stride` elements apart.
+ * expert_offsets: device, int32 [E+1]; perm_src: device, int32 [T*k], token of
+ *           each row; dest_row: device, int32 [T, k].
+ * workspace: device, >= minite_workspace_bytes(MINITE_OP_PERMUTE_ROWS, T, 0, E, k),
+ *           256-byte aligned, contents on entry ignored.
+ * Shape rules: 1 <= H < 2^30, 1 <= E <= 1024, 1 <= k <= 32, T*k < 2^31, T = 0
+ * allowed (offsets become 0), strides at least H and below 2^31. Matrices are
+ * aligned to their element; accesses are 32 bytes wide where base addresses, row
+ * sizes and strides are multiples of that, 16, 4 or 2 bytes otherwise.
+ */
+int minite_moe_permute_rows(const void* x, int dtype, int64_t x_stride, const int32_t* topk_ids,
+                            int64_t T, int64_t H, int32_t E, int32_t k, void* rows,
+                            int64_t rows_stride, int32_t* expert_offsets, int32_t* perm_src,
+                            int32_t* dest_row, void* workspace, size_t ws_bytes, int32_t* status,
+                            minite_stream_t stream);
+
+/*
+ * minite_moe_spread_rows -- rows by a routing that is already there:
+ * rows[dest_row[t, j]] = x[t] (the gradient of minite_moe_combine, or the tokens
+ * of a weight gradient). dest_row: a permutation's, int32 [T, k]; negative entries
+ * are skipped, those at or above M too, with bit 1<<MINITE_ERR_BAD_ROUTING. No two
+ * entries name the same row. Rows that none names are left as they were. Rules as
+ * minite_moe_permute_rows, rows being [M, H] with M < 2^31.
+ */
+int minite_moe_spread_rows(const void* x, int dtype, int64_t x_stride, const int32_t* dest_row,
+                           int64_t T, int64_t M, int64_t H, int32_t k, void* rows,
+                           int64_t rows_stride, int32_t* status, minite_stream_t stream);
+
+/*
+ * minite_moe_combine_rows -- back to token order with the routing weights:
+ *   y[t] = sum_j weights[t, j] * rows[dest_row[t, j]]
+ * in FP32, fused multiply-adds in slot order starting from 0, rounded once. With
+ * weights NULL they are 1: the gradient of minite_moe_permute_rows. Skipped slots
+ * (see minite_moe_spread_rows) add nothing, whatever their weight; a token without
+ * any gets zeros. A weight of 0 still reads its row (0 times infinity is NaN).
+ *
+ * rows: device, BF16 or FP32 [M, H]; weights: device, float [T, k]; y: device, the
+ * type of rows, [T, H], no overlap with rows. Rules as minite_moe_spread_rows.
+ */
+int minite_moe_combine_rows(const void* rows, int dtype, int64_t rows_stride,
+                            const int32_t* dest_row, const float* weights, int64_t T, int64_t M,
+                            int64_t H, int32_t k, void* y, int64_t y_stride, int32_t* status,
+                            minite_stream_t stream);
+
+/*
+ * minite_moe_combine_rows_backward -- the gradient of minite_moe_combine_rows:
+ *   drows[dest_row[t, j]] = weights[t, j] * dy[t]          (rounded once)
+ *   dweights[t, j] = sum_h dy[t, h] * rows[dest_row[t, j], h]   (0 if skipped)
+ * The sums are FP32, over pieces of 32 accesses of a row (their width follows from
+ * the alignment, see minite_moe_permute_rows) and then over the pieces in order: a
+ * result depends on its own two rows and on their alignment alone.
+ *
+ * rows, dweights: both NULL where the router is not trained. drows may be rows
+ * itself (with the same stride), otherwise no overlap; rows that no slot names are
+ * left as they were. Rules as minite_moe_combine_rows; weights is not NULL (see
+ * minite_moe_spread_rows).
+ */
+int minite_moe_combine_rows_backward(const void* dy, int dtype, int64_t dy_stride,
+                                     const void* rows, int64_t rows_stride,
+                                     const int32_t* dest_row, const float* weights, int64_t T,
+                                     int64_t M, int64_t H, int32_t k, void* drows,
+                                     int64_t drows_stride, float* dweights, int32_t* status,
+                                     minite_stream_t stream);
+
+/*
+ * minite_grad_norm -- the global norm of many gradients and the factor that clips
+ * it, which minite_adamw_step takes as grad_scale and the host never reads.
+ *
+ *   norm = sqrt(sum g^2) over all elements of all tensors (MINITE_NORM_2), or the
+ *          largest |g| (MINITE_NORM_MAX)
+ *   factor = min(1, max_norm / (norm + 1e-6))
+ * Squares are added in FP32 64 at a time, all else in 64 bits, in an order that
+ * depends on the tensors' sizes and the device alone. Nothing overflows or
+ * vanishes on the way: norm is infinite only where it does not fit FP32. A NaN
+ * among the gradients makes both NaN, an infinity norm infinite and factor 0. No
+ * elements: norm 0.
+ *
+ * tensors: HOST array, read during the call (out and out_dtype are ignored).
+ * norm, factor: device, float [1], one of them may be NULL.
+ * max_norm: at or above 0, infinity allowed.
+ * workspace: device, >= minite_workspace_bytes(MINITE_OP_GRAD_NORM, n_tensors, 0,
+ *          0, 0) bytes, 8-byte aligned, contents on entry ignored.
+ */
+typedef struct minite_grad_tensor {
+  const void* grad;    /* device, aligned to its element */
+  void* out;           /* device, aligned to its element: minite_clip_grads only */
+  int64_t n;           /* elements, 0 is skipped */
+  int32_t grad_dtype;  /* MINITE_OUT_BF16 or MINITE_OUT_FP32 */
+  int32_t out_dtype;
+} minite_grad_tensor;
+
+int minite_grad_norm(const minite_grad_tensor* tensors, int64_t n_tensors, int order,
+                     double max_norm, float* norm, float* factor, void* workspace,
+                     size_t ws_bytes, minite_stream_t stream);
+
+/*
+ * minite_clip_grads -- out = grad * factor[0] for many tensors, in FP32, rounded
+ * once to out_dtype. out may be grad itself (of the same type); where that holds
+ * for every tensor, a factor of exactly 1 leaves them untouched. Otherwise no
+ * overlap. factor: device, float [1], as minite_grad_norm wrote it, say.
+ */
+int minite_clip_grads(const minite_grad_tensor* tensors, int64_t n_tensors, const float* factor,
+                      minite_stream_t stream);
+
+/*
+ * minite_verify_drafts -- drafted tokens of B sequences verified against the
+ * target's probabilities (speculative sampling: every token that comes out is
+ * distributed as the target's).
+ *
+ * Cites: miniTE report summary, "Follow the numerical execution path" (the
+ * sampler's token log probabilities are what the learner's are compared by).
+ *
+ * p_i = softmax(target[b, i] / temperature), q_i = softmax(draft[b, i] / temperature),
+ * x_i = draft_tokens[b, i], u_i = uniforms[b, i], e = noise[b]. A sequence's drafts are
+ * those before its first negative token. Draft i stands while u_i q_i(x_i) < p_i(x_i)
+ * and all before it stand. With n that stand,
+ *   tokens[b] = x_0 ... x_(n-1), next, -1 ...;  accepted[b] = n
+ *   next = argmax_j max(p_n(j) - q_n(j), 0) / e_j   where draft n fell,
+ *          argmax_j p_n(j) / e_j                     where there is none
+ * equal quotients by the lower id. Where p_n - q_n leaves nothing above 0 (by
+ * rounding), p_n is taken. With draft NULL the drafts were looked up: q_i is 1 at x_i.
+ * logprobs[b, i] = log p_i(tokens[b, i]), 0 behind the last token.
+ * Probabilities are FP32: a draft within some 2^-20 of the border, or two quotients as
+ * near to each other, may go either way. A masked token (-inf) has probability 0; where
+ * a row has no probabilities (a NaN or +inf logit, or none above -inf) a draft does not
+ * stand, and a row to sample from that has none, or whose draft's row has none, gives
+ * token -1 with logprob NaN. A draft at or above V sets bit 1<<MINITE_ERR_BAD_TOKEN and
+ * ends its sequence's drafts.
+ *
+ * target: device, BF16 or FP32 [B * (S + 1), V], rows `target_stride` elements apart;
+ * draft:  device, BF16 or FP32 [B * S, V] or NULL. Both aligned to the element.
+ * draft_tokens: device, int32 [B, S]; uniforms: device, float [B, S], in [0, 1).
+ * noise:  device, float [B, V], rows `noise_stride` apart: exponential variates, > 0 (a
+ *         token of weight above 0 whose variate is not wins).
+ * tokens: device, int32 [B, S + 1]; accepted: device, int32 [B]; logprobs: device, float
+ *         [B, S + 1] or NULL.
+ * workspace: device, >= minite_workspace_bytes(MINITE_OP_VERIFY_DRAFTS, B, S, 0, 0)
+ *         bytes, 256-byte aligned, contents on entry ignored.
+ * Shape rules: 0 <= S <= 31 (0: one token is sampled), 0 <= B <= 2^24, 1 <= V < 2^31.
+ */
+int minite_verify_drafts(const void* target, int target_dtype, int64_t target_stride,
+                         const void* draft, int draft_dtype, int64_t draft_stride,
+                         const int32_t* draft_tokens, const float* uniforms, const float* noise,
+                         int64_t noise_stride, int64_t B, int32_t S, int64_t V,
+                         float temperature, int32_t* tokens, int32_t* accepted, float* logprobs,
+                         void* workspace, size_t ws_bytes, int32_t* status,
+                         minite_stream_t stream);
+
 /* Workspace bytes needed by `op` (MINITE_OP_QUANTIZE: a = groups;
  * MINITE_OP_PERMUTE_QUANT: a = T, b = H, E, k; MINITE_OP_COMBINE_BACKWARD_QUANT:
  * a = T, b = H; MINITE_OP_QUANTIZE_TOKENS: a = E, b = source rows when
  * they are gathered and no row maxima are passed, else 0;
- * MINITE_OP_GATE_UP_SWIGLU: a = M_total, b = I). 0 means none needed. */
+ * MINITE_OP_GATE_UP_SWIGLU: a = M_total, b = I; MINITE_OP_PERMUTE_ROWS: a = T, E,
+ * k; MINITE_OP_GRAD_NORM: a = tensors; MINITE_OP_VERIFY_DRAFTS: a = B, b = S). 0
+ * means none needed. */
 size_t minite_workspace_bytes(int op, int64_t a, int64_t b, int32_t E, int32_t k);
 
 /* Static description of a status code. */

@@ -1,0 +1,373 @@
+// minite_grad_norm and minite_clip_grads: the global norm of many gradients, the
+// clipping factor, and gradients times that factor.
+//
+//   norm = sqrt(sum over all tensors of g^2)   or   max |g|
+//   factor = min(1, max_norm / (norm + 1e-6))
+//
+// A thread adds the squares of 64 elements in FP32 and their sum to a double;
+// everything after that is in 64 bits and in a fixed order. Where the 64 squares
+// leave the range in which FP32 adds them without loss, they are added again,
+// scaled by a power of two that brings their largest to a harmless size: the norm
+// is right for every finite gradient, FP32 denormals and 3e38 among them.
+//
+// Bound by HBM.
+#include <cmath>
+
+#include "common.cuh"
+#include "host_util.h"
+
+namespace minite {
+namespace gradnorm {
+
+constexpr int kThreads = 256;
+constexpr int kPieces = 4;        // 16-element pieces of a thread in a chunk
+constexpr int kPiece = 16;
+constexpr int64_t kChunk = static_cast<int64_t>(kThreads) * kPieces * kPiece;
+constexpr int kBlocksPerSm = 2;
+constexpr int kMaxBlocks = 1024;  // partial sums of a launch
+
+struct Tensor {
+  const void* g;
+  void* out;
+  int64_t n;
+};
+
+// The tensors of a launch: chunks chunk0[i] .. chunk0[i + 1] belong to tensor i.
+template <int CAP> struct Batch {
+  Tensor t[CAP];
+  int32_t chunk0[CAP + 1];
+  uint8_t fp32[CAP];       // bit 0: the gradient, bit 1: its destination
+  int32_t count;
+};
+
+// 16 values at p[0 .. 16), those from index n on 0.
+__device__ __forceinline__ void load16(const float* p, int64_t n, bool wide, float (&v)[16]) {
+  if (n >= 16 && wide) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=f"(v[8 * i]), "=f"(v[8 * i + 1]), "=f"(v[8 * i + 2]), "=f"(v[8 * i + 3]), "=f"(v[8 * i + 4]),
+                     "=f"(v[8 * i + 5]), "=f"(v[8 * i + 6]), "=f"(v[8 * i + 7]) : "l"(p + 8 * i) : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = i < n ? p[i] : 0.0f;
+  }
+}
+__device__ __forceinline__ void load16(const uint16_t* p, int64_t n, bool wide, float (&v)[16]) {
+  if (n >= 16 && wide) {
+    uint32_t w[8];
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p) : "memory");
+    unpack_bf16x16(w, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = i < n ? __uint_as_float(static_cast<uint32_t>(p[i]) << 16) : 0.0f;
+  }
+}
+__device__ __forceinline__ void store16(float* p, int64_t n, bool wide, const float (&v)[16]) {
+  if (n >= 16 && wide) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      st_global_v8(p + 8 * i, __float_as_uint(v[8 * i]), __float_as_uint(v[8 * i + 1]), __float_as_uint(v[8 * i + 2]),
+                   __float_as_uint(v[8 * i + 3]), __float_as_uint(v[8 * i + 4]), __float_as_uint(v[8 * i + 5]),
+                   __float_as_uint(v[8 * i + 6]), __float_as_uint(v[8 * i + 7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) if (i < n) p[i] = v[i];
+  }
+}
+__device__ __forceinline__ void store16(uint16_t* p, int64_t n, bool wide, const float (&v)[16]) {
+  if (n >= 16 && wide) {
+    st_global_v8(p, pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]), pack_bf16x2_rn(v[4], v[5]),
+                 pack_bf16x2_rn(v[6], v[7]), pack_bf16x2_rn(v[8], v[9]), pack_bf16x2_rn(v[10], v[11]),
+                 pack_bf16x2_rn(v[12], v[13]), pack_bf16x2_rn(v[14], v[15]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) p[i] = static_cast<uint16_t>(pack_bf16x2_rn(v[i], 0.0f));
+  }
+}
+
+__device__ __forceinline__ bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
+
+// |v| as an integer: ordered as the values are, NaN above infinity.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// The sum of the squares of 64 values.
+__device__ __forceinline__ double squares(const float (&v)[kPieces][16]) {
+  float s[4] = {};
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) s[j & 3] = fmaf(v[i][j], v[i][j], s[j & 3]);
+  const float sum = (s[0] + s[1]) + (s[2] + s[3]);
+  // below 2^-90 squares may have been lost under FP32's smallest value, above
+  // 2^126 their sum may have left its range
+  if (sum >= 0x1p-90f && sum < 0x1p126f) return static_cast<double>(sum);
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) m = max(m, magnitude(v[i][j]));
+  if (m == 0) return 0.0;
+  const bool large = m >= 0x3F800000u;             // 1
+  const float up = large ? 0x1p-70f : 0x1p100f;
+  float r = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float x = v[i][j] * up;
+      r = fmaf(x, x, r);
+    }
+  return static_cast<double>(r) * (large ? 0x1p140 : 0x1p-200);
+}
+
+// A chunk's tensor: the last one that starts at or before it.
+template <int CAP> __device__ __forceinline__ int tensor_of(const Batch<CAP>& b, int64_t chunk) {
+  int lo = 0, hi = b.count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (b.chunk0[mid] <= chunk) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+template <typename T>
+__device__ __forceinline__ void load_chunk(const T* p, int64_t left, float (&v)[kPieces][16]) {
+  const bool wide = aligned32(p);
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int64_t at = (static_cast<int64_t>(i) * kThreads + threadIdx.x) * kPiece;
+    load16(p + at, left - at, wide, v[i]);
+  }
+}
+
+// The sum, or the largest, over a block, in a fixed order (thread 0's result).
+template <bool MAX> __device__ __forceinline__ double join(double a, double b) {
+  if constexpr (MAX) return (a >= b || a != a) ? a : b;   // NaN stays
+  else return a + b;
+}
+template <bool MAX> __device__ __forceinline__ double block_join(double v) {
+  __shared__ double s[kThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = join<MAX>(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    for (int w = 1; w < kThreads / 32; ++w) v = join<MAX>(v, s[w]);
+  return v;
+}
+
+template <int CAP, bool MAX>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_kernel(const __grid_constant__ Batch<CAP> b,
+                                                                      double* __restrict__ partial) {
+  pdl_wait();
+  const int64_t chunks = b.chunk0[b.count];
+  double acc = 0.0;
+  uint32_t most = 0;
+  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const int i = tensor_of(b, c);
+    const int64_t base = (c - b.chunk0[i]) * kChunk;
+    float v[kPieces][16];
+    if (b.fp32[i] & 1) load_chunk(static_cast<const float*>(b.t[i].g) + base, b.t[i].n - base, v);
+    else load_chunk(static_cast<const uint16_t*>(b.t[i].g) + base, b.t[i].n - base, v);
+    if constexpr (MAX) {
+#pragma unroll
+      for (int p = 0; p < kPieces; ++p)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) most = max(most, magnitude(v[p][j]));
+    } else {
+      acc += squares(v);
+    }
+  }
+  if constexpr (MAX) acc = static_cast<double>(__uint_as_float(most));
+  const double total = block_join<MAX>(acc);
+  if (threadIdx.x == 0) partial[blockIdx.x] = total;
+}
+
+// Norm and factor from the partial sums; every block that asks gets the same.
+template <bool MAX>
+__device__ __forceinline__ void finish(const double* partial, int n, double max_norm, float* norm, float* factor) {
+  double v = 0.0;
+  for (int i = threadIdx.x; i < n; i += kThreads) v = join<MAX>(v, partial[i]);
+  const double total = block_join<MAX>(v);
+  if (threadIdx.x == 0) {
+    const double r = MAX ? total : sqrt(total);
+    const double f = max_norm / (r + 1e-6);
+    if (norm) *norm = static_cast<float>(r);
+    if (factor) *factor = f > 1.0 ? 1.0f : static_cast<float>(f);   // NaN stays
+  }
+}
+
+template <bool MAX>
+__global__ void __launch_bounds__(kThreads) finish_kernel(const double* partial, int n, double max_norm, float* norm,
+                                                          float* factor) {
+  pdl_wait();
+  finish<MAX>(partial, n, max_norm, norm, factor);
+}
+
+template <typename G, typename O>
+__device__ __forceinline__ void scale_chunk(const Tensor& t, int64_t base, float f) {
+  const G* g = static_cast<const G*>(t.g) + base;
+  O* o = static_cast<O*>(t.out) + base;
+  const int64_t left = t.n - base;
+  const bool wide = aligned32(o);
+  float v[kPieces][16];
+  load_chunk(g, left, v);
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const int64_t at = (static_cast<int64_t>(i) * kThreads + threadIdx.x) * kPiece;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[i][j] *= f;
+    store16(o + at, left - at, wide, v[i]);
+  }
+}
+
+// in_place: every destination is its gradient, and a factor of 1 changes nothing.
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) clip_kernel(const __grid_constant__ Batch<CAP> b,
+                                                                      const float* __restrict__ factor, bool in_place) {
+  pdl_wait();
+  const float f = *factor;
+  if (in_place && f == 1.0f) return;
+  const int64_t chunks = b.chunk0[b.count];
+  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const int i = tensor_of(b, c);
+    const int64_t base = (c - b.chunk0[i]) * kChunk;
+    switch (b.fp32[i]) {
+      case 0: scale_chunk<uint16_t, uint16_t>(b.t[i], base, f); break;
+      case 1: scale_chunk<float, uint16_t>(b.t[i], base, f); break;
+      case 2: scale_chunk<uint16_t, float>(b.t[i], base, f); break;
+      default: scale_chunk<float, float>(b.t[i], base, f); break;
+    }
+  }
+}
+
+constexpr int kSmall = 128, kLarge = 1000;   // tensors of a launch
+
+inline int grid_of(int64_t chunks) {
+  int64_t cap = static_cast<int64_t>(num_sms()) * kBlocksPerSm;
+  if (cap > kMaxBlocks) cap = kMaxBlocks;
+  return static_cast<int>(chunks < cap ? chunks : cap);
+}
+
+// As many tensors as a launch takes into a batch; the next one's index.
+template <int CAP>
+int64_t fill(Batch<CAP>& b, const minite_grad_tensor* t, int64_t i, int64_t n) {
+  int64_t chunks = 0;
+  b.count = 0;
+  for (; i < n && b.count < CAP; ++i) {
+    if (t[i].n == 0) continue;
+    const int64_t c = (t[i].n + kChunk - 1) / kChunk;
+    if (b.count > 0 && chunks + c > 0x7FFFFFFF) break;
+    b.t[b.count] = {t[i].grad, t[i].out, t[i].n};
+    b.fp32[b.count] = static_cast<uint8_t>((t[i].grad_dtype == MINITE_OUT_FP32 ? 1 : 0) |
+                                           (t[i].out_dtype == MINITE_OUT_FP32 ? 2 : 0));
+    b.chunk0[b.count++] = static_cast<int32_t>(chunks);
+    chunks += c;
+  }
+  b.chunk0[b.count] = static_cast<int32_t>(chunks);
+  return i;
+}
+
+// `launch` for the tensors in batches of up to CAP.
+template <int CAP, typename Launch>
+cudaError_t in_batches(const minite_grad_tensor* t, int64_t n, Launch launch) {
+  static_assert(sizeof(Batch<kSmall>) <= 4096 && sizeof(Batch<kLarge>) + 64 <= 32764, "parameters");
+  Batch<CAP> b;
+  for (int64_t i = 0; i < n;) {
+    i = fill(b, t, i, n);
+    if (b.count == 0) break;
+    const cudaError_t e = launch(b, grid_of(b.chunk0[b.count]));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+int64_t launches_of(int64_t n) { return n <= kSmall ? 1 : (n + kLarge - 1) / kLarge; }
+
+template <int CAP, bool MAX>
+cudaError_t norm_as(const minite_grad_tensor* t, int64_t n, double max_norm, float* norm, float* factor,
+                    double* partial, cudaStream_t s) {
+  int parts = 0;
+  cudaError_t e = in_batches<CAP>(t, n, [&](const Batch<CAP>& b, int grid) {
+    const cudaError_t r = launch_pdl(norm_kernel<CAP, MAX>, dim3(grid), dim3(kThreads), 0, s, b, partial + parts);
+    parts += grid;
+    return r;
+  });
+  if (e != cudaSuccess) return e;
+  return launch_pdl(finish_kernel<MAX>, dim3(1), dim3(kThreads), 0, s, static_cast<const double*>(partial), parts,
+                    max_norm, norm, factor);
+}
+
+template <int CAP>
+cudaError_t clip_as(const minite_grad_tensor* t, int64_t n, const float* factor, bool in_place, cudaStream_t s) {
+  return in_batches<CAP>(t, n, [&](const Batch<CAP>& b, int grid) {
+    return launch_pdl(clip_kernel<CAP>, dim3(grid), dim3(kThreads), 0, s, b, factor, in_place);
+  });
+}
+
+bool dtype_ok(int d) { return d == MINITE_OUT_BF16 || d == MINITE_OUT_FP32; }
+
+int check(const minite_grad_tensor* t, int64_t n, bool out) {
+  if (n < 0 || (n > 0 && !t)) return MINITE_ERR_INVALID_ARG;
+  if (n > (int64_t(1) << 24)) return MINITE_ERR_UNSUPPORTED_SHAPE;
+  for (int64_t i = 0; i < n; ++i) {
+    if (t[i].n < 0 || t[i].n >= (int64_t(1) << 42)) return MINITE_ERR_UNSUPPORTED_SHAPE;
+    if (!dtype_ok(t[i].grad_dtype) || (out && !dtype_ok(t[i].out_dtype))) return MINITE_ERR_INVALID_ARG;
+    if (t[i].n == 0) continue;
+    if (!t[i].grad || !aligned(t[i].grad, t[i].grad_dtype == MINITE_OUT_FP32 ? 4 : 2)) return MINITE_ERR_INVALID_ARG;
+    if (out && (!t[i].out || !aligned(t[i].out, t[i].out_dtype == MINITE_OUT_FP32 ? 4 : 2) ||
+                (t[i].out == t[i].grad && t[i].out_dtype != t[i].grad_dtype)))
+      return MINITE_ERR_INVALID_ARG;
+  }
+  return MINITE_OK;
+}
+
+}  // namespace gradnorm
+
+size_t grad_norm_workspace_bytes(int64_t n_tensors) {
+  return static_cast<size_t>(gradnorm::launches_of(n_tensors)) * gradnorm::kMaxBlocks * sizeof(double);
+}
+
+}  // namespace minite
+
+using namespace minite;
+
+extern "C" int minite_grad_norm(const minite_grad_tensor* tensors, int64_t n_tensors, int order, double max_norm,
+                                float* norm, float* factor, void* workspace, size_t ws_bytes,
+                                minite_stream_t stream) {
+  using namespace gradnorm;
+  const int rc = check(tensors, n_tensors, false);
+  if (rc != MINITE_OK) return rc;
+  if ((order != MINITE_NORM_2 && order != MINITE_NORM_MAX) || !(max_norm >= 0.0) || (!norm && !factor) ||
+      !aligned(norm, 4) || !aligned(factor, 4) || !workspace || !aligned(workspace, 8) ||
+      ws_bytes < grad_norm_workspace_bytes(n_tensors))
+    return MINITE_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  double* p = static_cast<double*>(workspace);
+  cudaError_t e;
+  if (n_tensors <= kSmall)
+    e = order == MINITE_NORM_2 ? norm_as<kSmall, false>(tensors, n_tensors, max_norm, norm, factor, p, s)
+                               : norm_as<kSmall, true>(tensors, n_tensors, max_norm, norm, factor, p, s);
+  else
+    e = order == MINITE_NORM_2 ? norm_as<kLarge, false>(tensors, n_tensors, max_norm, norm, factor, p, s)
+                               : norm_as<kLarge, true>(tensors, n_tensors, max_norm, norm, factor, p, s);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MINITE_OK : MINITE_ERR_CUDA;
+}
+
+extern "C" int minite_clip_grads(const minite_grad_tensor* tensors, int64_t n_tensors, const float* factor,
+                                 minite_stream_t stream) {
+  using namespace gradnorm;
+  const int rc = check(tensors, n_tensors, true);
+  if (rc != MINITE_OK) return rc;
+  if (!factor || !aligned(factor, 4)) return MINITE_ERR_INVALID_ARG;
+  bool in_place = true;
+  for (int64_t i = 0; i < n_tensors; ++i) in_place &= tensors[i].n == 0 || tensors[i].out == tensors[i].grad;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = n_tensors <= kSmall ? clip_as<kSmall>(tensors, n_tensors, factor, in_place, s)
+                                            : clip_as<kLarge>(tensors, n_tensors, factor, in_place, s);
+  return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MINITE_OK : MINITE_ERR_CUDA;
+}

@@ -89,7 +89,7 @@ constexpr int kRankWarps = 4;  // chunks per block
 __global__ void __launch_bounds__(32 * kRankWarps) permute_rank_kernel(
     const int32_t* __restrict__ ids, int64_t T, int k, int E, int ct, int nchunks,
     int32_t* __restrict__ table, int32_t* __restrict__ dest_row, uint32_t* __restrict__ counter,
-    int32_t* status) {
+    bool negative_ok, int32_t* status) {
   pdl_wait();
   extern __shared__ int32_t cnt_all[];  // [kRankWarps][E]
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(32 * kRankWarps) permute_rank_kernel(
     const int p = b + lane;
     const int e = ids_r[r];
     const bool valid = e >= 0 && e < E;
-    if (p < npairs && !valid) bad = true;
+    if (p < npairs && !valid && !(negative_ok && e < 0)) bad = true;
     const uint32_t mask = __match_any_sync(0xffffffffu, valid ? e : E + lane);
     const int before = __popc(mask & ((1u << lane) - 1u));
     const int run = valid ? cnt[e] : 0;
@@ -195,15 +195,37 @@ __global__ void __launch_bounds__(kPermThreads) permute_scan_kernel(
     const int ex_pad = block_exclusive_scan((cnt + 127) & ~127, warp_sums, &tot_pad);
     if (i < E) {
       expert_offsets[i] = off + ex;
-      sf_row_offsets[i] = sfoff + ex_pad;
+      if (sf_row_offsets) sf_row_offsets[i] = sfoff + ex_pad;
     }
     off += tot;
     sfoff += tot_pad;
   }
   if (threadIdx.x == 0) {
     expert_offsets[E] = off;
-    sf_row_offsets[E] = sfoff;
+    if (sf_row_offsets) sf_row_offsets[E] = sfoff;
   }
+}
+
+// The ranking and scan alone, for permutations that place rows themselves: a
+// pair's row is expert_offsets[e] + table[e][t / ct] + rank[pair]. A negative id
+// is a slot that is not used, without a status bit. Any T >= 1, E <= 1024, k <= 32.
+size_t routing_workspace_bytes(int64_t T, int E, int k) {
+  return perm_ws_base_bytes(T, E, k) + align256(static_cast<size_t>(T) * k * 4);
+}
+void launch_routing(const int32_t* ids, int64_t T, int k, int E, void* workspace,
+                    int32_t* expert_offsets, const int32_t** table, const int32_t** rank, int* ct,
+                    int* nchunks, int32_t* status, cudaStream_t s) {
+  const PermWs w = perm_ws(workspace, T, 0, E, k, false);
+  int32_t* r = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + perm_ws_base_bytes(T, E, k));
+  *ct = permute_chunk_tokens(k);
+  *nchunks = static_cast<int>((T + *ct - 1) / *ct);
+  *table = w.table;
+  *rank = r;
+  launch_pdl(permute_rank_kernel, dim3((*nchunks + kRankWarps - 1) / kRankWarps), dim3(32 * kRankWarps),
+             kRankWarps * E * sizeof(int32_t), s, ids, T, k, E, *ct, *nchunks, w.table, r, w.counter,
+             true, status);
+  launch_pdl(permute_scan_kernel, dim3(E), dim3(kPermThreads), 0, s, w.table, *nchunks, E, w.counter,
+             w.totals, expert_offsets, static_cast<int32_t*>(nullptr));
 }
 
 // Quantize and scatter, one warp per token over a grid of resident blocks:
@@ -530,7 +552,7 @@ static int permute_quant_impl(const void* x, const int32_t* topk_ids, const floa
   const int rank_blocks = (nchunks + kRankWarps - 1) / kRankWarps;
   launch_pdl(permute_rank_kernel, dim3(rank_blocks), dim3(32 * kRankWarps),
              kRankWarps * E * sizeof(int32_t), s, topk_ids, T, static_cast<int>(k),
-             static_cast<int>(E), ct, nchunks, w.table, dest_row, w.counter, status);
+             static_cast<int>(E), ct, nchunks, w.table, dest_row, w.counter, false, status);
   launch_pdl(permute_scan_kernel, dim3(E), dim3(kPermThreads), 0, s, w.table, nchunks,
              static_cast<int>(E), w.counter, w.totals, expert_offsets, sf_row_offsets);
   const int rc = launch_quant_gather(x, topk_ids, T, H, E, k, expert_offsets, sf_row_offsets,

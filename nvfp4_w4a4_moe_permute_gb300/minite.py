@@ -10,7 +10,9 @@ every call raises ``MiniteError``.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+from array import array
 
 import numpy as np
 import torch
@@ -21,7 +23,8 @@ SCALE_PER_ROW, SCALE_PER_GROUP = 0, 1
 ALONG_COLS, ALONG_ROWS = 0, 1
 OUT_BF16, OUT_FP32 = 0, 1
 OP_QUANTIZE, OP_PERMUTE_QUANT, OP_COMBINE_BACKWARD_QUANT, OP_QUANTIZE_TOKENS = 0, 1, 2, 3
-OP_GATE_UP_SWIGLU = 4
+OP_GATE_UP_SWIGLU, OP_PERMUTE_ROWS, OP_GRAD_NORM, OP_VERIFY_DRAFTS = 4, 5, 6, 7
+NORM_2, NORM_MAX = 0, 1
 W_NK, W_KN = 0, 1
 ERR_TIMEOUT, ERR_BAD_ROUTING, ERR_BAD_TOKEN = 4, 5, 7
 
@@ -37,6 +40,9 @@ EXPORTS = [
     "minite_swiglu_backward_quant_keep", "minite_gate_up_swiglu_quant_nvfp4",
     "minite_grouped_gemm_bf16", "minite_grouped_wgrad_bf16", "minite_token_logprobs",
     "minite_token_logprobs_backward", "minite_adamw_step", "minite_test_adamw_math",
+    "minite_moe_permute_rows", "minite_moe_spread_rows", "minite_moe_combine_rows",
+    "minite_moe_combine_rows_backward", "minite_grad_norm", "minite_clip_grads",
+    "minite_verify_drafts",
 ]
 
 
@@ -94,6 +100,17 @@ def load(path: str | None = None):
                                            _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp],
         "minite_adamw_step": [_vp, _i64, _int, _int, _int] + [ctypes.c_double] * 5 +
                              [_i64, _vp, _vp],
+        "minite_moe_permute_rows": [_vp, _int, _i64, _vp, _i64, _i64, _i32, _i32, _vp, _i64, _vp, _vp, _vp,
+                                    _vp, _sz, _vp, _vp],
+        "minite_moe_spread_rows": [_vp, _int, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _i64, _vp, _vp],
+        "minite_moe_combine_rows": [_vp, _int, _i64, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _i64, _vp,
+                                    _vp],
+        "minite_moe_combine_rows_backward": [_vp, _int, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i64,
+                                             _i32, _vp, _i64, _vp, _vp, _vp],
+        "minite_grad_norm": [_vp, _i64, _int, ctypes.c_double, _vp, _vp, _vp, _sz, _vp],
+        "minite_clip_grads": [_vp, _i64, _vp, _vp],
+        "minite_verify_drafts": [_vp, _int, _i64, _vp, _int, _i64, _vp, _vp, _vp, _i64, _i64, _i32, _i64,
+                                 ctypes.c_float, _vp, _vp, _vp, _vp, _sz, _vp, _vp],
         "minite_test_convert": [_vp, _i64, _vp, _vp, _vp, _vp],
         "minite_test_div6_exhaustive": [_vp, _vp],
         "minite_test_adamw_math": [_vp, _vp],
@@ -545,6 +562,169 @@ def minite_token_logprobs_backward(logits, targets, stats, entropy, grad_logprob
         _check(rc, name)
 
 
+def _int32(t, shape, name, what, dev):
+    """Address of an int32 tensor of this shape on this device."""
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise MiniteError(f"{name}: {what} is int32 {list(shape)}, contiguous")
+    return _ptr(t, dev)
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _same_type(name, *tensors):
+    if any(t is not None and t.dtype is not tensors[0].dtype for t in tensors):
+        raise MiniteError(f"{name}: the matrices have one type")
+
+
+def minite_moe_permute_rows(x, topk_ids, E, rows, expert_offsets, perm_src, dest_row, workspace,
+                            status=None, stream=None):
+    """x [T, H] and rows [T*k, H] bf16 or fp32; topk_ids, dest_row int32 [T, k]; perm_src int32 [T*k]."""
+    name = "minite_moe_permute_rows"
+    T, H = _shape(x, 2, name, "x")
+    k = _shape(topk_ids, 2, name, "topk_ids")[1]
+    _same_type(name, x, rows)
+    if rows.shape != (T * k, H):
+        raise MiniteError(f"{name}: rows is [T * k, H]")
+    d = _device(x)
+    rc = load().minite_moe_permute_rows(
+        x.data_ptr(), _dtype(x, name), _rows(x, name), _int32(topk_ids, (T, k), name, "topk_ids", d), T, H, E, k,
+        _ptr(rows, d), _rows(rows, name), _offsets(expert_offsets, E, name, d),
+        _int32(perm_src, (T * k,), name, "perm_src", d), _int32(dest_row, (T, k), name, "dest_row", d),
+        _ptr(workspace, d), _bytes(workspace), _status(status, name, d), _raw(stream, d))
+    if rc:
+        _check(rc, name)
+
+
+def minite_moe_spread_rows(x, dest_row, rows, status=None, stream=None):
+    """x [T, H] and rows [M, H] bf16 or fp32; dest_row int32 [T, k]."""
+    name = "minite_moe_spread_rows"
+    T, H = _shape(x, 2, name, "x")
+    k = _shape(dest_row, 2, name, "dest_row")[1]
+    _same_type(name, x, rows)
+    M, Hr = _shape(rows, 2, name, "rows")
+    if Hr != H:
+        raise MiniteError(f"{name}: shapes of x and rows do not match")
+    d = _device(x)
+    rc = load().minite_moe_spread_rows(
+        x.data_ptr(), _dtype(x, name), _rows(x, name), _int32(dest_row, (T, k), name, "dest_row", d), T, M, H, k,
+        _ptr(rows, d), _rows(rows, name), _status(status, name, d), _raw(stream, d))
+    if rc:
+        _check(rc, name)
+
+
+def minite_moe_combine_rows(rows, dest_row, weights, y, status=None, stream=None):
+    """rows [M, H] and y [T, H] bf16 or fp32; dest_row int32, weights fp32 (or None) [T, k]."""
+    name = "minite_moe_combine_rows"
+    M, H = _shape(rows, 2, name, "rows")
+    T, k = _shape(dest_row, 2, name, "dest_row")
+    _same_type(name, rows, y)
+    if y.shape != (T, H):
+        raise MiniteError(f"{name}: y is [T, H]")
+    d = _device(rows)
+    rc = load().minite_moe_combine_rows(
+        rows.data_ptr(), _dtype(rows, name), _rows(rows, name), _int32(dest_row, (T, k), name, "dest_row", d),
+        _f32(weights, (T, k), name, "weights", d), T, M, H, k, _ptr(y, d), _rows(y, name),
+        _status(status, name, d), _raw(stream, d))
+    if rc:
+        _check(rc, name)
+
+
+def minite_moe_combine_rows_backward(dy, rows, dest_row, weights, drows, dweights, status=None, stream=None):
+    """dy [T, H], rows (or None, with dweights None) and drows [M, H] bf16 or fp32; dest_row int32,
+    weights and dweights fp32 [T, k]."""
+    name = "minite_moe_combine_rows_backward"
+    T, H = _shape(dy, 2, name, "dy")
+    k = _shape(dest_row, 2, name, "dest_row")[1]
+    _same_type(name, dy, rows, drows)
+    M, Hr = _shape(drows, 2, name, "drows")
+    if Hr != H or (rows is not None and rows.shape != (M, H)):
+        raise MiniteError(f"{name}: shapes of dy, rows and drows do not match")
+    d = _device(dy)
+    rc = load().minite_moe_combine_rows_backward(
+        dy.data_ptr(), _dtype(dy, name), _rows(dy, name), _ptr(rows, d), 0 if rows is None else _rows(rows, name),
+        _int32(dest_row, (T, k), name, "dest_row", d), _f32(weights, (T, k), name, "weights", d), T, M, H, k,
+        _ptr(drows, d), _rows(drows, name), _f32(dweights, (T, k), name, "dweights", d), _status(status, name, d),
+        _raw(stream, d))
+    if rc:
+        _check(rc, name)
+
+
+def _grad_table(grads, outs, name):
+    """struct minite_grad_tensor of every gradient (and destination), and the device."""
+    if len(grads) == 0:
+        raise MiniteError(f"{name}: needs gradients")
+    if len(outs) != len(grads):
+        raise MiniteError(f"{name}: one destination a gradient")
+    d = _device(grads[0])
+    table = array("q")
+    for g, o in zip(grads, outs):
+        n = g.numel()
+        if not (g.is_contiguous() and o.is_contiguous()) or o.numel() != n:
+            raise MiniteError(f"{name}: gradients are contiguous, and destinations contiguous and of their size")
+        if g.get_device() != d or o.get_device() != d:
+            raise _elsewhere("tensor", g.get_device() if g.get_device() != d else o.get_device(), d)
+        at = g.data_ptr()
+        table.extend((at, at if o is g else o.data_ptr(), n, _dtype(g, name) | _dtype(o, name) << 32))
+    return table, d
+
+
+def minite_grad_norm(grads, order, max_norm, norm, factor, workspace, stream=None):
+    """grads: contiguous bf16 or fp32 tensors; norm and factor fp32 [1], one of them may be None."""
+    name = "minite_grad_norm"
+    table, d = _grad_table(grads, grads, name)
+    rc = load().minite_grad_norm(table.buffer_info()[0], len(grads), order, max_norm,
+                                 _f32(norm, (1,), name, "norm", d), _f32(factor, (1,), name, "factor", d),
+                                 _ptr(workspace, d), _bytes(workspace), _raw(stream, d))
+    if rc:
+        _check(rc, name)
+
+
+def minite_clip_grads(grads, outs, factor, stream=None):
+    """outs[i] = grads[i] * factor; outs[i] may be grads[i]; factor fp32 [1]."""
+    name = "minite_clip_grads"
+    table, d = _grad_table(grads, outs, name)
+    rc = load().minite_clip_grads(table.buffer_info()[0], len(grads), _f32(factor, (1,), name, "factor", d),
+                                  _raw(stream, d))
+    if rc:
+        _check(rc, name)
+
+
+def _sequence_rows(t, name, what):
+    """Row stride of [B, R, V] whose B * R rows are contiguous and evenly spaced."""
+    B, R, V = _shape(t, 3, name, what)
+    s0, s1, s2 = t.stride()
+    ld = s1 if R > 1 else s0 if B > 1 else V
+    if (V > 1 and s2 != 1) or ld < V or (R > 1 and B > 1 and s0 != R * s1):
+        raise MiniteError(f"{name}: {what} has contiguous rows that are evenly spaced")
+    return ld
+
+
+def minite_verify_drafts(target, draft, draft_tokens, uniforms, noise, temperature, tokens, accepted, logprobs,
+                         workspace, status=None, stream=None):
+    """target [B, S + 1, V], draft [B, S, V] (or None) bf16 or fp32; draft_tokens int32 and uniforms
+    fp32 [B, S]; noise fp32 [B, V]; tokens int32 and logprobs (or None) fp32 [B, S + 1]; accepted int32 [B]."""
+    name = "minite_verify_drafts"
+    B, S1, V = _shape(target, 3, name, "target")
+    S = _shape(draft_tokens, 2, name, "draft_tokens")[1]
+    if S1 != S + 1 or (draft is not None and draft.shape != (B, S, V)):
+        raise MiniteError(f"{name}: target is [B, S + 1, V], draft [B, S, V], draft_tokens [B, S]")
+    if noise.dtype is not torch.float32 or noise.shape != (B, V):
+        raise MiniteError(f"{name}: noise is float32 [B, V]")
+    d = _device(target)
+    ld = _sequence_rows(target, name, "target")
+    rc = load().minite_verify_drafts(
+        target.data_ptr(), _dtype(target, name), ld, _ptr(draft, d), 0 if draft is None else _dtype(draft, name),
+        0 if draft is None else _sequence_rows(draft, name, "draft") if S else V,
+        _int32(draft_tokens, (B, S), name, "draft_tokens", d), _f32(uniforms, (B, S), name, "uniforms", d),
+        _ptr(noise, d), _rows(noise, name), B, S, V, temperature, _int32(tokens, (B, S1), name, "tokens", d),
+        _int32(accepted, (B,), name, "accepted", d), _f32(logprobs, (B, S1), name, "logprobs", d),
+        _ptr(workspace, d), _bytes(workspace), _status(status, name, d), _raw(stream, d))
+    if rc:
+        _check(rc, name)
+
+
 # struct minite_adamw_tensor
 ADAMW_TENSOR = np.dtype([("param", "u8"), ("grad", "u8"), ("exp_avg", "u8"), ("exp_avg_sq", "u8"),
                          ("exp_avg_scale", "u8"), ("exp_avg_sq_scale", "u8"), ("param_bf16", "u8"),
@@ -701,6 +881,103 @@ def token_logprobs_backward(logits, targets, forward, grad_logprob=None, grad_en
     minite_token_logprobs_backward(logits, targets, forward["stats"], forward["entropy"],
                                    grad_logprob, grad_entropy, out, temperature, status, stream)
     return out
+
+
+def _workspace(op, like, stream, a, b=0, E=0, k=0):
+    n = load().minite_workspace_bytes(op, a, b, E, k)
+    return _empty((n,), torch.uint8, like, stream) if n else None
+
+
+def permute_rows(x, topk_ids, E, into=None, status=None, stream=None):
+    """Rows of x [T, H] (bf16 or fp32) sorted by expert: rows[dest_row[t, j]] = x[t]
+    for every slot with an id in [0, E) (a negative one is not used). Returns
+    dict(rows [T*k, H], offsets [E + 1], perm_src [T*k], dest_row [T, k]); ``into``
+    is such a dict whose tensors are written again. Rows from offsets[E] on are
+    left as they were, their perm_src is -1."""
+    T, H = _shape(x, 2, "permute_rows", "x")
+    k = _shape(topk_ids, 2, "permute_rows", "topk_ids")[1]
+    if into is None:
+        into = dict(rows=_empty((T * k, H), x.dtype, x, stream), offsets=_empty((E + 1,), torch.int32, x, stream),
+                    perm_src=_empty((T * k,), torch.int32, x, stream),
+                    dest_row=_empty((T, k), torch.int32, x, stream))
+    minite_moe_permute_rows(x, topk_ids, E, into["rows"], into["offsets"], into["perm_src"], into["dest_row"],
+                            _workspace(OP_PERMUTE_ROWS, x, stream, T, 0, E, k), status, stream)
+    return into
+
+
+def permute_rows_backward(drows, dest_row, out=None, status=None, stream=None):
+    """The gradient of permute_rows' x: dx[t] = sum over slots of drows[dest_row[t, j]]."""
+    return combine_rows(drows, dest_row, None, out, status, stream)
+
+
+def spread_rows(x, dest_row, rows, status=None, stream=None):
+    """rows[dest_row[t, j]] = x[t] by a routing that is already there; returns ``rows``
+    (those that no slot names are left as they were)."""
+    minite_moe_spread_rows(x, dest_row, rows, status, stream)
+    return rows
+
+
+def combine_rows(rows, dest_row, weights=None, out=None, status=None, stream=None):
+    """y[t] = sum over slots of weights[t, j] * rows[dest_row[t, j]] (weights fp32
+    [T, k], None for 1), summed in FP32 in slot order. Returns [T, H]."""
+    if out is None:
+        H = _shape(rows, 2, "combine_rows", "rows")[1]
+        out = _empty((_shape(dest_row, 2, "combine_rows", "dest_row")[0], H), rows.dtype, rows, stream)
+    minite_moe_combine_rows(rows, dest_row, weights, out, status, stream)
+    return out
+
+
+def combine_rows_backward(dy, rows, dest_row, weights, out=None, status=None, stream=None):
+    """The gradients of combine_rows: (drows, dweights). ``out`` receives drows (it may be
+    ``rows``); its rows that no slot names are not written. With rows None (and
+    ``out`` given) the weights' gradient is left out: (drows, None)."""
+    if out is None:
+        if rows is None:
+            raise MiniteError("combine_rows_backward: needs rows or out")
+        out = _empty(tuple(rows.shape), rows.dtype, rows, stream)
+    dweights = None if rows is None else _empty(tuple(dest_row.shape), torch.float32, dy, stream)
+    minite_moe_combine_rows_backward(dy, rows, dest_row, weights, out, dweights, status, stream)
+    return out, dweights
+
+
+def grad_norm(grads, max_norm=math.inf, order=2.0, stream=None):
+    """The global norm of a list of gradients (bf16 and fp32 may be mixed), and the
+    factor min(1, max_norm / (norm + 1e-6)) for ``AdamW.step(grad_scale=)``:
+    dict(norm [1], scale [1]), on the device. order: 2 or math.inf (the largest |g|)."""
+    if order not in (2, math.inf):
+        raise MiniteError(f"grad_norm: order is 2 or inf, not {order}")
+    if len(grads) == 0:
+        raise MiniteError("grad_norm: needs gradients")
+    like = grads[0]
+    norm, scale = _empty((1,), torch.float32, like, stream), _empty((1,), torch.float32, like, stream)
+    minite_grad_norm(grads, NORM_2 if order == 2 else NORM_MAX, max_norm, norm, scale,
+                     _workspace(OP_GRAD_NORM, like, stream, len(grads)), stream)
+    return {"norm": norm, "scale": scale}
+
+
+def clip_grads(grads, max_norm, order=2.0, out=None, stream=None):
+    """Gradients times grad_norm's factor, in place or into the tensors ``out``
+    (of either type). Returns grad_norm's dict."""
+    r = grad_norm(grads, max_norm, order, stream)
+    minite_clip_grads(grads, grads if out is None else out, r["scale"], stream)
+    return r
+
+
+def verify_drafts(logits, draft_tokens, uniforms, noise, draft_logits=None, temperature=1.0, status=None,
+                  stream=None):
+    """Drafted tokens [B, S] int32 (negative: no more drafts) verified against the
+    target's logits [B, S + 1, V] with ``uniforms`` [B, S] in [0, 1) and exponential
+    variates ``noise`` [B, V]; ``draft_logits`` [B, S, V] is what the drafts were
+    sampled from at the same temperature, None where they were looked up. Returns
+    dict(tokens [B, S + 1], accepted [B], logprobs [B, S + 1]): the drafts that stand,
+    the token that follows them, -1."""
+    B, S1 = _shape(logits, 3, "verify_drafts", "logits")[:2]
+    S = _shape(draft_tokens, 2, "verify_drafts", "draft_tokens")[1]
+    tokens, accepted = _empty((B, S1), torch.int32, logits, stream), _empty((B,), torch.int32, logits, stream)
+    logprobs = _empty((B, S1), torch.float32, logits, stream)
+    minite_verify_drafts(logits, draft_logits, draft_tokens, uniforms, noise, temperature, tokens, accepted,
+                         logprobs, _workspace(OP_VERIFY_DRAFTS, logits, stream, B, S), status, stream)
+    return {"tokens": tokens, "accepted": accepted, "logprobs": logprobs}
 
 
 class AdamW:
