@@ -882,9 +882,10 @@ int minite_clip_grads(const minite_grad_tensor* tensors, int64_t n_tensors, cons
  *         token of weight above 0 whose variate is not wins).
  * tokens: device, int32 [B, S + 1]; accepted: device, int32 [B]; logprobs: device, float
  *         [B, S + 1] or NULL.
- * workspace: device, >= minite_workspace_bytes(MINITE_OP_VERIFY_DRAFTS, B, S, 0, 0)
+ * workspace: device, >= minite_workspace_bytes(MINITE_OP_VERIFY_DRAFTS, B, V, S, 0)
  *         bytes, 256-byte aligned, contents on entry ignored.
- * Shape rules: 0 <= S <= 31 (0: one token is sampled), 0 <= B <= 2^24, 1 <= V < 2^31.
+ * Shape rules: 0 <= S <= 31 (0: one token is sampled), B >= 0 (0: nothing is enqueued),
+ * B (2 S + 1) <= 2^24, 1 <= V < 2^31, B (S + 1) V <= 2^42; log2(e) / temperature fits FP32.
  */
 int minite_verify_drafts(const void* target, int target_dtype, int64_t target_stride,
                          const void* draft, int draft_dtype, int64_t draft_stride,
@@ -899,8 +900,8 @@ int minite_verify_drafts(const void* target, int target_dtype, int64_t target_st
  * a = T, b = H; MINITE_OP_QUANTIZE_TOKENS: a = E, b = source rows when
  * they are gathered and no row maxima are passed, else 0;
  * MINITE_OP_GATE_UP_SWIGLU: a = M_total, b = I; MINITE_OP_PERMUTE_ROWS: a = T, E,
- * k; MINITE_OP_GRAD_NORM: a = tensors; MINITE_OP_VERIFY_DRAFTS: a = B, b = S). 0
- * means none needed. */
+ * k; MINITE_OP_GRAD_NORM: a = tensors; MINITE_OP_VERIFY_DRAFTS: a = B, b = V, E =
+ * S). 0 means none needed. */
 size_t minite_workspace_bytes(int op, int64_t a, int64_t b, int32_t E, int32_t k);
 
 /* Static description of a status code. */

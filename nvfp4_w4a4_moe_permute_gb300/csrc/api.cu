@@ -13,7 +13,7 @@ size_t tokens_workspace_bytes(int32_t E, int64_t x_rows);
 size_t swiglu_fused_workspace_words(int64_t M, int64_t I);
 size_t routing_workspace_bytes(int64_t T, int E, int k);
 size_t grad_norm_workspace_bytes(int64_t n_tensors);
-size_t verify_workspace_bytes(int64_t B, int64_t S);
+size_t verify_workspace_bytes(int64_t B, int64_t S, int64_t V);
 
 int num_sms() {
   static std::atomic<int> cache[64];
@@ -119,7 +119,7 @@ extern "C" size_t minite_workspace_bytes(int op, int64_t a, int64_t b, int32_t E
     case MINITE_OP_GRAD_NORM:
       return a >= 0 ? grad_norm_workspace_bytes(a) : 0;
     case MINITE_OP_VERIFY_DRAFTS:
-      return (a > 0 && b >= 0) ? verify_workspace_bytes(a, b) : 0;
+      return (a > 0 && b > 0 && E >= 0) ? verify_workspace_bytes(a, E, b) : 0;
     default:
       return 0;
   }

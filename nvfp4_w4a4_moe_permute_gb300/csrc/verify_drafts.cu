@@ -10,10 +10,16 @@
 // A sample of weights r is argmax r_j / e_j for exponential variates e_j: the
 // variates' race, which needs neither the weights' sum nor an order of additions.
 //
-// The rows' maxima and sums come from the log probabilities' kernel, which
-// streams target and draft rows once. Here a cluster of CTAs per sequence looks
-// at every draft (each CTA for itself), then runs the race over its parts of
-// the one row that is sampled from.
+// Two launches. stats_kernel streams the rows that may matter (draft i's, and the
+// target's up to the position after the last draft) once, a CTA 32 KB of a row,
+// and leaves the largest logit and the sum of each such segment: no loop, the
+// whole segment is in registers between the two passes over it. race_kernel, a
+// number of CTAs a sequence, joins the segments of the sequence's rows, looks at
+// every draft (each CTA for itself) and runs the race over its part of the one row
+// that is sampled from; the CTAs' winners meet in one 64-bit maximum.
+//
+// Sums are kept without the maximum's own term, r = s - 1, and log s = log1p(r):
+// the log probability of an almost certain token is not lost beside the 1.
 #include <cmath>
 
 #include "common.cuh"
@@ -24,21 +30,26 @@ namespace verify {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kVectors = 4;       // 32-byte vectors a thread holds of its segment
+constexpr int kMaxDrafts = 31;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Params {
   const void* target;       // [B][S + 1][V]
   const void* draft;        // [B][S][V], or null
   int64_t target_ld, draft_ld, noise_ld;
-  const float2* target_stats;   // [B][S + 1] {largest logit, log of the sum}
-  const float2* draft_stats;    // [B][S]
   const int32_t* draft_tokens;  // [B][S]
   const float* uniforms;        // [B][S]
   const float* noise;           // [B][V]
   int64_t V;
   int S;
-  float inv_t, k2;
+  float inv_t, k2;          // 1 / T, log2(e) / T
+  int target_segs, draft_segs;
+  float2* target_part;      // [B][S + 1][target_segs] {largest logit, sum without one maximum}
+  float2* draft_part;       // [B][S][draft_segs]
+  unsigned long long* best; // [B] the race so far, zeroed by stats_kernel
+  uint32_t* arrived;        // [B] CTAs that have run their part, likewise
+  int ctas;                 // of a sequence in race_kernel
   int32_t* tokens;          // [B][S + 1]
   float* logprobs;          // [B][S + 1], or null
   int32_t* accepted;        // [B]
@@ -48,126 +59,364 @@ struct Params {
 __device__ __forceinline__ float value(float x) { return x; }
 __device__ __forceinline__ float value(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
 
-// Whether a row has probabilities: neither NaN, nor +inf, nor a logit above -inf missing.
-__device__ __forceinline__ bool usable(float2 st) { return fabsf(st.x) < INFINITY && fabsf(st.y) < INFINITY; }
-
-struct Row {
-  float m, shift, k2;   // largest logit, log2 of the sum, log2(e) / T
-  __device__ __forceinline__ Row(float2 st, float k) : m(st.x), shift(st.y * kLog2e), k2(k) {}
-  __device__ __forceinline__ float p(float x) const { return exp2f(fmaf(x - m, k2, -shift)); }
-};
-
-// A place in the race: larger weight / variate first, then the lower index. 0: no weight.
-__device__ __forceinline__ uint64_t place(float weight, float e, int64_t j) {
-  if (!(weight > 0.0f)) return 0;
-  const float v = e > 0.0f ? __fdiv_rn(weight, e) : INFINITY;
-  return (static_cast<uint64_t>(__float_as_uint(v)) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(j));
+// 2^x, within 2 units in the last place; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
-__device__ __forceinline__ uint64_t larger(uint64_t a, uint64_t b) { return a > b ? a : b; }
-__device__ __forceinline__ uint64_t warp_larger(uint64_t v) {
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+template <typename T> constexpr int kPerVec = 32 / static_cast<int>(sizeof(T));
+template <typename T> inline int segments(int64_t V) {
+  constexpr int64_t per = static_cast<int64_t>(kThreads) * kVectors * kPerVec<T>;
+  return static_cast<int>((V + per - 1) / per);
+}
+
+struct Vec { uint32_t w[8]; };
+__device__ __forceinline__ Vec load_vec(const void* p) {
+  Vec v;
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]),
+                 "=r"(v.w[7]) : "l"(p) : "memory");
+  return v;
+}
+template <typename T> __device__ __forceinline__ void values(const Vec& v, float (&x)[kPerVec<T>]) {
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = larger(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v.w[i]);
+  } else {
+    unpack_bf16x16(v.w, x);
+  }
+}
+
+// The largest of a thread's logits, NaN if there is one.
+template <typename T> __device__ __forceinline__ float max_of(const Vec (&v)[kVectors]) {
+  if constexpr (sizeof(T) == 4) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max_nan(m, __uint_as_float(v[i].w[j]));
+    return m;
+  } else {
+    uint32_t m = v[0].w[0];
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(v[i].w[j]));
+    return max_nan(bf16lo(m), bf16hi(m));
+  }
+}
+
+// A set of logits: the largest, and the sum of 2^((x - m) k) over the others. No
+// logit above -inf: m = -inf. NaN and +inf stay in m.
+__device__ __forceinline__ float2 join(float2 a, float2 b, float k) {
+  const float m = max_nan(a.x, b.x);
+  if (!(fabsf(m) < INFINITY)) return make_float2(m, 0.0f);
+  const float ca = ex2((a.x - m) * k), cb = ex2((b.x - m) * k);   // -inf: 0
+  float r = a.x == m && b.x == m ? 1.0f : 0.0f;   // one maximum of the two counts
+  r += a.x == m ? a.y : ca * (a.y + 1.0f);
+  r += b.x == m ? b.y : cb * (b.y + 1.0f);
+  return make_float2(m, r);
+}
+__device__ __forceinline__ float2 warp_join(float2 v, float k) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    float2 u;
+    u.x = __shfl_xor_sync(0xffffffffu, v.x, o);
+    u.y = __shfl_xor_sync(0xffffffffu, v.y, o);
+    v = join(v, u, k);
+  }
   return v;
 }
 
+// One segment of one row: its largest logit, then the sum over the others. Only the
+// warps that hold the largest look at every element for it; the rest add two
+// elements an instruction.
+template <typename T>
+__device__ __forceinline__ void segment(const T* row, int64_t V, int seg, int segs, float k, float2* out) {
+  __shared__ float s_max[kWarps], s_sum[kWarps];
+  constexpr int kPer = kPerVec<T>;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  // the row as a head up to a 32-byte boundary, vectors, and a tail
+  int head = static_cast<int>(((32 - (reinterpret_cast<uintptr_t>(row) & 31)) & 31) / sizeof(T));
+  if (head > V) head = static_cast<int>(V);
+  const int64_t nv = (V - head) / kPer;
+  const int tail = static_cast<int>(V - head - nv * kPer);
+  const int64_t v0 = static_cast<int64_t>(seg) * kThreads * kVectors + tid;
+  Vec v[kVectors];
+#pragma unroll
+  for (int i = 0; i < kVectors; ++i) {
+    if (v0 + i * kThreads < nv) {
+      v[i] = load_vec(row + head + (v0 + i * kThreads) * kPer);
+    } else {   // logits of -inf
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i].w[j] = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
+    }
+  }
+  float xh = -INFINITY, xt = -INFINITY;
+  if (seg == 0 && tid < head) xh = value(row[tid]);
+  if (seg == segs - 1 && tid < tail) xt = value(row[V - tail + tid]);
+  const float mine = max_nan(max_nan(xh, xt), max_of<T>(v));
+  float m = mine;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) s_max[wid] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) m = max_nan(m, s_max[w]);
+  if (!(fabsf(m) < INFINITY)) {   // no logit, or no probabilities
+    if (tid == 0) *out = make_float2(m, 0.0f);
+    return;
+  }
+  float r;
+  if (__any_sync(0xffffffffu, mine == m)) {
+    float n = 0.0f;
+    r = 0.0f;
+    auto add = [&](float x) {
+      if (x == m) n += 1.0f;
+      else r += ex2((x - m) * k);
+    };
+    add(xh);
+    add(xt);
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i) {
+      float x[kPer];
+      values<T>(v[i], x);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) add(x[j]);
+    }
+    // the lanes' counts, less the one maximum that is left out
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      r += __shfl_xor_sync(0xffffffffu, r, o);
+      n += __shfl_xor_sync(0xffffffffu, n, o);
+    }
+    bool first = true;
+    for (int w = 0; w < wid; ++w) first &= s_max[w] != m;
+    r += first ? n - 1.0f : n;
+  } else {
+    uint64_t acc = pair(ex2((xh - m) * k), ex2((xt - m) * k));
+    const uint64_t minus = pair(-m, -m), k2 = pair(k, k);
+#pragma unroll
+    for (int i = 0; i < kVectors; ++i) {
+      float x[kPer];
+      values<T>(v[i], x);
+#pragma unroll
+      for (int j = 0; j < kPer; j += 2) {
+        float a, b;
+        unpair(mul2(add2(pair(x[j], x[j + 1]), minus), k2), a, b);
+        acc = add2(acc, pair(ex2(a), ex2(b)));
+      }
+    }
+    float a, b;
+    unpair(acc, a, b);
+    r = a + b;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+  }
+  if (lane == 0) s_sum[wid] = r;
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < kWarps; ++w) r += s_sum[w];
+    *out = make_float2(m, r);
+  }
+}
+
 template <typename T, typename D>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const Params p, int cluster) {
-  __shared__ int s_n, s_falls;
-  __shared__ uint64_t s_best[kWarps][2];
-  __shared__ uint32_t s_all[kMaxCluster][4];   // every CTA's best, in the cluster's first CTA
-  cluster_arrive();   // every CTA runs before one writes to another's shared memory
+__global__ void __launch_bounds__(kThreads) stats_kernel(const Params p, int64_t B) {
   pdl_wait();
-  const int64_t b = blockIdx.x / cluster;
-  const int rank = blockIdx.x % cluster;
+  const int64_t target_units = B * (p.S + 1) * p.target_segs;
+  int64_t u = blockIdx.x;
+  if (u < target_units) {
+    const int64_t row = div_nonneg(u, p.target_segs);
+    const int seg = static_cast<int>(u - row * p.target_segs);
+    const int64_t b = div_nonneg(row, p.S + 1);
+    const int i = static_cast<int>(row - b * (p.S + 1));
+    if (i == 0 && seg == 0 && threadIdx.x == 0) {
+      p.best[b] = 0;
+      p.arrived[b] = 0;
+    }
+    if (i > 0) {   // a position behind a missing draft is not reached
+      const int x = p.draft_tokens[b * p.S + i - 1];
+      if (x < 0 || x >= p.V) return;
+    }
+    segment<T>(static_cast<const T*>(p.target) + row * p.target_ld, p.V, seg, p.target_segs, p.k2,
+               p.target_part + u);
+  } else {
+    u -= target_units;
+    const int64_t row = div_nonneg(u, p.draft_segs);
+    const int x = p.draft_tokens[row];
+    if (x < 0 || x >= p.V) return;
+    segment<D>(static_cast<const D*>(p.draft) + row * p.draft_ld, p.V,
+               static_cast<int>(u - row * p.draft_segs), p.draft_segs, p.k2, p.draft_part + u);
+  }
+}
+
+// A row's probabilities: p(x) = 2^((x - m) k - shift).
+struct Row {
+  float m, log_s;
+  __device__ __forceinline__ bool usable() const { return fabsf(m) < INFINITY && fabsf(log_s) < INFINITY; }
+  __device__ __forceinline__ float p(float x, float k, float shift) const { return ex2(fmaf(x - m, k, -shift)); }
+  __device__ __forceinline__ float p(float x, float k) const { return p(x, k, log_s * kLog2e); }
+};
+// From its segments, by a warp.
+__device__ __forceinline__ Row row_of(const float2* part, int segs, float k) {
+  float2 v = make_float2(-INFINITY, 0.0f);
+  for (int s = threadIdx.x & 31; s < segs; s += 32) v = join(v, part[s], k);
+  v = warp_join(v, k);
+  return {v.x, log1pf(v.y)};
+}
+
+// The race: the largest weight / variate, the lower index where they are equal.
+struct Lead {
+  float v = -1.0f;
+  int32_t j = 0;
+  __device__ __forceinline__ void offer(float weight, float e, int32_t at) {
+    if (!(weight > 0.0f)) return;
+    const float q = e > 0.0f ? __fdividef(weight, e) : INFINITY;   // within 2 units
+    if (q > v) {
+      v = q;
+      j = at;
+    }
+  }
+  __device__ __forceinline__ unsigned long long key() const {
+    return v < 0.0f ? 0ull : (static_cast<unsigned long long>(__float_as_uint(v)) << 32) |
+                                 (0xFFFFFFFFu - static_cast<uint32_t>(j));
+  }
+};
+__device__ __forceinline__ unsigned long long warp_larger(unsigned long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const unsigned long long u = __shfl_xor_sync(0xffffffffu, v, o);
+    v = u > v ? u : v;
+  }
+  return v;
+}
+
+constexpr int kAhead = 8;   // elements of a thread in flight
+
+// Elements [j0, j1) of the race. WITH_Q: less the draft's probabilities; otherwise
+// token `without` has none.
+template <bool WITH_Q, typename T, typename D>
+__device__ __forceinline__ Lead race(const T* xt, const D* xd, const float* noise, Row rt, Row rd, float k,
+                                     int32_t without, int64_t j0, int64_t j1) {
+  Lead lead;
+  const float st = rt.log_s * kLog2e, sd = rd.log_s * kLog2e;
+  for (int64_t base = j0 + threadIdx.x; base < j1; base += kThreads * kAhead) {
+    float a[kAhead], b[kAhead], e[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t j = base + i * kThreads;
+      if (j < j1) {
+        a[i] = value(xt[j]);
+        e[i] = noise[j];
+        if (WITH_Q) b[i] = value(xd[j]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t j = base + i * kThreads;
+      if (j < j1) {
+        float w = rt.p(a[i], k, st);
+        if (WITH_Q) w -= rd.p(b[i], k, sd);
+        else if (j == without) w = 0.0f;
+        lead.offer(w, e[i], static_cast<int32_t>(j));
+      }
+    }
+  }
+  return lead;
+}
+
+template <typename T, typename D>
+__global__ void __launch_bounds__(kThreads, 4) race_kernel(const Params p) {
+  __shared__ Row s_target[kMaxDrafts + 1], s_draft[kMaxDrafts + 1];
+  __shared__ uint8_t s_given[kMaxDrafts + 1], s_stands[kMaxDrafts + 1];
+  __shared__ unsigned long long s_best[kWarps];
+  __shared__ int s_last;
+  pdl_wait();
+  const int64_t b = div_nonneg(blockIdx.x, p.ctas);
+  const int rank = static_cast<int>(blockIdx.x - b * p.ctas);
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const T* target = static_cast<const T*>(p.target) + b * (p.S + 1) * p.target_ld;
   const D* draft = p.draft ? static_cast<const D*>(p.draft) + b * p.S * p.draft_ld : nullptr;
-  const float2* tst = p.target_stats + b * (p.S + 1);
-  const float2* dst = p.draft_stats + b * p.S;
   const int32_t* drafts = p.draft_tokens + b * p.S;
-  if (wid == 0) {   // lane i looks at draft i
-    int x = -1;
-    bool stands = false;
-    if (lane < p.S) {
-      x = drafts[lane];
-      if (x >= p.V) {
-        if (rank == 0) set_status(p.status, MINITE_ERR_BAD_TOKEN);
-        x = -1;
-      }
-      if (x >= 0 && usable(tst[lane]) && (!draft || usable(dst[lane]))) {
-        const float px = Row(tst[lane], p.k2).p(value(target[lane * p.target_ld + x]));
-        const float qx = draft ? Row(dst[lane], p.k2).p(value(draft[lane * p.draft_ld + x])) : 1.0f;
-        stands = p.uniforms[b * p.S + lane] * qx < px;
-      }
+  for (int i = wid; i <= p.S; i += kWarps) {   // a warp a position
+    const int before = i > 0 ? drafts[i - 1] : 0, x = i < p.S ? drafts[i] : -1;
+    const bool reached = before >= 0 && before < p.V, given = x >= 0 && x < p.V;
+    Row rt = {0.0f, 0.0f}, rd = {0.0f, 0.0f};
+    float xt = 0.0f, xd = 0.0f, u = 0.0f;
+    if (given) {   // asked for before the segments are waited for
+      xt = value(target[i * p.target_ld + x]);
+      if (draft) xd = value(draft[i * p.draft_ld + x]);
+      u = p.uniforms[b * p.S + i];
     }
-    const uint32_t none = ~__ballot_sync(0xffffffffu, x >= 0), out = ~__ballot_sync(0xffffffffu, stands);
-    const int given = none ? __ffs(none) - 1 : 32, n = out ? __ffs(out) - 1 : 32;   // S <= 31: never 32
+    if (reached) rt = row_of(p.target_part + (b * (p.S + 1) + i) * p.target_segs, p.target_segs, p.k2);
+    if (given && draft) rd = row_of(p.draft_part + (b * p.S + i) * p.draft_segs, p.draft_segs, p.k2);
     if (lane == 0) {
-      s_n = min(n, given);
-      s_falls = n < given;
+      bool stands = false;
+      if (reached && given && rt.usable() && rd.usable()) {
+        const float qx = draft ? rd.p(xd, p.k2) : 1.0f;
+        stands = u * qx < rt.p(xt, p.k2);
+      }
+      if (rank == 0 && x >= p.V) set_status(p.status, MINITE_ERR_BAD_TOKEN);
+      s_target[i] = rt;
+      s_draft[i] = rd;
+      s_given[i] = given;
+      s_stands[i] = stands;
     }
   }
   __syncthreads();
-  const int n = s_n;
-  const bool falls = s_falls;
-  const Row rt(tst[n], p.k2);
-  const bool ok = usable(tst[n]) && (!falls || !draft || usable(dst[n]));
-  uint64_t best = 0, best_p = 0;   // of what is left of p without q, and of p itself
-  if (ok) {
-    const T* xt = target + n * p.target_ld;
-    const float* e = p.noise + b * p.noise_ld;
-    const int64_t j0 = p.V * rank / cluster, j1 = p.V * (rank + 1) / cluster;
-    const int64_t drafted = falls && !draft ? drafts[n] : -1;
-    const bool with_q = falls && draft;
-    const Row rd(with_q ? dst[n] : make_float2(0.0f, 0.0f), p.k2);
-    const D* xd = with_q ? draft + n * p.draft_ld : nullptr;
-    for (int64_t j = j0 + threadIdx.x; j < j1; j += kThreads) {
-      const float w = rt.p(value(xt[j])), v = e[j];
-      best_p = larger(best_p, place(w, v, j));
-      float r = w;
-      if (with_q) r = w - rd.p(value(xd[j]));
-      else if (j == drafted) r = 0.0f;
-      best = larger(best, place(r, v, j));
-    }
+  int n = 0;   // drafts that stand
+  while (n < p.S && s_stands[n]) ++n;
+  const bool falls = n < p.S && s_given[n];   // draft n is there and does not
+  const Row rt = s_target[n], rd = s_draft[n];
+  const bool usable = rt.usable() && (!falls || rd.usable());
+  const T* xt = target + n * p.target_ld;
+  const float* noise = p.noise + b * p.noise_ld;
+  unsigned long long best = 0;
+  if (usable) {
+    const int64_t j0 = p.V * rank / p.ctas, j1 = p.V * (rank + 1) / p.ctas;
+    Lead lead;
+    if (falls && draft)
+      lead = race<true>(xt, draft + n * p.draft_ld, noise, rt, rd, p.k2, -1, j0, j1);
+    else
+      lead = race<false>(xt, xt, noise, rt, rt, p.k2, falls ? drafts[n] : -1, j0, j1);
+    best = warp_larger(lead.key());
   }
-  best = warp_larger(best);
-  best_p = warp_larger(best_p);
-  cluster_wait();
-  if (lane == 0) {
-    s_best[wid][0] = best;
-    s_best[wid][1] = best_p;
-  }
+  if (lane == 0) s_best[wid] = best;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int w = 1; w < kWarps; ++w) {
-      best = larger(best, s_best[w][0]);
-      best_p = larger(best_p, s_best[w][1]);
-    }
-    const uint32_t at = mapa_shared(smem_u32(&s_all[rank][0]), 0);
-    st_shared_cluster(at, static_cast<uint32_t>(best));
-    st_shared_cluster(at + 4, static_cast<uint32_t>(best >> 32));
-    st_shared_cluster(at + 8, static_cast<uint32_t>(best_p));
-    st_shared_cluster(at + 12, static_cast<uint32_t>(best_p >> 32));
+    for (int w = 1; w < kWarps; ++w) best = s_best[w] > best ? s_best[w] : best;
+    if (best) atomicMax(p.best + b, best);
+    __threadfence();
+    s_last = atomicAdd(p.arrived + b, 1u) == static_cast<uint32_t>(p.ctas) - 1;
   }
-  cluster_sync_all();
-  if (rank != 0 || wid != 0) return;
-  best = best_p = 0;
-  if (lane < cluster) {
-    best = s_all[lane][0] | static_cast<uint64_t>(s_all[lane][1]) << 32;
-    best_p = s_all[lane][2] | static_cast<uint64_t>(s_all[lane][3]) << 32;
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  best = *reinterpret_cast<volatile unsigned long long*>(p.best + b);
+  if (usable && best == 0) {   // q is as large as p everywhere but for roundings: p itself
+    best = warp_larger(race<false>(xt, xt, noise, rt, rt, p.k2, -1, 0, p.V).key());
+    if (lane == 0) s_best[wid] = best;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) best = s_best[w] > best ? s_best[w] : best;
   }
-  best = warp_larger(best);
-  best_p = warp_larger(best_p);
-  // q may be as large as p everywhere but for roundings: p itself then
-  const uint64_t key = best ? best : best_p;
-  const int32_t next = key ? static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(key)) : -1;
+  if (wid != 0) return;
+  const int32_t next = best ? static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(best)) : -1;
   if (lane == 0) p.accepted[b] = n;
   if (lane <= p.S) {
     const int32_t x = lane < n ? drafts[lane] : lane == n ? next : -1;
     p.tokens[b * (p.S + 1) + lane] = x;
     if (p.logprobs) {
       float lp = 0.0f;
-      if (x >= 0) lp = (value(target[lane * p.target_ld + x]) - tst[lane].x) * p.inv_t - tst[lane].y;
+      if (x >= 0) lp = (value(target[lane * p.target_ld + x]) - s_target[lane].m) * p.inv_t - s_target[lane].log_s;
       else if (lane == n) lp = __int_as_float(0x7FC00000);   // nothing to sample from
       p.logprobs[b * (p.S + 1) + lane] = lp;
     }
@@ -175,34 +424,35 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Params p, int cl
 }
 
 template <typename T, typename D>
-cudaError_t launch(const Params& p, int64_t B, cudaStream_t s) {
-  // enough CTAs a sequence to fill the SMs, with 2048 tokens each at least
-  int cluster = 1;
-  while (cluster < kMaxCluster && p.V >= 4096 * cluster && B * cluster < 4 * num_sms()) cluster *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(B * cluster));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, verify_kernel<T, D>, p, cluster);
+cudaError_t launch(Params& p, int64_t B, cudaStream_t s) {
+  const int64_t units = B * ((p.S + 1) * static_cast<int64_t>(p.target_segs) + static_cast<int64_t>(p.S) * p.draft_segs);
+  if (units > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  cudaError_t e = launch_pdl(stats_kernel<T, D>, dim3(static_cast<unsigned>(units)), dim3(kThreads), 0, s, p, B);
+  if (e != cudaSuccess) return e;
+  // CTAs of a sequence: one round of its threads' loads each where sequences are
+  // few, otherwise as many as are resident at once (the look at the drafts costs every
+  // CTA some 3 us)
+  int64_t ctas = (p.V + kThreads * kAhead - 1) / (kThreads * kAhead);
+  const int64_t fill = 4 * static_cast<int64_t>(num_sms()) / B > 1 ? 4 * static_cast<int64_t>(num_sms()) / B : 1;
+  if (ctas > fill) ctas = fill;
+  p.ctas = static_cast<int>(ctas);
+  return launch_pdl(race_kernel<T, D>, dim3(static_cast<unsigned>(B * ctas)), dim3(kThreads), 0, s, p);
 }
 
 inline size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+// Segments are counted for FP32 rows, which have the most.
+inline size_t target_bytes(int64_t B, int64_t S, int64_t V) {
+  return align256(static_cast<size_t>(B) * (S + 1) * segments<float>(V) * sizeof(float2));
+}
+inline size_t draft_bytes(int64_t B, int64_t S, int64_t V) {
+  return align256(static_cast<size_t>(B) * S * segments<float>(V) * sizeof(float2));
+}
 
 }  // namespace verify
 
-size_t verify_workspace_bytes(int64_t B, int64_t S) {
-  using verify::align256;
-  return align256(static_cast<size_t>(B) * (S + 1) * 8) + align256(static_cast<size_t>(B) * S * 8) +
-         align256(static_cast<size_t>(B) * S * 4);
+size_t verify_workspace_bytes(int64_t B, int64_t S, int64_t V) {
+  using namespace verify;
+  return target_bytes(B, S, V) + draft_bytes(B, S, V) + align256(static_cast<size_t>(B) * 12);
 }
 
 }  // namespace minite
@@ -218,9 +468,10 @@ extern "C" int minite_verify_drafts(const void* target, int target_dtype, int64_
   using namespace verify;
   const bool tf = target_dtype == MINITE_OUT_FP32, df = draft_dtype == MINITE_OUT_FP32;
   if ((!tf && target_dtype != MINITE_OUT_BF16) || (draft && !df && draft_dtype != MINITE_OUT_BF16) ||
-      !(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature))
+      !(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(kLog2e / temperature))
     return MINITE_ERR_INVALID_ARG;
-  if (B < 0 || S < 0 || S > 31 || B > (int64_t(1) << 24) || V < 1 || V > 0x7FFFFFFF || target_stride < V ||
+  if (B < 0 || S < 0 || S > kMaxDrafts || V < 1 || V > 0x7FFFFFFF || B > (int64_t(1) << 31) ||
+      B * (S + 1) * V > (int64_t(1) << 42) || B * (2 * S + 1) > (int64_t(1) << 24) || target_stride < V ||
       (draft && draft_stride < V) || noise_stride < V)
     return MINITE_ERR_UNSUPPORTED_SHAPE;
   if (B == 0) return MINITE_OK;
@@ -228,30 +479,22 @@ extern "C" int minite_verify_drafts(const void* target, int target_dtype, int64_
       !aligned(target, tf ? 4 : 2) || !aligned(draft, df ? 4 : 2) || !aligned(draft_tokens, 4) ||
       !aligned(uniforms, 4) || !aligned(noise, 4) || !aligned(tokens, 4) || !aligned(accepted, 4) ||
       !aligned(logprobs, 4) || !aligned(workspace, 256) || !aligned(status, 4) ||
-      ws_bytes < verify_workspace_bytes(B, S))
+      ws_bytes < verify_workspace_bytes(B, S, V))
     return MINITE_ERR_INVALID_ARG;
   if (S == 0) draft = nullptr;
-  char* ws = static_cast<char*>(workspace);
-  float* tst = reinterpret_cast<float*>(ws);
-  ws += align256(static_cast<size_t>(B) * (S + 1) * 8);
-  float* dst = reinterpret_cast<float*>(ws);
-  ws += align256(static_cast<size_t>(B) * S * 8);
-  int rc = minite_token_logprobs(target, target_dtype, B * (S + 1), V, target_stride, nullptr, 0, temperature,
-                                 nullptr, nullptr, tst, 0, nullptr, nullptr, nullptr, stream);
-  if (rc != MINITE_OK) return rc;
-  if (draft) {   // rows without a draft are not read
-    rc = minite_token_logprobs(draft, draft_dtype, B * S, V, draft_stride, draft_tokens, 0, temperature,
-                               reinterpret_cast<float*>(ws), nullptr, dst, 0, nullptr, nullptr, nullptr, stream);
-    if (rc != MINITE_OK) return rc;
-  }
   Params p = {};
+  char* ws = static_cast<char*>(workspace);
+  p.target_part = reinterpret_cast<float2*>(ws);
+  ws += target_bytes(B, S, V);
+  p.draft_part = reinterpret_cast<float2*>(ws);
+  ws += draft_bytes(B, S, V);
+  p.best = reinterpret_cast<unsigned long long*>(ws);
+  p.arrived = reinterpret_cast<uint32_t*>(p.best + B);
   p.target = target;
   p.draft = draft;
   p.target_ld = target_stride;
   p.draft_ld = draft_stride;
   p.noise_ld = noise_stride;
-  p.target_stats = reinterpret_cast<const float2*>(tst);
-  p.draft_stats = reinterpret_cast<const float2*>(dst);
   p.draft_tokens = draft_tokens;
   p.uniforms = uniforms;
   p.noise = noise;
@@ -259,6 +502,8 @@ extern "C" int minite_verify_drafts(const void* target, int target_dtype, int64_
   p.S = S;
   p.inv_t = 1.0f / temperature;
   p.k2 = p.inv_t * kLog2e;
+  p.target_segs = tf ? segments<float>(V) : segments<uint16_t>(V);
+  p.draft_segs = !draft ? 0 : df ? segments<float>(V) : segments<uint16_t>(V);
   p.tokens = tokens;
   p.logprobs = logprobs;
   p.accepted = accepted;

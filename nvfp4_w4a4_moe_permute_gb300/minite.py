@@ -652,28 +652,41 @@ def minite_moe_combine_rows_backward(dy, rows, dest_row, weights, drows, dweight
 
 
 def _grad_table(grads, outs, name):
-    """struct minite_grad_tensor of every gradient (and destination), and the device."""
+    """struct minite_grad_tensor of every gradient and its destination (outs may be
+    grads), and the device."""
     if len(grads) == 0:
         raise MiniteError(f"{name}: needs gradients")
-    if len(outs) != len(grads):
-        raise MiniteError(f"{name}: one destination a gradient")
     d = _device(grads[0])
-    table = array("q")
-    for g, o in zip(grads, outs):
-        n = g.numel()
-        if not (g.is_contiguous() and o.is_contiguous()) or o.numel() != n:
-            raise MiniteError(f"{name}: gradients are contiguous, and destinations contiguous and of their size")
-        if g.get_device() != d or o.get_device() != d:
-            raise _elsewhere("tensor", g.get_device() if g.get_device() != d else o.get_device(), d)
-        at = g.data_ptr()
-        table.extend((at, at if o is g else o.data_ptr(), n, _dtype(g, name) | _dtype(o, name) << 32))
+    sizes = [g.numel() for g in grads]
+    at = [g.data_ptr() for g in grads]
+    kinds = [_DTYPES.get(g.dtype) for g in grads]
+    tensors = grads
+    out_at, out_kinds = at, kinds
+    if outs is not grads:
+        if [o.numel() for o in outs] != sizes:
+            raise MiniteError(f"{name}: one destination a gradient, of its size")
+        out_at = [o.data_ptr() for o in outs]
+        out_kinds = [_DTYPES.get(o.dtype) for o in outs]
+        tensors = [*grads, *outs]
+    if not all([t.is_contiguous() for t in tensors]):
+        raise MiniteError(f"{name}: gradients and destinations are contiguous")
+    if None in kinds or None in out_kinds:
+        raise MiniteError(f"{name}: expected bfloat16 or float32")
+    for t in tensors:
+        if t.get_device() != d:
+            raise _elsewhere("tensor", t.get_device(), d)
+    table = array("q", bytes(32 * len(grads)))
+    table[0::4] = array("q", at)
+    table[1::4] = array("q", out_at)
+    table[2::4] = array("q", sizes)
+    table[3::4] = array("q", [a | b << 32 for a, b in zip(kinds, out_kinds)])
     return table, d
 
 
-def minite_grad_norm(grads, order, max_norm, norm, factor, workspace, stream=None):
+def minite_grad_norm(grads, order, max_norm, norm, factor, workspace, stream=None, table=None):
     """grads: contiguous bf16 or fp32 tensors; norm and factor fp32 [1], one of them may be None."""
     name = "minite_grad_norm"
-    table, d = _grad_table(grads, grads, name)
+    table, d = _grad_table(grads, grads, name) if table is None else table
     rc = load().minite_grad_norm(table.buffer_info()[0], len(grads), order, max_norm,
                                  _f32(norm, (1,), name, "norm", d), _f32(factor, (1,), name, "factor", d),
                                  _ptr(workspace, d), _bytes(workspace), _raw(stream, d))
@@ -681,10 +694,10 @@ def minite_grad_norm(grads, order, max_norm, norm, factor, workspace, stream=Non
         _check(rc, name)
 
 
-def minite_clip_grads(grads, outs, factor, stream=None):
+def minite_clip_grads(grads, outs, factor, stream=None, table=None):
     """outs[i] = grads[i] * factor; outs[i] may be grads[i]; factor fp32 [1]."""
     name = "minite_clip_grads"
-    table, d = _grad_table(grads, outs, name)
+    table, d = _grad_table(grads, outs, name) if table is None else table
     rc = load().minite_clip_grads(table.buffer_info()[0], len(grads), _f32(factor, (1,), name, "factor", d),
                                   _raw(stream, d))
     if rc:
@@ -940,26 +953,30 @@ def combine_rows_backward(dy, rows, dest_row, weights, out=None, status=None, st
     return out, dweights
 
 
+def _norm_of(grads, max_norm, order, stream, table, name):
+    if order not in (2, math.inf):
+        raise MiniteError(f"{name}: order is 2 or inf, not {order}")
+    like = grads[0]
+    norm, scale = _empty((1,), torch.float32, like, stream), _empty((1,), torch.float32, like, stream)
+    minite_grad_norm(grads, NORM_2 if order == 2 else NORM_MAX, max_norm, norm, scale,
+                     _workspace(OP_GRAD_NORM, like, stream, len(grads)), stream, table)
+    return {"norm": norm, "scale": scale}
+
+
 def grad_norm(grads, max_norm=math.inf, order=2.0, stream=None):
     """The global norm of a list of gradients (bf16 and fp32 may be mixed), and the
     factor min(1, max_norm / (norm + 1e-6)) for ``AdamW.step(grad_scale=)``:
     dict(norm [1], scale [1]), on the device. order: 2 or math.inf (the largest |g|)."""
-    if order not in (2, math.inf):
-        raise MiniteError(f"grad_norm: order is 2 or inf, not {order}")
-    if len(grads) == 0:
-        raise MiniteError("grad_norm: needs gradients")
-    like = grads[0]
-    norm, scale = _empty((1,), torch.float32, like, stream), _empty((1,), torch.float32, like, stream)
-    minite_grad_norm(grads, NORM_2 if order == 2 else NORM_MAX, max_norm, norm, scale,
-                     _workspace(OP_GRAD_NORM, like, stream, len(grads)), stream)
-    return {"norm": norm, "scale": scale}
+    return _norm_of(grads, max_norm, order, stream, _grad_table(grads, grads, "grad_norm"), "grad_norm")
 
 
 def clip_grads(grads, max_norm, order=2.0, out=None, stream=None):
     """Gradients times grad_norm's factor, in place or into the tensors ``out``
     (of either type). Returns grad_norm's dict."""
-    r = grad_norm(grads, max_norm, order, stream)
-    minite_clip_grads(grads, grads if out is None else out, r["scale"], stream)
+    out = grads if out is None else out
+    table = _grad_table(grads, out, "clip_grads")
+    r = _norm_of(grads, max_norm, order, stream, table, "clip_grads")
+    minite_clip_grads(grads, out, r["scale"], stream, table)
     return r
 
 
@@ -971,12 +988,12 @@ def verify_drafts(logits, draft_tokens, uniforms, noise, draft_logits=None, temp
     sampled from at the same temperature, None where they were looked up. Returns
     dict(tokens [B, S + 1], accepted [B], logprobs [B, S + 1]): the drafts that stand,
     the token that follows them, -1."""
-    B, S1 = _shape(logits, 3, "verify_drafts", "logits")[:2]
+    B, S1, V = _shape(logits, 3, "verify_drafts", "logits")
     S = _shape(draft_tokens, 2, "verify_drafts", "draft_tokens")[1]
     tokens, accepted = _empty((B, S1), torch.int32, logits, stream), _empty((B,), torch.int32, logits, stream)
     logprobs = _empty((B, S1), torch.float32, logits, stream)
     minite_verify_drafts(logits, draft_logits, draft_tokens, uniforms, noise, temperature, tokens, accepted,
-                         logprobs, _workspace(OP_VERIFY_DRAFTS, logits, stream, B, S), status, stream)
+                         logprobs, _workspace(OP_VERIFY_DRAFTS, logits, stream, B, V, S), status, stream)
     return {"tokens": tokens, "accepted": accepted, "logprobs": logprobs}
 
 
