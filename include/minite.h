@@ -749,9 +749,9 @@ int minite_adamw_step(const minite_adamw_tensor* tensors, int64_t n_tensors, int
  * rows:     device, the type of x, [T*k, H], rows `rows_stride` elements apart.
  * expert_offsets: device, int32 [E+1]; perm_src: device, int32 [T*k], token of
  *           each row; dest_row: device, int32 [T, k].
- * workspace: device, >= minite_workspace_bytes(MINITE_OP_PERMUTE_ROWS, T, 0, E, k),
- *           256-byte aligned, contents on entry ignored.
- * Shape rules: 1 <= H < 2^30, 1 <= E <= 1024, 1 <= k <= 32, T*k < 2^31, T = 0
+ * workspace: device, >= minite_workspace_bytes(MINITE_OP_PERMUTE_ROWS, T, 0, E, k)
+ *           bytes, 256-byte aligned, contents on entry ignored; NULL where that is 0.
+ * Shape rules: 1 <= H <= 2^24, 1 <= E <= 1024, 1 <= k <= 32, T*k < 2^31, T = 0
  * allowed (offsets become 0), strides at least H and below 2^31. Matrices are
  * aligned to their element; accesses are 32 bytes wide where base addresses, row
  * sizes and strides are multiples of that, 16, 4 or 2 bytes otherwise.

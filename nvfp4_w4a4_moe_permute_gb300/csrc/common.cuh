@@ -150,6 +150,18 @@ __device__ __forceinline__ void unpack_bf16x8(const uint4& u, float (&v)[8]) {
   v[4] = bf16lo(u.z); v[5] = bf16hi(u.z); v[6] = bf16lo(u.w); v[7] = bf16hi(u.w);
 }
 
+// The lanes whose id (in [0, limit]) is this lane's, by a vote on every bit.
+// Warp-collective.
+__device__ __forceinline__ uint32_t same_id_lanes(int id, int limit) {
+  uint32_t same = 0xffffffffu;
+  for (int b = 0; (limit >> b) != 0; ++b) {
+    const bool bit = (id >> b) & 1;
+    const uint32_t vote = __ballot_sync(0xffffffffu, bit);
+    same &= bit ? vote : ~vote;
+  }
+  return same;
+}
+
 // a / b for a >= 0, b > 0: the 32-bit division when both fit in 32 bits (the
 // usual case; a 64-bit division is a long instruction sequence).
 __device__ __forceinline__ int64_t div_nonneg(int64_t a, int64_t b) {

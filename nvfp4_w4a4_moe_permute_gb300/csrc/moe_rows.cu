@@ -166,9 +166,329 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(Matrix x, int64_t T, int
       r.perm_src[i] = -1;
 }
 
-// y[t] = sum over slots of weight * row, U words of 32 lanes a unit.
+// Permutations of up to kTablePairs slots, without a scan kernel: every CTA has a
+// range of tokens and finds out by itself how many slots of each expert come before
+// them and in all.
+//   TABLE false, up to kDirectPairs slots: one launch. The CTA reads all ids and
+//     counts them by atomics in shared memory (10 cycles each 32 ids).
+//   TABLE true: after the ranking kernel, whose counts of each expert in each chunk
+//     of 512 slots it adds up.
+// The ids of one 4096-token micro-batch with 8 slots each take the first form 5 us,
+// the ranking and the sums 4, the ranking, a scan kernel and the copies' look at its
+// results 6.
+constexpr int64_t kDirectPairs = 16384;
+constexpr int64_t kTablePairs = 65536;
+constexpr int64_t kTableEntries = 16384;   // of chunks x experts: what a CTA reads
+constexpr int kRangeThreads = 512;
+constexpr int kRangeWarps = kRangeThreads / 32;
+// A range then has at most 65536 / 152 slots and lies in two chunks at most.
+
+// Sum of v over the threads in front of this one, and over all.
+__device__ __forceinline__ int scan_before(int v, int* s_warp, int* total) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  int in = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, in, o);
+    if (lane >= o) in += u;
+  }
+  if (lane == 31) s_warp[wid] = in;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kRangeWarps; ++w) {
+    const int x = s_warp[w];
+    if (w < wid) before += x;
+    all += x;
+  }
+  *total = all;
+  return before + in - v;
+}
+
+template <int B, int U, bool TABLE>
+__global__ void __launch_bounds__(kRangeThreads, 1) range_kernel(
+    Matrix x, int64_t T, int64_t words, int k, int E, const int32_t* __restrict__ ids,
+    const int32_t* __restrict__ table, const int32_t* __restrict__ rank, int ct, int nchunks,
+    int32_t* __restrict__ offsets, int32_t* __restrict__ perm_src, int32_t* __restrict__ dest_row, Matrix out,
+    int32_t* status) {
+  extern __shared__ int32_t sm[];
+  __shared__ int s_warp[kRangeWarps];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int per = static_cast<int>((T + gridDim.x - 1) / gridDim.x);
+  const int t0 = min(static_cast<int>(T), static_cast<int>(blockIdx.x) * per), t1 = min(static_cast<int>(T), t0 + per);
+  const int p0 = t0 * k, own = (t1 - t0) * k, pairs = static_cast<int>(T) * k;
+  int32_t* s_before = sm;            // [E] slots before the range; then the row of the first in it
+  int32_t* s_all = sm + E;           // [E] slots after that; TABLE: in all
+  int32_t* s_first = sm + 2 * E;     // [E] TABLE: slots in the range's first chunk
+  int32_t* s_dest = sm + 3 * E;      // [per * k] ids, then rows
+  if constexpr (!TABLE) {
+    for (int e = tid; e < 2 * E; e += kRangeThreads) sm[e] = 0;
+    __syncthreads();
+  }
+  pdl_wait();
+  // units of this CTA: a token and U words a lane
+  const int parts = static_cast<int>((words + 32 * U - 1) / (32 * U));
+  const int units = (t1 - t0) * parts;
+  auto fetch = [&](int u, Word<B> (&v)[U]) {
+    if (u >= units) return;
+    const int t = u / parts;
+    const int64_t w0 = static_cast<int64_t>(u - t * parts) * (32 * U) + lane;
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (w0 + 32 * i < words) v[i].load(x.p + (t0 + t) * x.ld + (w0 + 32 * i) * B);
+  };
+  Word<B> va[U], vb[U];
+  fetch(wid, va);
+  const int c0 = t0 / (TABLE ? ct : 1);   // the first token's chunk
+  if constexpr (TABLE) {
+    constexpr int kAhead = 8;
+    for (int e0 = wid; e0 < E; e0 += kAhead * kRangeWarps) {
+      int all[kAhead] = {}, before[kAhead] = {}, first[kAhead] = {};
+      for (int c = lane; c < nchunks; c += 32) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int e = e0 + i * kRangeWarps;
+          const int n = e < E ? table[e * nchunks + c] : 0;
+          all[i] += n;
+          if (c < c0) before[i] += n;
+          if (c == c0) first[i] = n;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int e = e0 + i * kRangeWarps;
+        const int a = __reduce_add_sync(0xffffffffu, all[i]), f = __reduce_add_sync(0xffffffffu, before[i]),
+                  g = __reduce_add_sync(0xffffffffu, first[i]);
+        if (lane == 0 && e < E) {
+          s_all[e] = a;
+          s_before[e] = f;
+          s_first[e] = g;
+        }
+      }
+    }
+  } else {
+    bool bad = false;
+    auto count = [&](int p, int e) {
+      const bool valid = e >= 0 && e < E;
+      bad |= e >= E;
+      if (valid) atomicAdd(sm + (p < p0 ? e : E + e), 1);
+      if (p >= p0 && p < p0 + own) s_dest[p - p0] = valid ? e : -1;
+    };
+    if ((reinterpret_cast<uintptr_t>(ids) & 15) == 0) {
+      const int4* ids4 = reinterpret_cast<const int4*>(ids);
+      for (int q = tid; q < pairs / 4; q += kRangeThreads) {
+        const int4 a = __ldg(ids4 + q);
+        count(4 * q, a.x);
+        count(4 * q + 1, a.y);
+        count(4 * q + 2, a.z);
+        count(4 * q + 3, a.w);
+      }
+      for (int p = (pairs & ~3) + tid; p < pairs; p += kRangeThreads) count(p, ids[p]);
+    } else {
+      for (int p = tid; p < pairs; p += kRangeThreads) count(p, ids[p]);
+    }
+    if (bad && blockIdx.x == 0) set_status(status, MINITE_ERR_BAD_ROUTING);
+  }
+  __syncthreads();
+  int used = 0;
+  for (int base = 0; base < E; base += kRangeThreads) {
+    const int e = base + tid;
+    const int n = e < E ? s_all[e] + (TABLE ? 0 : s_before[e]) : 0;
+    int total;
+    const int at = used + scan_before(n, s_warp, &total);
+    if (e < E) {
+      s_before[e] += at;
+      if (blockIdx.x == 0) offsets[e] = at;
+    }
+    used += total;
+    __syncthreads();
+  }
+  if (blockIdx.x == 0 && tid == 0) offsets[E] = used;
+  // rows of this CTA's slots
+  if constexpr (TABLE) {
+    for (int p = tid; p < own; p += kRangeThreads) {
+      const int e = ids[p0 + p];
+      int dest = -1;
+      if (e >= 0 && e < E) dest = s_before[e] + ((t0 + p / k) / ct > c0 ? s_first[e] : 0) + rank[p0 + p];
+      s_dest[p] = dest;
+      dest_row[p0 + p] = dest;
+      if (dest >= 0) perm_src[dest] = t0 + p / k;
+    }
+  } else if (wid == 0) {   // 32 at a time, in their order
+    for (int b = 0; b < own; b += 32) {
+      const int p = b + lane;
+      const int e = p < own ? s_dest[p] : -1;
+      const uint32_t same = same_id_lanes(e >= 0 ? e : E, E);
+      const int before = __popc(same & ((1u << lane) - 1u));
+      const int at = e >= 0 ? s_before[e] : 0;
+      __syncwarp();
+      if (e >= 0 && before == 0) s_before[e] = at + __popc(same);
+      __syncwarp();
+      if (p < own) {
+        const int dest = e >= 0 ? at + before : -1;
+        s_dest[p] = dest;
+        dest_row[p0 + p] = dest;
+        if (dest >= 0) perm_src[dest] = t0 + p / k;
+      }
+    }
+  }
+  __syncthreads();
+  auto spread = [&](int u, const Word<B> (&v)[U]) {
+    if (u >= units) return;
+    const int t = u / parts;
+    const int64_t w0 = static_cast<int64_t>(u - t * parts) * (32 * U) + lane;
+    for (int j = 0; j < k; ++j) {
+      const int d = s_dest[t * k + j];
+      if (d < 0) continue;
+      char* row = out.p + d * out.ld;
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (w0 + 32 * i < words) v[i].store(row + (w0 + 32 * i) * B);
+    }
+  };
+  for (int u = wid; u < units; u += 2 * kRangeWarps) {
+    fetch(u + kRangeWarps, vb);
+    spread(u, va);
+    fetch(u + 2 * kRangeWarps, va);
+    spread(u + kRangeWarps, vb);
+  }
+  for (int i = used + blockIdx.x * kRangeThreads + tid; i < pairs; i += gridDim.x * kRangeThreads) perm_src[i] = -1;
+}
+
+// 16 bytes of global memory to a slot of shared memory that only this thread uses.
+__device__ __forceinline__ void ask16(void* slot, const char* p) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(slot)), "l"(p) : "memory");
+}
+__device__ __forceinline__ void close_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void wait_groups() {
+  asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
+__device__ __forceinline__ Word<16> slot_word(const uint4& u) { return {{u.x, u.y, u.z, u.w}}; }
+
+constexpr int kDepth = 4;             // steps of a warp in flight
+constexpr int kPieceBytes = 32 * 16;  // of a row, a warp's
+
+// Eight values a lane to their sums over the warp: lane l returns the sum of
+// value l / 4.
+__device__ __forceinline__ float warp_sum8(float (&v)[8]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 4; s > 0; s >>= 1) {
+    const bool up = lane & (4 * s);
+#pragma unroll
+    for (int i = 0; i < s; ++i) {
+      const float give = up ? v[i] : v[i + s], keep = up ? v[i + s] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * s);
+    }
+  }
+  float r = v[0];
+  r += __shfl_xor_sync(0xffffffffu, r, 2);
+  r += __shfl_xor_sync(0xffffffffu, r, 1);
+  return r;
+}
+
+// y[t] = sum over slots of weight * row, for rows of whole 16-byte words. A step is
+// a 512-byte piece of a token's row in up to 8 of its slots; a warp asks for four
+// steps ahead, by asynchronous copies to places that only the asking lane reads (no
+// barrier, few registers, 192 KB in flight on an SM), and for their routing eight
+// steps ahead (one step more than the copies' left every step waiting for it).
+constexpr int kCombineWarps = 12;
+struct CombineShared {
+  uint4 stage[kCombineWarps][kDepth][kSlots][32];
+};
+template <typename T>
+__global__ void __launch_bounds__(32 * kCombineWarps, 1) combine_kernel(
+    Matrix rows, const int32_t* __restrict__ dest_row, const float* __restrict__ weights, int64_t T_, int64_t M,
+    int64_t row_bytes, int k, Matrix y, int32_t* status) {
+  using V = Values<T, 16>;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  uint4 (*stage)[kSlots][32] = reinterpret_cast<CombineShared*>(smem_raw)->stage[wid];
+  pdl_wait();
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * kCombineWarps + wid;
+  const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kCombineWarps;
+  const int64_t parts = (row_bytes + kPieceBytes - 1) / kPieceBytes;
+  const int64_t units = T_ * parts;
+  const int groups = (k + kSlots - 1) / kSlots;
+  const int64_t steps = warp < units ? ((units - warp - 1) / nwarps + 1) * groups : 0;
+  struct Route {
+    int dest;     // lane j: of slot 8 g + j
+    float w;
+    int64_t t;
+    int32_t col;  // in bytes; row_bytes or more: none for this lane
+  };
+  auto route = [&](int64_t i) {
+    Route r = {-1, 1.0f, 0, 0};
+    if (i < steps) {
+      const int64_t turn = div_nonneg(i, groups);
+      const int64_t u = warp + turn * nwarps;
+      r.t = div_nonneg(u, parts);
+      r.col = static_cast<int32_t>((u - r.t * parts) * kPieceBytes) + 16 * lane;
+      const int j = static_cast<int>(i - turn * groups) * kSlots + lane;
+      if (lane < kSlots && j < k) {
+        r.dest = dest_row[r.t * k + j];
+        if (weights) r.w = weights[r.t * k + j];
+      }
+    }
+    return r;
+  };
+  auto ask = [&](Route& r, int s) {
+    if (r.dest >= M) {
+      set_status(status, MINITE_ERR_BAD_ROUTING);
+      r.dest = -1;
+    }
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      const int d = __shfl_sync(0xffffffffu, r.dest, j);
+      if (d >= 0 && r.col < row_bytes) ask16(&stage[s][j][lane], rows.p + d * rows.ld + r.col);
+    }
+    close_group();
+  };
+  Route r[kDepth], next[kDepth];
+#pragma unroll
+  for (int s = 0; s < kDepth; ++s) r[s] = route(s);
+#pragma unroll
+  for (int s = 0; s < kDepth; ++s) next[s] = route(kDepth + s);
+#pragma unroll
+  for (int s = 0; s < kDepth; ++s) ask(r[s], s);
+  float acc[V::kN];
+#pragma unroll
+  for (int c = 0; c < V::kN; ++c) acc[c] = 0.0f;
+  int g = 0;
+  for (int64_t i = 0; i < steps;) {
+#pragma unroll
+    for (int s = 0; s < kDepth; ++s, ++i) {
+      if (i >= steps) break;
+      wait_groups<kDepth - 1>();
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) {
+        const int d = __shfl_sync(0xffffffffu, r[s].dest, j);
+        const float w = __shfl_sync(0xffffffffu, r[s].w, j);
+        if (d >= 0) {
+          float f[V::kN];
+          V::get(slot_word(stage[s][j][lane]), f);
+#pragma unroll
+          for (int c = 0; c < V::kN; ++c) acc[c] = fmaf(w, f[c], acc[c]);
+        }
+      }
+      if (++g == groups) {
+        Word<16> o;
+        V::put(o, acc);
+        if (r[s].col < row_bytes) o.store(y.p + r[s].t * y.ld + r[s].col);
+#pragma unroll
+        for (int c = 0; c < V::kN; ++c) acc[c] = 0.0f;
+        g = 0;
+      }
+      r[s] = next[s];
+      ask(r[s], s);
+      next[s] = route(i + 2 * kDepth);
+    }
+  }
+}
+
+// The same for rows of any alignment, U elements of 32 lanes a unit.
 template <typename T, int B, int U>
-__global__ void __launch_bounds__(kThreads, 2) combine_kernel(Matrix rows, const int32_t* __restrict__ dest_row,
+__global__ void __launch_bounds__(kThreads, 2) combine_any_kernel(Matrix rows, const int32_t* __restrict__ dest_row,
                                                               const float* __restrict__ weights, int64_t T_,
                                                               int64_t M, int64_t words, int k, Matrix y,
                                                               int32_t* status) {
@@ -241,50 +561,166 @@ __global__ void __launch_bounds__(kThreads, 2) combine_kernel(Matrix rows, const
   }
 }
 
-// Eight values a lane to their sums over the warp: lane l returns the sum of
-// value l / 4.
-__device__ __forceinline__ float warp_sum8(float (&v)[8]) {
-  const int lane = threadIdx.x & 31;
+// drows[d] = weight * dy[t] and, with DOT, dweights = <dy[t], rows[d]>, for rows of
+// whole 16-byte words. `team` warps of a CTA share a token: member m takes the
+// 512-byte pieces m, m + team, ... of its row. A step is one piece in up to 8 slots,
+// asked for four steps ahead as in combine_kernel. A member's dot products stay in
+// its lanes until its last piece, and wait in shared memory for the other members';
+// every kHeld tokens all are added, in the members' order. team follows from the
+// row's size alone, so the sums do not depend on the other tokens. drows may be
+// rows: a piece is read by the warp that writes it, before it does.
+constexpr int kHeld = 16;
+struct BackwardShared {
+  uint4 stage[kWarps][kDepth][kSlots + 1][32];   // the last: dy
+  float dot[kHeld][kWarps][kSlots];
+};
+template <typename T, bool DOT>
+__global__ void __launch_bounds__(kThreads, 1) combine_backward_kernel(
+    Matrix dy, Matrix rows, const int32_t* __restrict__ dest_row, const float* __restrict__ weights, int64_t T_,
+    int64_t M, int64_t row_bytes, int k, int team, Matrix drows, float* __restrict__ dweights, int32_t* status) {
+  using V = Values<T, 16>;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  BackwardShared& S = *reinterpret_cast<BackwardShared*>(smem_raw);
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  uint4 (*stage)[kSlots + 1][32] = S.stage[wid];
+  pdl_wait();
+  const int teams = kWarps / team, mine = wid / team, member = wid % team;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * teams;   // the CTA's first token
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * teams;
+  const int groups = (k + kSlots - 1) / kSlots;
+  const int parts = static_cast<int>((row_bytes + kPieceBytes - 1) / kPieceBytes);
+  const int pieces = (parts + team - 1) / team;   // steps of an item, the last may have no piece
+  // an item is a token and 8 of its slots: item i of a team is group i % groups of
+  // its token i / groups; the same number for every team of the CTA
+  const int64_t items = first < T_ ? ((T_ - first - 1) / stride + 1) * groups : 0;
+  const int64_t steps = items * pieces;
+  struct Route {
+    int dest;
+    float w;
+    int64_t t;
+    int32_t col;
+  };
+  auto route = [&](int64_t i) {
+    Route r = {-1, 0.0f, 0, 0x7FFFFFFF};
+    if (i < steps) {
+      const int64_t item = div_nonneg(i, pieces);
+      const int piece = static_cast<int>(i - item * pieces) * team + member;
+      const int64_t turn = div_nonneg(item, groups);
+      r.t = first + mine + turn * stride;
+      const int j = static_cast<int>(item - turn * groups) * kSlots + lane;
+      if (r.t < T_ && piece < parts) {
+        r.col = piece * kPieceBytes + 16 * lane;
+        if (lane < kSlots && j < k) {
+          r.dest = dest_row[r.t * k + j];
+          r.w = weights[r.t * k + j];
+        }
+      }
+    }
+    return r;
+  };
+  auto ask = [&](Route& r, int s) {
+    if (r.dest >= M) {
+      set_status(status, MINITE_ERR_BAD_ROUTING);
+      r.dest = -1;
+    }
+    if (r.col < row_bytes) ask16(&stage[s][kSlots][lane], dy.p + r.t * dy.ld + r.col);
+    if constexpr (DOT) {
 #pragma unroll
-  for (int s = 4; s > 0; s >>= 1) {
-    const bool up = lane & (4 * s);
+      for (int j = 0; j < kSlots; ++j) {
+        const int d = __shfl_sync(0xffffffffu, r.dest, j);
+        if (d >= 0 && r.col < row_bytes) ask16(&stage[s][j][lane], rows.p + d * rows.ld + r.col);
+      }
+    }
+    close_group();
+  };
+  Route r[kDepth], next[kDepth];
 #pragma unroll
-    for (int i = 0; i < s; ++i) {
-      const float give = up ? v[i] : v[i + s], keep = up ? v[i + s] : v[i];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 4 * s);
+  for (int s = 0; s < kDepth; ++s) r[s] = route(s);
+#pragma unroll
+  for (int s = 0; s < kDepth; ++s) next[s] = route(kDepth + s);
+#pragma unroll
+  for (int s = 0; s < kDepth; ++s) ask(r[s], s);
+  float dot[kSlots];
+#pragma unroll
+  for (int j = 0; j < kSlots; ++j) dot[j] = 0.0f;
+  int piece = 0, held = 0;
+  int64_t item0 = 0;   // the first item that is held
+  for (int64_t i = 0; i < steps;) {
+#pragma unroll
+    for (int s = 0; s < kDepth; ++s, ++i) {
+      if (i >= steps) break;
+      wait_groups<kDepth - 1>();
+      const bool live = r[s].col < row_bytes;
+      float d[V::kN];
+      V::get(slot_word(stage[s][kSlots][lane]), d);
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) {
+        const int to = __shfl_sync(0xffffffffu, r[s].dest, j);
+        const float w = __shfl_sync(0xffffffffu, r[s].w, j);
+        if (to >= 0 && live) {
+          float f[V::kN];
+          if constexpr (DOT) {
+            V::get(slot_word(stage[s][j][lane]), f);
+#pragma unroll
+            for (int c = 0; c < V::kN; ++c) dot[j] = fmaf(d[c], f[c], dot[j]);
+          }
+#pragma unroll
+          for (int c = 0; c < V::kN; ++c) f[c] = w * d[c];
+          Word<16> o;
+          V::put(o, f);
+          o.store(drows.p + to * drows.ld + r[s].col);
+        }
+      }
+      r[s] = next[s];
+      ask(r[s], s);
+      next[s] = route(i + 2 * kDepth);
+      if constexpr (DOT) {
+        if (++piece == pieces) {
+          const float sum = warp_sum8(dot);
+          if ((lane & 3) == 0) S.dot[held][wid][lane >> 2] = sum;
+#pragma unroll
+          for (int j = 0; j < kSlots; ++j) dot[j] = 0.0f;
+          piece = 0;
+          if (++held == kHeld || i + 1 == steps) {
+            __syncthreads();
+            for (int x = threadIdx.x; x < held * teams * kSlots; x += kThreads) {
+              const int j = x % kSlots, q = x / kSlots % teams;
+              const int64_t item = item0 + x / (kSlots * teams);
+              const int64_t turn = div_nonneg(item, groups), t = first + q + turn * stride;
+              const int slot = static_cast<int>(item - turn * groups) * kSlots + j;
+              if (t < T_ && slot < k) {
+                float v = 0.0f;
+                for (int m = 0; m < team; ++m) v += S.dot[x / (kSlots * teams)][q * team + m][j];
+                dweights[t * k + slot] = v;
+              }
+            }
+            __syncthreads();
+            item0 += held;
+            held = 0;
+          }
+        }
+      }
     }
   }
-  float r = v[0];
-  r += __shfl_xor_sync(0xffffffffu, r, 2);
-  r += __shfl_xor_sync(0xffffffffu, r, 1);
-  return r;
 }
 
-// drows[d] = weight * dy[t] and, with DOT, dweights = <dy[t], rows[d]>. `group`
-// warps of a CTA (a power of two) share a token, taking its pieces in turn; a
-// piece's dot products are summed over the warp, then over the pieces in order,
-// so that the sums do not depend on `group`. drows may be rows: every piece is
-// read by the warp that writes it, before it does.
+// The same for rows of any alignment, U elements of 32 lanes a piece, a warp a
+// token: a piece's dot products are summed over the warp, then over the pieces in
+// order.
 template <typename T, int B, int U, bool DOT>
-__global__ void __launch_bounds__(kThreads, 2) combine_backward_kernel(
+__global__ void __launch_bounds__(kThreads, 2) combine_backward_any_kernel(
     Matrix dy, Matrix rows, const int32_t* __restrict__ dest_row, const float* __restrict__ weights,
-    int64_t T_, int64_t M, int64_t words, int k, int group, Matrix drows, float* __restrict__ dweights,
+    int64_t T_, int64_t M, int64_t words, int k, Matrix drows, float* __restrict__ dweights,
     int32_t* status) {
   using V = Values<T, B>;
-  extern __shared__ float s_part[];   // [kWarps / group][parts][kSlots], with group > 1
   pdl_wait();
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int per_cta = kWarps / group;
-  const int member = wid % group, team = wid / group;
+  const int lane = threadIdx.x & 31;
   const int parts = static_cast<int>((words + 32 * U - 1) / (32 * U));
-  const int64_t step = static_cast<int64_t>(gridDim.x) * per_cta;
-  // every warp of a CTA makes the same number of turns, for the barriers
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * per_cta; t0 < T_; t0 += step) {
-    const int64_t t = t0 + team;
-    const bool live = t < T_;
+  const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < T_; t += nwarps) {
     int mine = -1;
     float my_w = 0.0f;
-    if (live && lane < k) {
+    if (lane < k) {
       mine = dest_row[t * k + lane];
       my_w = weights[t * k + lane];
       if (mine >= M) {
@@ -294,70 +730,56 @@ __global__ void __launch_bounds__(kThreads, 2) combine_backward_kernel(
     }
     for (int j0 = 0; j0 < k; j0 += kSlots) {
       float sum = 0.0f;
-      if (live) {
-        for (int part = member; part < parts; part += group) {
-          const int64_t w0 = static_cast<int64_t>(part) * (32 * U) + lane;
-          float d[U][V::kN];
-          Word<B> v[kSlots][U];
+      for (int part = 0; part < parts; ++part) {
+        const int64_t w0 = static_cast<int64_t>(part) * (32 * U) + lane;
+        float d[U][V::kN];
+        Word<B> v[kSlots][U];
 #pragma unroll
-          for (int i = 0; i < U; ++i) {
-            Word<B> u = {};
-            if (w0 + 32 * i < words) u.load(dy.p + t * dy.ld + (w0 + 32 * i) * B);
-            V::get(u, d[i]);
-          }
-          if constexpr (DOT) {
-#pragma unroll
-            for (int jj = 0; jj < kSlots; ++jj) {
-              const int to = __shfl_sync(0xffffffffu, mine, (j0 + jj) & 31);
-              const char* row = rows.p + to * rows.ld;
-#pragma unroll
-              for (int i = 0; i < U; ++i) {
-                v[jj][i] = {};
-                if (j0 + jj < k && to >= 0 && w0 + 32 * i < words) v[jj][i].load(row + (w0 + 32 * i) * B);
-              }
-            }
-          }
-          float dot[kSlots];
+        for (int i = 0; i < U; ++i) {
+          Word<B> u = {};
+          if (w0 + 32 * i < words) u.load(dy.p + t * dy.ld + (w0 + 32 * i) * B);
+          V::get(u, d[i]);
+        }
+        if constexpr (DOT) {
 #pragma unroll
           for (int jj = 0; jj < kSlots; ++jj) {
             const int to = __shfl_sync(0xffffffffu, mine, (j0 + jj) & 31);
-            const float w = __shfl_sync(0xffffffffu, my_w, (j0 + jj) & 31);
-            dot[jj] = 0.0f;
-            if (j0 + jj < k && to >= 0) {
-              char* row = drows.p + to * drows.ld;
+            const char* row = rows.p + to * rows.ld;
 #pragma unroll
-              for (int i = 0; i < U; ++i) {
-                float f[V::kN];
-                if constexpr (DOT) {
-                  V::get(v[jj][i], f);
-#pragma unroll
-                  for (int c = 0; c < V::kN; ++c) dot[jj] = fmaf(d[i][c], f[c], dot[jj]);
-                }
-#pragma unroll
-                for (int c = 0; c < V::kN; ++c) f[c] = w * d[i][c];
-                Word<B> o;
-                V::put(o, f);
-                if (w0 + 32 * i < words) o.store(row + (w0 + 32 * i) * B);
-              }
+            for (int i = 0; i < U; ++i) {
+              v[jj][i] = {};
+              if (j0 + jj < k && to >= 0 && w0 + 32 * i < words) v[jj][i].load(row + (w0 + 32 * i) * B);
             }
           }
-          if constexpr (DOT) {
-            const float s = warp_sum8(dot);
-            if (group == 1) sum += s;
-            else if ((lane & 3) == 0) s_part[(team * parts + part) * kSlots + (lane >> 2)] = s;
+        }
+        float dot[kSlots];
+#pragma unroll
+        for (int jj = 0; jj < kSlots; ++jj) {
+          const int to = __shfl_sync(0xffffffffu, mine, (j0 + jj) & 31);
+          const float w = __shfl_sync(0xffffffffu, my_w, (j0 + jj) & 31);
+          dot[jj] = 0.0f;
+          if (j0 + jj < k && to >= 0) {
+            char* row = drows.p + to * drows.ld;
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+              float f[V::kN];
+              if constexpr (DOT) {
+                V::get(v[jj][i], f);
+#pragma unroll
+                for (int c = 0; c < V::kN; ++c) dot[jj] = fmaf(d[i][c], f[c], dot[jj]);
+              }
+#pragma unroll
+              for (int c = 0; c < V::kN; ++c) f[c] = w * d[i][c];
+              Word<B> o;
+              V::put(o, f);
+              if (w0 + 32 * i < words) o.store(row + (w0 + 32 * i) * B);
+            }
           }
         }
+        if constexpr (DOT) sum += warp_sum8(dot);
       }
-      if constexpr (DOT) {
-        if (group > 1) {
-          __syncthreads();
-          if (live && member == 0 && (lane & 3) == 0)
-            for (int part = 0; part < parts; ++part) sum += s_part[(team * parts + part) * kSlots + (lane >> 2)];
-          __syncthreads();
-        }
-        if (live && member == 0 && (lane & 3) == 0 && j0 + (lane >> 2) < k)
-          dweights[t * k + j0 + (lane >> 2)] = sum;
-      }
+      if constexpr (DOT)
+        if ((lane & 3) == 0 && j0 + (lane >> 2) < k) dweights[t * k + j0 + (lane >> 2)] = sum;
     }
   }
 }
@@ -385,6 +807,32 @@ cudaError_t copy_as(const Matrix& x, int64_t T, int64_t row_bytes, int k, const 
   return launch_pdl(copy_kernel<B, U>, dim3(blocks_for(T * parts, 6)), dim3(kThreads), 0, s, x, T, words, k, r,
                     out, M, status);
 }
+
+struct Sorted {   // what a permutation writes besides the rows
+  int32_t* offsets;
+  int32_t* perm_src;
+  int32_t* dest_row;
+};
+template <int B, int U, bool TABLE>
+cudaError_t range_as(const Matrix& x, int64_t T, int64_t row_bytes, int k, int E, const Routing& r, const Sorted& o,
+                     const Matrix& out, int32_t* status, cudaStream_t s) {
+  const int64_t grid = T < num_sms() ? T : num_sms();
+  const size_t smem = (3 * static_cast<size_t>(E) + static_cast<size_t>((T + grid - 1) / grid) * k) * sizeof(int32_t);
+  return launch_pdl(range_kernel<B, U, TABLE>, dim3(static_cast<unsigned>(grid)), dim3(kRangeThreads), smem, s, x, T,
+                    row_bytes / B, k, E, r.ids, r.table, r.rank, r.ct, r.nchunks, o.offsets, o.perm_src, o.dest_row,
+                    out, status);
+}
+template <bool TABLE>
+cudaError_t range(const Matrix& x, int64_t T, int64_t row_bytes, int k, int E, const Routing& r, const Sorted& o,
+                  const Matrix& out, int32_t* status, cudaStream_t s) {
+  switch (width(row_bytes, {x, out})) {
+    case 32: return range_as<32, 2, TABLE>(x, T, row_bytes, k, E, r, o, out, status, s);
+    case 16: return range_as<16, 4, TABLE>(x, T, row_bytes, k, E, r, o, out, status, s);
+    case 4: return range_as<4, 8, TABLE>(x, T, row_bytes, k, E, r, o, out, status, s);
+    default: return range_as<2, 8, TABLE>(x, T, row_bytes, k, E, r, o, out, status, s);
+  }
+}
+
 cudaError_t copy(const Matrix& x, int64_t T, int64_t row_bytes, int k, const Routing& r, const Matrix& out,
                  int64_t M, int32_t* status, cudaStream_t s) {
   switch (width(row_bytes, {x, out})) {
@@ -395,52 +843,50 @@ cudaError_t copy(const Matrix& x, int64_t T, int64_t row_bytes, int k, const Rou
   }
 }
 
-template <typename T, int B, int U>
-cudaError_t combine_as(const Matrix& rows, const int32_t* dest_row, const float* weights, int64_t T_, int64_t M,
-                       int64_t H, int k, const Matrix& y, int32_t* status, cudaStream_t s) {
-  const int64_t words = H * static_cast<int64_t>(sizeof(T)) / B, parts = (words + 32 * U - 1) / (32 * U);
-  return launch_pdl(combine_kernel<T, B, U>, dim3(blocks_for(T_ * parts, 2)), dim3(kThreads), 0, s, rows, dest_row,
-                    weights, T_, M, words, k, y, status);
-}
 template <typename T>
 cudaError_t combine(const Matrix& rows, const int32_t* dest_row, const float* weights, int64_t T_, int64_t M,
                     int64_t H, int k, const Matrix& y, int32_t* status, cudaStream_t s) {
-  switch (width(H * static_cast<int64_t>(sizeof(T)), {rows, y})) {
-    case 32: return combine_as<T, 32, 1>(rows, dest_row, weights, T_, M, H, k, y, status, s);
-    case 16: return combine_as<T, 16, 1>(rows, dest_row, weights, T_, M, H, k, y, status, s);
-    default: return combine_as<T, sizeof(T), 8>(rows, dest_row, weights, T_, M, H, k, y, status, s);
+  const int64_t row_bytes = H * static_cast<int64_t>(sizeof(T));
+  if (width(row_bytes, {rows, y}) < 16) {
+    const int64_t parts = (H + 255) / 256;
+    return launch_pdl(combine_any_kernel<T, sizeof(T), 8>, dim3(blocks_for(T_ * parts, 2)), dim3(kThreads), 0, s,
+                      rows, dest_row, weights, T_, M, H, k, y, status);
   }
+  static std::atomic<uint64_t> devices{0};
+  const cudaError_t e = allow_smem(devices, combine_kernel<T>, sizeof(CombineShared));
+  if (e != cudaSuccess) return e;
+  const int64_t units = T_ * ((row_bytes + kPieceBytes - 1) / kPieceBytes);
+  int64_t ctas = (units + kCombineWarps - 1) / kCombineWarps;
+  if (ctas > num_sms()) ctas = num_sms();
+  return launch_pdl(combine_kernel<T>, dim3(static_cast<unsigned>(ctas)), dim3(32 * kCombineWarps),
+                    sizeof(CombineShared), s, rows, dest_row, weights, T_, M, row_bytes, k, y, status);
 }
 
-template <typename T, int B, int U, bool DOT>
-cudaError_t backward_as(const Matrix& dy, const Matrix& rows, const int32_t* dest_row, const float* weights,
-                        int64_t T_, int64_t M, int64_t H, int k, const Matrix& drows, float* dweights,
-                        int32_t* status, cudaStream_t s) {
-  const int64_t words = H * static_cast<int64_t>(sizeof(T)) / B, parts = (words + 32 * U - 1) / (32 * U);
-  int group = 1;   // warps a token, so that few tokens still fill the SMs
-  if (parts <= 256)   // their sums take 32 KB of shared memory at most
-    while (group < kWarps && group < parts && T_ * group < 16 * static_cast<int64_t>(num_sms())) group *= 2;
-  const size_t smem = group > 1 ? static_cast<size_t>(kWarps / group) * parts * kSlots * sizeof(float) : 0;
-  return launch_pdl(combine_backward_kernel<T, B, U, DOT>, dim3(blocks_for(T_ * group, 2)), dim3(kThreads), smem, s,
-                    dy, rows, dest_row, weights, T_, M, words, k, group, drows, dweights, status);
-}
 template <typename T, bool DOT>
 cudaError_t backward(const Matrix& dy, const Matrix& rows, const int32_t* dest_row, const float* weights, int64_t T_,
                      int64_t M, int64_t H, int k, const Matrix& drows, float* dweights, int32_t* status,
                      cudaStream_t s) {
   const int64_t row_bytes = H * static_cast<int64_t>(sizeof(T));
-  switch (DOT ? width(row_bytes, {dy, rows, drows}) : width(row_bytes, {dy, drows})) {
-    case 32: return backward_as<T, 32, 1, DOT>(dy, rows, dest_row, weights, T_, M, H, k, drows, dweights, status, s);
-    case 16: return backward_as<T, 16, 1, DOT>(dy, rows, dest_row, weights, T_, M, H, k, drows, dweights, status, s);
-    default:
-      return backward_as<T, sizeof(T), 8, DOT>(dy, rows, dest_row, weights, T_, M, H, k, drows, dweights, status, s);
-  }
+  if ((DOT ? width(row_bytes, {dy, rows, drows}) : width(row_bytes, {dy, drows})) < 16)
+    return launch_pdl(combine_backward_any_kernel<T, sizeof(T), 8, DOT>, dim3(blocks_for(T_, 2)), dim3(kThreads), 0, s,
+                      dy, rows, dest_row, weights, T_, M, H, k, drows, dweights, status);
+  static std::atomic<uint64_t> devices{0};
+  const cudaError_t e = allow_smem(devices, combine_backward_kernel<T, DOT>, sizeof(BackwardShared));
+  if (e != cudaSuccess) return e;
+  int team = 1;
+  while (team < kWarps && team * kPieceBytes < row_bytes) team *= 2;
+  const int teams = kWarps / team;
+  int64_t ctas = (T_ + teams - 1) / teams;
+  if (ctas > num_sms()) ctas = num_sms();
+  return launch_pdl(combine_backward_kernel<T, DOT>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads),
+                    sizeof(BackwardShared), s, dy, rows, dest_row, weights, T_, M, row_bytes, k, team, drows, dweights,
+                    status);
 }
 
 // The shape rules that all four entry points share.
 inline int check(int dtype, int64_t T, int64_t M, int64_t H, int32_t k, std::initializer_list<int64_t> strides) {
   if (!dtype_ok(dtype)) return MINITE_ERR_INVALID_ARG;
-  if (T < 0 || M < 0 || H < 1 || H >= (int64_t(1) << 30) || k < 1 || k > 32 || T >= (int64_t(1) << 31) ||
+  if (T < 0 || M < 0 || H < 1 || H > (int64_t(1) << 24) || k < 1 || k > 32 || T >= (int64_t(1) << 31) ||
       T * k >= (int64_t(1) << 31) || M >= (int64_t(1) << 31))
     return MINITE_ERR_UNSUPPORTED_SHAPE;
   for (int64_t s : strides)
@@ -452,6 +898,12 @@ inline Matrix matrix(const void* p, int dtype, int64_t stride) {
 }
 
 }  // namespace rows
+
+// 0: minite_moe_permute_rows takes one launch and needs none.
+size_t permute_rows_workspace_bytes(int64_t T, int E, int k) {
+  return T * k <= rows::kDirectPairs ? 0 : routing_workspace_bytes(T, E, k);
+}
+
 }  // namespace minite
 
 using namespace minite;
@@ -471,19 +923,31 @@ extern "C" int minite_moe_permute_rows(const void* x, int dtype, int64_t x_strid
     return cudaMemsetAsync(expert_offsets, 0, (static_cast<size_t>(E) + 1) * 4, s) == cudaSuccess ? MINITE_OK
                                                                                                   : MINITE_ERR_CUDA;
   const uintptr_t a = static_cast<uintptr_t>(size_of(dtype));
-  if (!x || !topk_ids || !rows_out || !perm_src || !dest_row || !workspace || !aligned(x, a) ||
-      !aligned(rows_out, a) || !aligned(topk_ids, 4) || !aligned(perm_src, 4) || !aligned(dest_row, 4) ||
-      !aligned(workspace, 256) || ws_bytes < routing_workspace_bytes(T, E, k))
+  const size_t need = permute_rows_workspace_bytes(T, E, k);
+  if (!x || !topk_ids || !rows_out || !perm_src || !dest_row || !aligned(x, a) || !aligned(rows_out, a) ||
+      !aligned(topk_ids, 4) || !aligned(perm_src, 4) || !aligned(dest_row, 4) ||
+      (need > 0 && (!workspace || !aligned(workspace, 256) || ws_bytes < need)))
     return MINITE_ERR_INVALID_ARG;
+  const Matrix from = matrix(x, dtype, x_stride), to = matrix(rows_out, dtype, rows_stride);
+  const int64_t row_bytes = H * size_of(dtype);
+  const Sorted o = {expert_offsets, perm_src, dest_row};
   Routing r = {};
   r.ids = topk_ids;
   r.offsets = expert_offsets;
   r.E = E;
   r.dest_row = dest_row;
   r.perm_src = perm_src;
-  launch_routing(topk_ids, T, k, E, workspace, expert_offsets, &r.table, &r.rank, &r.ct, &r.nchunks, status, s);
-  const cudaError_t e = copy(matrix(x, dtype, x_stride), T, H * size_of(dtype), k, r,
-                             matrix(rows_out, dtype, rows_stride), T * k, status, s);
+  cudaError_t e;
+  if (need == 0) {
+    e = range<false>(from, T, row_bytes, k, E, r, o, to, status, s);
+  } else {
+    const int64_t chunks = (T + permute_chunk_tokens(k) - 1) / permute_chunk_tokens(k);
+    const bool scan = T * k > kTablePairs || chunks * E > kTableEntries;
+    launch_routing(topk_ids, T, k, E, workspace, scan ? expert_offsets : nullptr, &r.table, &r.rank, &r.ct,
+                   &r.nchunks, status, s);
+    e = scan ? copy(from, T, row_bytes, k, r, to, T * k, status, s)
+             : range<true>(from, T, row_bytes, k, E, r, o, to, status, s);
+  }
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MINITE_OK : MINITE_ERR_CUDA;
 }
 

@@ -9,7 +9,7 @@
 // execution path".
 //
 // Four launches, no host synchronization:
-//   permute_rank_kernel      one warp per token chunk: stable in-chunk rank of
+//   permute_rank_kernel      one block per token chunk: stable in-chunk rank of
 //                            every (token, slot) pair (kept in dest_row) and
 //                            the chunk's expert histogram -> table[e][chunk];
 //                            also resets the scan's completion counter.
@@ -79,55 +79,44 @@ static PermWs perm_ws(void* ws, int64_t T, int64_t H, int E, int k, bool compact
   return w;
 }
 
-// One warp per chunk of ct tokens (ct * k <= 512 pairs): the stable rank of
-// every pair among the chunk's pairs with the same expert, in pair order, 32
-// pairs at a time. Lanes carrying the same expert find each other with a
-// match, take their order among themselves from the match mask and continue
-// a per-expert running count kept in shared memory; the final counts are the
-// chunk's histogram. The local rank goes to dest_row (completed later).
-constexpr int kRankWarps = 4;  // chunks per block
-__global__ void __launch_bounds__(32 * kRankWarps) permute_rank_kernel(
+// One block per chunk of ct tokens (ct * k <= 512 pairs), one thread a pair: the
+// stable rank of every pair among the chunk's pairs with the same expert, in pair
+// order. A warp's lanes with the same expert find each other by votes on the bits
+// of their ids (a __match_any_sync takes 700 cycles, the ten votes 100), every warp
+// leaves its count of each expert in shared memory, and a pair adds those of the
+// warps in front of its own. The counts' sums are the chunk's histogram. The local
+// rank goes to dest_row (completed later).
+constexpr int kRankThreads = 512;
+constexpr int kRankWarps = kRankThreads / 32;
+__global__ void __launch_bounds__(kRankThreads) permute_rank_kernel(
     const int32_t* __restrict__ ids, int64_t T, int k, int E, int ct, int nchunks,
     int32_t* __restrict__ table, int32_t* __restrict__ dest_row, uint32_t* __restrict__ counter,
     bool negative_ok, int32_t* status) {
+  extern __shared__ __align__(4) uint16_t cnt[];  // [kRankWarps][E]
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  for (int i = tid; i < kRankWarps * E; i += kRankThreads) cnt[i] = 0;
+  __syncthreads();
   pdl_wait();
-  extern __shared__ int32_t cnt_all[];  // [kRankWarps][E]
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int c = blockIdx.x * kRankWarps + wid;
-  int32_t* cnt = cnt_all + wid * E;
-  for (int e = lane; e < E; e += 32) cnt[e] = 0;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0u;
-  __syncwarp();
-  if (c >= nchunks) return;
+  const int c = blockIdx.x;
+  if (c == 0 && tid == 0) *counter = 0u;
   const int64_t p0 = static_cast<int64_t>(c) * ct * k;
   const int npairs = static_cast<int>(min(static_cast<int64_t>(c + 1) * ct, T) * k - p0);
-  bool bad = false;
-  // all of the chunk's ids requested at once (at most 16 per lane)
-  int ids_r[16];
+  const int e = tid < npairs ? ids[p0 + tid] : -1;
+  const bool valid = e >= 0 && e < E;
+  if (tid < npairs && !valid && !(negative_ok && e < 0)) set_status(status, MINITE_ERR_BAD_ROUTING);
+  const uint32_t same = same_id_lanes(valid ? e : E, E);
+  int rank = __popc(same & ((1u << lane) - 1u));
+  if (valid && rank == 0) cnt[wid * E + e] = static_cast<uint16_t>(__popc(same));
+  __syncthreads();
+  if (valid)
+    for (int w = 0; w < wid; ++w) rank += cnt[w * E + e];
+  if (tid < npairs) dest_row[p0 + tid] = valid ? rank : -1;
+  for (int i = tid; i < E; i += kRankThreads) {
+    int n = 0;
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int p = 32 * r + lane;
-    ids_r[r] = p < npairs ? ids[p0 + p] : -1;
+    for (int w = 0; w < kRankWarps; ++w) n += cnt[w * E + i];
+    table[static_cast<int64_t>(i) * nchunks + c] = n;
   }
-#pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int b = 32 * r;
-    if (b >= npairs) break;  // warp-uniform
-    const int p = b + lane;
-    const int e = ids_r[r];
-    const bool valid = e >= 0 && e < E;
-    if (p < npairs && !valid && !(negative_ok && e < 0)) bad = true;
-    const uint32_t mask = __match_any_sync(0xffffffffu, valid ? e : E + lane);
-    const int before = __popc(mask & ((1u << lane) - 1u));
-    const int run = valid ? cnt[e] : 0;
-    __syncwarp();
-    if (valid && before == 0) cnt[e] = run + __popc(mask);
-    __syncwarp();
-    if (p < npairs) dest_row[p0 + p] = valid ? run + before : -1;
-  }
-  if (bad) set_status(status, MINITE_ERR_BAD_ROUTING);
-  __syncwarp();
-  for (int e = lane; e < E; e += 32) table[static_cast<int64_t>(e) * nchunks + c] = cnt[e];
 }
 
 // Exclusive scan of one value per thread over a 256-thread block; returns the
@@ -207,7 +196,8 @@ __global__ void __launch_bounds__(kPermThreads) permute_scan_kernel(
 }
 
 // The ranking and scan alone, for permutations that place rows themselves: a
-// pair's row is expert_offsets[e] + table[e][t / ct] + rank[pair]. A negative id
+// pair's row is expert_offsets[e] + table[e][t / ct] + rank[pair]. Without
+// expert_offsets the ranking alone: table[e][c] is chunk c's count. A negative id
 // is a slot that is not used, without a status bit. Any T >= 1, E <= 1024, k <= 32.
 size_t routing_workspace_bytes(int64_t T, int E, int k) {
   return perm_ws_base_bytes(T, E, k) + align256(static_cast<size_t>(T) * k * 4);
@@ -221,9 +211,10 @@ void launch_routing(const int32_t* ids, int64_t T, int k, int E, void* workspace
   *nchunks = static_cast<int>((T + *ct - 1) / *ct);
   *table = w.table;
   *rank = r;
-  launch_pdl(permute_rank_kernel, dim3((*nchunks + kRankWarps - 1) / kRankWarps), dim3(32 * kRankWarps),
-             kRankWarps * E * sizeof(int32_t), s, ids, T, k, E, *ct, *nchunks, w.table, r, w.counter,
+  launch_pdl(permute_rank_kernel, dim3(*nchunks), dim3(kRankThreads),
+             kRankWarps * E * sizeof(uint16_t), s, ids, T, k, E, *ct, *nchunks, w.table, r, w.counter,
              true, status);
+  if (!expert_offsets) return;   // the chunks' counts themselves
   launch_pdl(permute_scan_kernel, dim3(E), dim3(kPermThreads), 0, s, w.table, *nchunks, E, w.counter,
              w.totals, expert_offsets, static_cast<int32_t*>(nullptr));
 }
@@ -549,9 +540,8 @@ static int permute_quant_impl(const void* x, const int32_t* topk_ids, const floa
   const int nchunks = static_cast<int>((T + ct - 1) / ct);
   PermWs w = perm_ws(workspace, T, H, E, k, compact);
 
-  const int rank_blocks = (nchunks + kRankWarps - 1) / kRankWarps;
-  launch_pdl(permute_rank_kernel, dim3(rank_blocks), dim3(32 * kRankWarps),
-             kRankWarps * E * sizeof(int32_t), s, topk_ids, T, static_cast<int>(k),
+  launch_pdl(permute_rank_kernel, dim3(nchunks), dim3(kRankThreads),
+             kRankWarps * E * sizeof(uint16_t), s, topk_ids, T, static_cast<int>(k),
              static_cast<int>(E), ct, nchunks, w.table, dest_row, w.counter, false, status);
   launch_pdl(permute_scan_kernel, dim3(E), dim3(kPermThreads), 0, s, w.table, nchunks,
              static_cast<int>(E), w.counter, w.totals, expert_offsets, sf_row_offsets);
