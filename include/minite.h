@@ -826,8 +826,9 @@ int minite_moe_combine_rows_backward(const void* dy, int dtype, int64_t dy_strid
  * tensors: HOST array, read during the call (out and out_dtype are ignored).
  * norm, factor: device, float [1], one of them may be NULL.
  * max_norm: at or above 0, infinity allowed.
- * workspace: device, >= minite_workspace_bytes(MINITE_OP_GRAD_NORM, n_tensors, 0,
- *          0, 0) bytes, 8-byte aligned, contents on entry ignored.
+ * workspace: device, >= minite_workspace_bytes(MINITE_OP_GRAD_NORM, n_tensors,
+ *          elements of all tensors, 0, 0) bytes, 8-byte aligned, contents on entry
+ *          ignored; NULL where that is 0.
  */
 typedef struct minite_grad_tensor {
   const void* grad;    /* device, aligned to its element */
@@ -878,14 +879,15 @@ int minite_clip_grads(const minite_grad_tensor* tensors, int64_t n_tensors, cons
  * target: device, BF16 or FP32 [B * (S + 1), V], rows `target_stride` elements apart;
  * draft:  device, BF16 or FP32 [B * S, V] or NULL. Both aligned to the element.
  * draft_tokens: device, int32 [B, S]; uniforms: device, float [B, S], in [0, 1).
- * noise:  device, float [B, V], rows `noise_stride` apart: exponential variates, > 0 (a
- *         token of weight above 0 whose variate is not wins).
+ * noise:  device, float [B, V], rows `noise_stride` apart: exponential variates, of
+ *         2^-100 to 2^90 (a token whose variate is negative or NaN never wins, one whose
+ *         variate is 0 wins where its weight is above 0).
  * tokens: device, int32 [B, S + 1]; accepted: device, int32 [B]; logprobs: device, float
  *         [B, S + 1] or NULL.
  * workspace: device, >= minite_workspace_bytes(MINITE_OP_VERIFY_DRAFTS, B, V, S, 0)
  *         bytes, 256-byte aligned, contents on entry ignored.
  * Shape rules: 0 <= S <= 31 (0: one token is sampled), B >= 0 (0: nothing is enqueued),
- * B (2 S + 1) <= 2^24, 1 <= V < 2^31, B (S + 1) V <= 2^42; log2(e) / temperature fits FP32.
+ * B (2 S + 1) <= 2^24, 1 <= V <= 2^30, B (S + 1) V <= 2^42; log2(e) / temperature fits FP32.
  */
 int minite_verify_drafts(const void* target, int target_dtype, int64_t target_stride,
                          const void* draft, int draft_dtype, int64_t draft_stride,
@@ -900,7 +902,8 @@ int minite_verify_drafts(const void* target, int target_dtype, int64_t target_st
  * a = T, b = H; MINITE_OP_QUANTIZE_TOKENS: a = E, b = source rows when
  * they are gathered and no row maxima are passed, else 0;
  * MINITE_OP_GATE_UP_SWIGLU: a = M_total, b = I; MINITE_OP_PERMUTE_ROWS: a = T, E,
- * k; MINITE_OP_GRAD_NORM: a = tensors; MINITE_OP_VERIFY_DRAFTS: a = B, b = V, E =
+ * k; MINITE_OP_GRAD_NORM: a = tensors, b = their
+ * elements; MINITE_OP_VERIFY_DRAFTS: a = B, b = V, E =
  * S). 0 means none needed. */
 size_t minite_workspace_bytes(int op, int64_t a, int64_t b, int32_t E, int32_t k);
 

@@ -12,7 +12,7 @@ size_t combine_backward_workspace_bytes(int64_t T, int64_t H);
 size_t tokens_workspace_bytes(int32_t E, int64_t x_rows);
 size_t swiglu_fused_workspace_words(int64_t M, int64_t I);
 size_t permute_rows_workspace_bytes(int64_t T, int E, int k);
-size_t grad_norm_workspace_bytes(int64_t n_tensors);
+size_t grad_norm_workspace_bytes(int64_t n_tensors, int64_t elements);
 size_t verify_workspace_bytes(int64_t B, int64_t S, int64_t V);
 
 int num_sms() {
@@ -117,7 +117,7 @@ extern "C" size_t minite_workspace_bytes(int op, int64_t a, int64_t b, int32_t E
     case MINITE_OP_PERMUTE_ROWS:
       return (a > 0 && E > 0 && k > 0) ? permute_rows_workspace_bytes(a, E, k) : 0;
     case MINITE_OP_GRAD_NORM:
-      return a >= 0 ? grad_norm_workspace_bytes(a) : 0;
+      return a >= 0 && b >= 0 ? grad_norm_workspace_bytes(a, b) : 0;
     case MINITE_OP_VERIFY_DRAFTS:
       return (a > 0 && b > 0 && E >= 0) ? verify_workspace_bytes(a, E, b) : 0;
     default:

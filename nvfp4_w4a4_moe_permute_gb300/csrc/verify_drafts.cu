@@ -31,6 +31,7 @@ namespace verify {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kVectors = 4;       // 32-byte vectors a thread holds of its segment
+constexpr int kRaceCtas = 4;      // of an SM
 constexpr int kMaxDrafts = 31;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -202,8 +203,10 @@ __device__ __forceinline__ void segment(const T* row, int64_t V, int seg, int se
     for (int w = 0; w < wid; ++w) first &= s_max[w] != m;
     r += first ? n - 1.0f : n;
   } else {
-    uint64_t acc = pair(ex2((xh - m) * k), ex2((xt - m) * k));
-    const uint64_t minus = pair(-m, -m), k2 = pair(k, k);
+    // x k - m k in one operation: what the product m k lost is a factor of every term
+    const float mk = -(m * k), lost = fmaf(m, k, mk);
+    uint64_t acc = pair(ex2(fmaf(xh, k, mk)), ex2(fmaf(xt, k, mk)));
+    const uint64_t minus = pair(mk, mk), k2 = pair(k, k);
 #pragma unroll
     for (int i = 0; i < kVectors; ++i) {
       float x[kPer];
@@ -211,13 +214,13 @@ __device__ __forceinline__ void segment(const T* row, int64_t V, int seg, int se
 #pragma unroll
       for (int j = 0; j < kPer; j += 2) {
         float a, b;
-        unpair(mul2(add2(pair(x[j], x[j + 1]), minus), k2), a, b);
+        unpair(fma2(pair(x[j], x[j + 1]), k2, minus), a, b);
         acc = add2(acc, pair(ex2(a), ex2(b)));
       }
     }
     float a, b;
     unpair(acc, a, b);
-    r = a + b;
+    r = (a + b) * ex2(-lost);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
   }
@@ -274,21 +277,25 @@ __device__ __forceinline__ Row row_of(const float2* part, int segs, float k) {
   return {v.x, log1pf(v.y)};
 }
 
-// The race: the largest weight / variate, the lower index where they are equal.
+// The race: the largest weight / variate, the lower index where they are equal. No
+// weight above 0: v stays 0.
 struct Lead {
-  float v = -1.0f;
+  float v = 0.0f;
   int32_t j = 0;
+  // weight times the variate's reciprocal, within 2 units; offered in rising order
   __device__ __forceinline__ void offer(float weight, float e, int32_t at) {
-    if (!(weight > 0.0f)) return;
-    const float q = e > 0.0f ? __fdividef(weight, e) : INFINITY;   // within 2 units
+    float q;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(e));
+    q *= weight;
     if (q > v) {
       v = q;
       j = at;
     }
   }
   __device__ __forceinline__ unsigned long long key() const {
-    return v < 0.0f ? 0ull : (static_cast<unsigned long long>(__float_as_uint(v)) << 32) |
-                                 (0xFFFFFFFFu - static_cast<uint32_t>(j));
+    return v > 0.0f ? (static_cast<unsigned long long>(__float_as_uint(v)) << 32) |
+                          (0xFFFFFFFFu - static_cast<uint32_t>(j))
+                    : 0ull;
   }
 };
 __device__ __forceinline__ unsigned long long warp_larger(unsigned long long v) {
@@ -301,41 +308,49 @@ __device__ __forceinline__ unsigned long long warp_larger(unsigned long long v) 
 }
 
 constexpr int kAhead = 8;   // elements of a thread in flight
+constexpr int kRound = kThreads * kAhead;
 
 // Elements [j0, j1) of the race. WITH_Q: less the draft's probabilities; otherwise
-// token `without` has none.
+// token `without` has none. Some 20 instructions an element; whole rounds carry no
+// checks (with them, 60).
 template <bool WITH_Q, typename T, typename D>
 __device__ __forceinline__ Lead race(const T* xt, const D* xd, const float* noise, Row rt, Row rd, float k,
-                                     int32_t without, int64_t j0, int64_t j1) {
+                                     int32_t without, int32_t j0, int32_t j1) {
   Lead lead;
   const float st = rt.log_s * kLog2e, sd = rd.log_s * kLog2e;
-  for (int64_t base = j0 + threadIdx.x; base < j1; base += kThreads * kAhead) {
-    float a[kAhead], b[kAhead], e[kAhead];
+  auto weight = [&](T a, D b, int32_t j) {
+    float w = rt.p(value(a), k, st);
+    if (WITH_Q) w -= rd.p(value(b), k, sd);
+    else if (j == without) w = 0.0f;
+    return w;
+  };
+  auto round = [&](int32_t j, bool whole) {
+    const T* pa = xt + j;
+    const D* pb = xd + j;
+    const float* pe = noise + j;
+    T a[kAhead];
+    D b[kAhead];
+    float e[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int64_t j = base + i * kThreads;
-      if (j < j1) {
-        a[i] = value(xt[j]);
-        e[i] = noise[j];
-        if (WITH_Q) b[i] = value(xd[j]);
+    for (int i = 0; i < kAhead; ++i)
+      if (whole || j + i * kThreads < j1) {
+        e[i] = pe[i * kThreads];
+        a[i] = pa[i * kThreads];
+        if (WITH_Q) b[i] = pb[i * kThreads];
       }
-    }
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int64_t j = base + i * kThreads;
-      if (j < j1) {
-        float w = rt.p(a[i], k, st);
-        if (WITH_Q) w -= rd.p(b[i], k, sd);
-        else if (j == without) w = 0.0f;
-        lead.offer(w, e[i], static_cast<int32_t>(j));
-      }
-    }
-  }
+    for (int i = 0; i < kAhead; ++i)
+      if (whole || j + i * kThreads < j1)
+        lead.offer(weight(a[i], b[i], j + i * kThreads), e[i], j + i * kThreads);
+  };
+  int32_t j = j0;
+  for (; j1 - j >= kRound; j += kRound) round(j + threadIdx.x, true);
+  if (j < j1) round(j + threadIdx.x, false);
   return lead;
 }
 
 template <typename T, typename D>
-__global__ void __launch_bounds__(kThreads, 4) race_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, kRaceCtas) race_kernel(const Params p) {
   __shared__ Row s_target[kMaxDrafts + 1], s_draft[kMaxDrafts + 1];
   __shared__ uint8_t s_given[kMaxDrafts + 1], s_stands[kMaxDrafts + 1];
   __shared__ unsigned long long s_best[kWarps];
@@ -382,7 +397,9 @@ __global__ void __launch_bounds__(kThreads, 4) race_kernel(const Params p) {
   const float* noise = p.noise + b * p.noise_ld;
   unsigned long long best = 0;
   if (usable) {
-    const int64_t j0 = p.V * rank / p.ctas, j1 = p.V * (rank + 1) / p.ctas;
+    const int32_t rounds = static_cast<int32_t>((p.V + kRound - 1) / kRound);   // whole ones a CTA, but for the last
+    const int32_t j0 = static_cast<int32_t>(static_cast<int64_t>(rounds) * rank / p.ctas) * kRound;
+    const int32_t j1 = min(static_cast<int32_t>(p.V), static_cast<int32_t>(static_cast<int64_t>(rounds) * (rank + 1) / p.ctas) * kRound);
     Lead lead;
     if (falls && draft)
       lead = race<true>(xt, draft + n * p.draft_ld, noise, rt, rd, p.k2, -1, j0, j1);
@@ -403,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 4) race_kernel(const Params p) {
   __threadfence();
   best = *reinterpret_cast<volatile unsigned long long*>(p.best + b);
   if (usable && best == 0) {   // q is as large as p everywhere but for roundings: p itself
-    best = warp_larger(race<false>(xt, xt, noise, rt, rt, p.k2, -1, 0, p.V).key());
+    best = warp_larger(race<false>(xt, xt, noise, rt, rt, p.k2, -1, 0, static_cast<int32_t>(p.V)).key());
     if (lane == 0) s_best[wid] = best;
     __syncthreads();
     for (int w = 0; w < kWarps; ++w) best = s_best[w] > best ? s_best[w] : best;
@@ -432,8 +449,9 @@ cudaError_t launch(Params& p, int64_t B, cudaStream_t s) {
   // CTAs of a sequence: one round of its threads' loads each where sequences are
   // few, otherwise as many as are resident at once (the look at the drafts costs every
   // CTA some 3 us)
-  int64_t ctas = (p.V + kThreads * kAhead - 1) / (kThreads * kAhead);
-  const int64_t fill = 4 * static_cast<int64_t>(num_sms()) / B > 1 ? 4 * static_cast<int64_t>(num_sms()) / B : 1;
+  int64_t ctas = (p.V + kRound - 1) / kRound;
+  const int64_t resident = kRaceCtas * static_cast<int64_t>(num_sms());
+  const int64_t fill = resident / B > 1 ? resident / B : 1;
   if (ctas > fill) ctas = fill;
   p.ctas = static_cast<int>(ctas);
   return launch_pdl(race_kernel<T, D>, dim3(static_cast<unsigned>(B * ctas)), dim3(kThreads), 0, s, p);
@@ -470,7 +488,7 @@ extern "C" int minite_verify_drafts(const void* target, int target_dtype, int64_
   if ((!tf && target_dtype != MINITE_OUT_BF16) || (draft && !df && draft_dtype != MINITE_OUT_BF16) ||
       !(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(kLog2e / temperature))
     return MINITE_ERR_INVALID_ARG;
-  if (B < 0 || S < 0 || S > kMaxDrafts || V < 1 || V > 0x7FFFFFFF || B > (int64_t(1) << 31) ||
+  if (B < 0 || S < 0 || S > kMaxDrafts || V < 1 || V > (int64_t(1) << 30) || B > (int64_t(1) << 31) ||
       B * (S + 1) * V > (int64_t(1) << 42) || B * (2 * S + 1) > (int64_t(1) << 24) || target_stride < V ||
       (draft && draft_stride < V) || noise_stride < V)
     return MINITE_ERR_UNSUPPORTED_SHAPE;

@@ -653,7 +653,7 @@ def minite_moe_combine_rows_backward(dy, rows, dest_row, weights, drows, dweight
 
 def _grad_table(grads, outs, name):
     """struct minite_grad_tensor of every gradient and its destination (outs may be
-    grads), and the device."""
+    grads), the device, and the number of elements."""
     if len(grads) == 0:
         raise MiniteError(f"{name}: needs gradients")
     d = _device(grads[0])
@@ -672,21 +672,21 @@ def _grad_table(grads, outs, name):
         raise MiniteError(f"{name}: gradients and destinations are contiguous")
     if None in kinds or None in out_kinds:
         raise MiniteError(f"{name}: expected bfloat16 or float32")
-    for t in tensors:
-        if t.get_device() != d:
-            raise _elsewhere("tensor", t.get_device(), d)
+    places = [t.get_device() for t in tensors]
+    if places.count(d) != len(places):
+        raise _elsewhere("tensor", next(i for i in places if i != d), d)
     table = array("q", bytes(32 * len(grads)))
     table[0::4] = array("q", at)
     table[1::4] = array("q", out_at)
     table[2::4] = array("q", sizes)
     table[3::4] = array("q", [a | b << 32 for a, b in zip(kinds, out_kinds)])
-    return table, d
+    return table, d, sum(sizes)
 
 
 def minite_grad_norm(grads, order, max_norm, norm, factor, workspace, stream=None, table=None):
     """grads: contiguous bf16 or fp32 tensors; norm and factor fp32 [1], one of them may be None."""
     name = "minite_grad_norm"
-    table, d = _grad_table(grads, grads, name) if table is None else table
+    table, d, _ = _grad_table(grads, grads, name) if table is None else table
     rc = load().minite_grad_norm(table.buffer_info()[0], len(grads), order, max_norm,
                                  _f32(norm, (1,), name, "norm", d), _f32(factor, (1,), name, "factor", d),
                                  _ptr(workspace, d), _bytes(workspace), _raw(stream, d))
@@ -697,7 +697,7 @@ def minite_grad_norm(grads, order, max_norm, norm, factor, workspace, stream=Non
 def minite_clip_grads(grads, outs, factor, stream=None, table=None):
     """outs[i] = grads[i] * factor; outs[i] may be grads[i]; factor fp32 [1]."""
     name = "minite_clip_grads"
-    table, d = _grad_table(grads, outs, name) if table is None else table
+    table, d, _ = _grad_table(grads, outs, name) if table is None else table
     rc = load().minite_clip_grads(table.buffer_info()[0], len(grads), _f32(factor, (1,), name, "factor", d),
                                   _raw(stream, d))
     if rc:
@@ -714,28 +714,37 @@ def _sequence_rows(t, name, what):
     return ld
 
 
+def _verify(target, draft, draft_tokens, uniforms, noise, temperature, tokens, accepted, logprobs, workspace,
+            ws_bytes, status, stream, d, name):
+    """The inputs' checks and the call; outputs are addresses."""
+    B, S1, V = target.shape
+    S = _shape(draft_tokens, 2, name, "draft_tokens")[1]
+    if S1 != S + 1 or (draft is not None and draft.shape != (B, S, V)):
+        raise MiniteError(f"{name}: the target's logits are [B, S + 1, V], the draft's [B, S, V], draft_tokens [B, S]")
+    if noise.dtype is not torch.float32 or noise.shape != (B, V):
+        raise MiniteError(f"{name}: noise is float32 [B, V]")
+    draft_at, draft_dtype, draft_ld = None, OUT_BF16, V
+    if draft is not None and S:
+        draft_at, draft_dtype, draft_ld = _ptr(draft, d), _dtype(draft, name), _sequence_rows(draft, name, "draft")
+    rc = load().minite_verify_drafts(
+        target.data_ptr(), _dtype(target, name), _sequence_rows(target, name, "target"), draft_at, draft_dtype,
+        draft_ld, _int32(draft_tokens, (B, S), name, "draft_tokens", d),
+        _f32(uniforms, (B, S), name, "uniforms", d), _ptr(noise, d), _rows(noise, name), B, S, V, temperature,
+        tokens, accepted, logprobs, workspace, ws_bytes, _status(status, name, d), _raw(stream, d))
+    if rc:
+        _check(rc, "minite_verify_drafts")
+
+
 def minite_verify_drafts(target, draft, draft_tokens, uniforms, noise, temperature, tokens, accepted, logprobs,
                          workspace, status=None, stream=None):
     """target [B, S + 1, V], draft [B, S, V] (or None) bf16 or fp32; draft_tokens int32 and uniforms
     fp32 [B, S]; noise fp32 [B, V]; tokens int32 and logprobs (or None) fp32 [B, S + 1]; accepted int32 [B]."""
     name = "minite_verify_drafts"
-    B, S1, V = _shape(target, 3, name, "target")
-    S = _shape(draft_tokens, 2, name, "draft_tokens")[1]
-    if S1 != S + 1 or (draft is not None and draft.shape != (B, S, V)):
-        raise MiniteError(f"{name}: target is [B, S + 1, V], draft [B, S, V], draft_tokens [B, S]")
-    if noise.dtype is not torch.float32 or noise.shape != (B, V):
-        raise MiniteError(f"{name}: noise is float32 [B, V]")
+    B, S1, _ = _shape(target, 3, name, "target")
     d = _device(target)
-    ld = _sequence_rows(target, name, "target")
-    rc = load().minite_verify_drafts(
-        target.data_ptr(), _dtype(target, name), ld, _ptr(draft, d), 0 if draft is None else _dtype(draft, name),
-        0 if draft is None else _sequence_rows(draft, name, "draft") if S else V,
-        _int32(draft_tokens, (B, S), name, "draft_tokens", d), _f32(uniforms, (B, S), name, "uniforms", d),
-        _ptr(noise, d), _rows(noise, name), B, S, V, temperature, _int32(tokens, (B, S1), name, "tokens", d),
-        _int32(accepted, (B,), name, "accepted", d), _f32(logprobs, (B, S1), name, "logprobs", d),
-        _ptr(workspace, d), _bytes(workspace), _status(status, name, d), _raw(stream, d))
-    if rc:
-        _check(rc, name)
+    _verify(target, draft, draft_tokens, uniforms, noise, temperature, _int32(tokens, (B, S1), name, "tokens", d),
+            _int32(accepted, (B,), name, "accepted", d), _f32(logprobs, (B, S1), name, "logprobs", d),
+            _ptr(workspace, d), _bytes(workspace), status, stream, d, name)
 
 
 # struct minite_adamw_tensor
@@ -959,7 +968,7 @@ def _norm_of(grads, max_norm, order, stream, table, name):
     like = grads[0]
     norm, scale = _empty((1,), torch.float32, like, stream), _empty((1,), torch.float32, like, stream)
     minite_grad_norm(grads, NORM_2 if order == 2 else NORM_MAX, max_norm, norm, scale,
-                     _workspace(OP_GRAD_NORM, like, stream, len(grads)), stream, table)
+                     _workspace(OP_GRAD_NORM, like, stream, len(grads), table[2]), stream, table)
     return {"norm": norm, "scale": scale}
 
 
@@ -989,11 +998,13 @@ def verify_drafts(logits, draft_tokens, uniforms, noise, draft_logits=None, temp
     dict(tokens [B, S + 1], accepted [B], logprobs [B, S + 1]): the drafts that stand,
     the token that follows them, -1."""
     B, S1, V = _shape(logits, 3, "verify_drafts", "logits")
-    S = _shape(draft_tokens, 2, "verify_drafts", "draft_tokens")[1]
+    d = _device(logits)
     tokens, accepted = _empty((B, S1), torch.int32, logits, stream), _empty((B,), torch.int32, logits, stream)
     logprobs = _empty((B, S1), torch.float32, logits, stream)
-    minite_verify_drafts(logits, draft_logits, draft_tokens, uniforms, noise, temperature, tokens, accepted,
-                         logprobs, _workspace(OP_VERIFY_DRAFTS, logits, stream, B, V, S), status, stream)
+    n = load().minite_workspace_bytes(OP_VERIFY_DRAFTS, B, V, S1 - 1, 0)
+    ws = _empty((n,), torch.uint8, logits, stream)
+    _verify(logits, draft_logits, draft_tokens, uniforms, noise, temperature, tokens.data_ptr(), accepted.data_ptr(),
+            logprobs.data_ptr(), ws.data_ptr(), n, status, stream, d, "verify_drafts")
     return {"tokens": tokens, "accepted": accepted, "logprobs": logprobs}
 
 
