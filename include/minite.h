@@ -817,8 +817,8 @@ int minite_moe_combine_rows_backward(const void* dy, int dtype, int64_t dy_strid
  *   norm = sqrt(sum g^2) over all elements of all tensors (MINITE_NORM_2), or the
  *          largest |g| (MINITE_NORM_MAX)
  *   factor = min(1, max_norm / (norm + 1e-6))
- * Squares are added in FP32 64 at a time, all else in 64 bits, in an order that
- * depends on the tensors' sizes and the device alone. Nothing overflows or
+ * Squares are added in FP32 up to 64 at a time, all else in 64 bits, in an order that
+ * depends on the tensors' sizes, their addresses modulo 32 and the device alone. Nothing overflows or
  * vanishes on the way: norm is infinite only where it does not fit FP32. A NaN
  * among the gradients makes both NaN, an infinity norm infinite and factor 0. No
  * elements: norm 0.
