@@ -253,7 +253,7 @@ __device__ __forceinline__ void write_norm(double total, double max_norm, float*
 
 template <int CAP, bool MAX, Kind KIND>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_kernel(const __grid_constant__ Batch<CAP> b,
-                                                                      double* __restrict__ partial) {
+                                                                      double* partial) {
   pdl_wait();
   const double part = part_of<CAP, MAX, KIND>(b, blockIdx.x, gridDim.x);
   if (threadIdx.x == 0) partial[blockIdx.x] = part;
@@ -314,7 +314,7 @@ __device__ __forceinline__ void scale_chunk(const Tensor& t, int64_t index, floa
 constexpr int kClipBlocksPerSm = 3;
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, kClipBlocksPerSm) clip_kernel(const __grid_constant__ Batch<CAP> b,
-                                                                          const float* __restrict__ factor,
+                                                                          const float* factor,
                                                                           bool in_place) {
   pdl_wait();
   const float f = *factor;
@@ -481,8 +481,12 @@ extern "C" int minite_clip_grads(const minite_grad_tensor* tensors, int64_t n_te
   const int rc = check(tensors, n_tensors, true);
   if (rc != MINITE_OK) return rc;
   if (!factor || !aligned(factor, 4)) return MINITE_ERR_INVALID_ARG;
-  bool in_place = true;
-  for (int64_t i = 0; i < n_tensors; ++i) in_place &= tensors[i].n == 0 || tensors[i].out == tensors[i].grad;
+  bool in_place = true, any = false;
+  for (int64_t i = 0; i < n_tensors; ++i) {
+    any |= tensors[i].n > 0;
+    in_place &= tensors[i].n == 0 || tensors[i].out == tensors[i].grad;
+  }
+  if (!any) return MINITE_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t e = n_tensors <= kSmall ? clip_as<kSmall>(tensors, n_tensors, factor, in_place, s)
                                             : clip_as<kLarge>(tensors, n_tensors, factor, in_place, s);

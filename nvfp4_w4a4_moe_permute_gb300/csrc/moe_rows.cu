@@ -181,7 +181,7 @@ constexpr int64_t kTablePairs = 65536;
 constexpr int64_t kTableEntries = 16384;   // of chunks x experts: what a CTA reads
 constexpr int kRangeThreads = 512;
 constexpr int kRangeWarps = kRangeThreads / 32;
-// A range then has at most 65536 / 152 slots and lies in two chunks at most.
+// A range is no longer than a chunk then (65536 / 152 slots), and lies in two at most.
 
 // Sum of v over the threads in front of this one, and over all.
 __device__ __forceinline__ int scan_before(int v, int* s_warp, int* total) {
@@ -207,9 +207,9 @@ __device__ __forceinline__ int scan_before(int v, int* s_warp, int* total) {
 
 template <int B, int U, bool TABLE>
 __global__ void __launch_bounds__(kRangeThreads, 1) range_kernel(
-    Matrix x, int64_t T, int64_t words, int k, int E, const int32_t* __restrict__ ids,
-    const int32_t* __restrict__ table, const int32_t* __restrict__ rank, int ct, int nchunks,
-    int32_t* __restrict__ offsets, int32_t* __restrict__ perm_src, int32_t* __restrict__ dest_row, Matrix out,
+    Matrix x, int64_t T, int64_t words, int k, int E, const int32_t* ids,
+    const int32_t* table, const int32_t* rank, int ct, int nchunks,
+    int32_t* offsets, int32_t* perm_src, int32_t* dest_row, Matrix out,
     int32_t* status) {
   extern __shared__ int32_t sm[];
   __shared__ int s_warp[kRangeWarps];
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kRangeThreads, 1) range_kernel(
     if ((reinterpret_cast<uintptr_t>(ids) & 15) == 0) {
       const int4* ids4 = reinterpret_cast<const int4*>(ids);
       for (int q = tid; q < pairs / 4; q += kRangeThreads) {
-        const int4 a = __ldg(ids4 + q);
+        const int4 a = ids4[q];
         count(4 * q, a.x);
         count(4 * q + 1, a.y);
         count(4 * q + 2, a.z);
@@ -398,7 +398,7 @@ struct CombineShared {
 };
 template <typename T>
 __global__ void __launch_bounds__(32 * kCombineWarps, 1) combine_kernel(
-    Matrix rows, const int32_t* __restrict__ dest_row, const float* __restrict__ weights, int64_t T_, int64_t M,
+    Matrix rows, const int32_t* dest_row, const float* weights, int64_t T_, int64_t M,
     int64_t row_bytes, int k, Matrix y, int32_t* status) {
   using V = Values<T, 16>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -488,8 +488,8 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 1) combine_kernel(
 
 // The same for rows of any alignment, U elements of 32 lanes a unit.
 template <typename T, int B, int U>
-__global__ void __launch_bounds__(kThreads, 2) combine_any_kernel(Matrix rows, const int32_t* __restrict__ dest_row,
-                                                              const float* __restrict__ weights, int64_t T_,
+__global__ void __launch_bounds__(kThreads, 2) combine_any_kernel(Matrix rows, const int32_t* dest_row,
+                                                              const float* weights, int64_t T_,
                                                               int64_t M, int64_t words, int k, Matrix y,
                                                               int32_t* status) {
   using V = Values<T, B>;
@@ -576,8 +576,8 @@ struct BackwardShared {
 };
 template <typename T, bool DOT>
 __global__ void __launch_bounds__(kThreads, 1) combine_backward_kernel(
-    Matrix dy, Matrix rows, const int32_t* __restrict__ dest_row, const float* __restrict__ weights, int64_t T_,
-    int64_t M, int64_t row_bytes, int k, int team, Matrix drows, float* __restrict__ dweights, int32_t* status) {
+    Matrix dy, Matrix rows, const int32_t* dest_row, const float* weights, int64_t T_,
+    int64_t M, int64_t row_bytes, int k, int team, Matrix drows, float* dweights, int32_t* status) {
   using V = Values<T, 16>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   BackwardShared& S = *reinterpret_cast<BackwardShared*>(smem_raw);
@@ -709,8 +709,8 @@ __global__ void __launch_bounds__(kThreads, 1) combine_backward_kernel(
 // order.
 template <typename T, int B, int U, bool DOT>
 __global__ void __launch_bounds__(kThreads, 2) combine_backward_any_kernel(
-    Matrix dy, Matrix rows, const int32_t* __restrict__ dest_row, const float* __restrict__ weights,
-    int64_t T_, int64_t M, int64_t words, int k, Matrix drows, float* __restrict__ dweights,
+    Matrix dy, Matrix rows, const int32_t* dest_row, const float* weights,
+    int64_t T_, int64_t M, int64_t words, int k, Matrix drows, float* dweights,
     int32_t* status) {
   using V = Values<T, B>;
   pdl_wait();
@@ -942,7 +942,8 @@ extern "C" int minite_moe_permute_rows(const void* x, int dtype, int64_t x_strid
     e = range<false>(from, T, row_bytes, k, E, r, o, to, status, s);
   } else {
     const int64_t chunks = (T + permute_chunk_tokens(k) - 1) / permute_chunk_tokens(k);
-    const bool scan = T * k > kTablePairs || chunks * E > kTableEntries;
+    const int64_t range_tokens = (T + num_sms() - 1) / num_sms();
+    const bool scan = T * k > kTablePairs || chunks * E > kTableEntries || range_tokens > permute_chunk_tokens(k);
     launch_routing(topk_ids, T, k, E, workspace, scan ? expert_offsets : nullptr, &r.table, &r.rank, &r.ct,
                    &r.nchunks, status, s);
     e = scan ? copy(from, T, row_bytes, k, r, to, T * k, status, s)
