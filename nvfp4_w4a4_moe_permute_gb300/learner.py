@@ -8,13 +8,13 @@ The model is one MoE layer with a residual and an output head:
     logits = y head^T                           BF16 product, one expert
     loss   = -mean(advantage * logprob(token)) - entropy_bonus * mean(entropy)
 
-and a step is forward, loss, BF16 backward, AdamW on FP32 master weights, and
-the requantization of the new weights:
+and a step is forward, loss, BF16 backward, the gradients' norm and clipping factor,
+AdamW on FP32 master weights, and the requantization of the new weights:
 
     python -m nvfp4_w4a4_moe_permute_gb300.learner --steps 8
 
-Every product, softmax, optimizer step and quantization runs in the library's
-kernels; torch provides memory, the gathers of rows and the residual sum.
+Every product, softmax, movement of rows, optimizer step and quantization runs in the
+library's kernels; torch provides memory and the residual sum.
 """
 from __future__ import annotations
 
@@ -56,6 +56,7 @@ class PolicyLearner:
                       torch.empty(rows, dtype=f32, device=d))
         self.logits = torch.empty((T, V), dtype=bf, device=d)
         self.dx_rows = torch.empty((rows, H), dtype=bf, device=d)
+        self.in_order = torch.empty((rows, H), dtype=bf, device=d)   # dy, then x, in expert order
         self.all_rows = torch.tensor([0, T], dtype=torch.int32, device=d)
         self.status = self.mlp.status
         self.requantize()
@@ -90,7 +91,6 @@ class PolicyLearner:
         one more micro-batch); returns the gradient of x. The logits' buffer
         becomes their gradient."""
         mlp, st = self.mlp, self.status
-        src = mlp.perm_src.long()
         d = M.token_logprobs_backward(self.logits, tokens, out, grad_logprob, grad_entropy,
                                       self.temperature, out=self.logits, status=st)
         gwgu, gwd, ghead = self.grads
@@ -98,24 +98,32 @@ class PolicyLearner:
                              accumulate=accumulate, status=st)
         dy = M.grouped_gemm_bf16(d, self.head.view(1, self.V, self.H), self.all_rows, w_as_stored=True,
                                  status=st)
-        dd = dy[src]                                          # the combine's backward
+        dd = M.spread_rows(dy, mlp.dest_row, self.in_order, status=st)   # the combine's backward
         M.grouped_wgrad_bf16(dd, self.h, mlp.offsets, out=gwd, accumulate=accumulate, status=st)
         dh = M.grouped_gemm_bf16(dd, self.wd, mlp.offsets, w_as_stored=True, status=st)
         M.minite_swiglu_backward_quant_keep(mlp.gate_up, dh, mlp.perm_w, self.E, mlp.offsets,
                                             mlp.sf_offsets, *self.dgu_q, self.dgu, st)
-        M.grouped_wgrad_bf16(self.dgu, x[src], mlp.offsets, out=gwgu, accumulate=accumulate, status=st)
+        x_rows = M.spread_rows(x, mlp.dest_row, self.in_order, status=st)
+        M.grouped_wgrad_bf16(self.dgu, x_rows, mlp.offsets, out=gwgu, accumulate=accumulate, status=st)
         M.grouped_gemm_bf16(self.dgu, self.wgu, mlp.offsets, w_as_stored=True, out=self.dx_rows, status=st)
         dx = torch.empty_like(x)
         M.minite_moe_combine(self.dx_rows, mlp.dest_row, dx, st)
         return dx + dy
 
-    def step(self, x, topk_ids, topk_w, tokens, advantages, grad_scale=None):
+    def step(self, x, topk_ids, topk_w, tokens, advantages, grad_scale=None, max_grad_norm=None):
         """Forward, backward, optimizer step and requantization; returns the
-        forward's result. ``advantages`` fp32 [T]."""
+        forward's result. ``advantages`` fp32 [T]. With ``max_grad_norm`` the
+        gradients' global norm is clipped to it (its value, a device scalar, is
+        ``grad_norm`` of the result), in place of a ``grad_scale``."""
+        if grad_scale is not None and max_grad_norm is not None:
+            raise M.MiniteError("PolicyLearner.step: either grad_scale or max_grad_norm")
         out = self.forward(x, topk_ids, topk_w, tokens)
         n = self.T
         self.backward(x, tokens, out, advantages * (-1.0 / n),
                       torch.full_like(advantages, -self.entropy_bonus / n) if self.entropy_bonus else None)
+        if max_grad_norm is not None:
+            r = M.grad_norm(self.grads, max_grad_norm)
+            grad_scale, out["grad_norm"] = r["scale"], r["norm"]
         self.optimizer.step(self.grads, grad_scale=grad_scale)
         self.requantize()
         return out
@@ -138,18 +146,20 @@ def main():
     for name, value in (("tokens", 4096), ("hidden", 2048), ("inter", 768), ("experts", 128),
                         ("topk", 8), ("vocab", 32768), ("steps", 8)):
         ap.add_argument("--" + name, type=int, default=value)
+    ap.add_argument("--max-grad-norm", type=float, default=None)
     a = ap.parse_args()
     learner = PolicyLearner(a.tokens, a.hidden, a.inter, a.experts, a.topk, a.vocab)
     x, ids, w, tokens, adv = synthetic_batch(a.tokens, a.hidden, a.experts, a.topk, a.vocab)
     begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
     for i in range(a.steps):
         begin.record()
-        out = learner.step(x, ids, w, tokens, adv)
+        out = learner.step(x, ids, w, tokens, adv, max_grad_norm=a.max_grad_norm)
         end.record()
         end.synchronize()
         print(f"step {i}: mean advantage * logprob {(adv * out['logprob']).mean().item():.4f}, "
               f"entropy {out['entropy'].mean().item():.3f}, {begin.elapsed_time(end):.2f} ms, "
-              f"device status {int(learner.status.item())}")
+              f"device status {int(learner.status.item())}"
+              + (f", gradient norm {out['grad_norm'].item():.4f}" if "grad_norm" in out else ""))
 
 
 if __name__ == "__main__":
