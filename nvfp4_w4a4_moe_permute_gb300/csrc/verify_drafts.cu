@@ -235,6 +235,7 @@ __device__ __forceinline__ void segment(const T* row, int64_t V, int seg, int se
 template <typename T, typename D>
 __global__ void __launch_bounds__(kThreads) stats_kernel(const Params p, int64_t B) {
   pdl_wait();
+  pdl_trigger();
   const int64_t target_units = B * (p.S + 1) * p.target_segs;
   int64_t u = blockIdx.x;
   if (u < target_units) {
@@ -355,9 +356,19 @@ __global__ void __launch_bounds__(kThreads, kRaceCtas) race_kernel(const Params 
   __shared__ uint8_t s_given[kMaxDrafts + 1], s_stands[kMaxDrafts + 1];
   __shared__ unsigned long long s_best[kWarps];
   __shared__ int s_last;
-  pdl_wait();
   const int64_t b = div_nonneg(blockIdx.x, p.ctas);
   const int rank = static_cast<int>(blockIdx.x - b * p.ctas);
+  // whole rounds a CTA, but for the last
+  const int32_t rounds = static_cast<int32_t>((p.V + kRound - 1) / kRound);
+  const int32_t j0 = static_cast<int32_t>(static_cast<int64_t>(rounds) * rank / p.ctas) * kRound;
+  const int32_t j1 = min(static_cast<int32_t>(p.V),
+                         static_cast<int32_t>(static_cast<int64_t>(rounds) * (rank + 1) / p.ctas) * kRound);
+  const float* noise = p.noise + b * p.noise_ld;
+  // the variates that this CTA will need, into L2 while the statistics are finished
+  // and the drafts looked at
+  for (int32_t j = j0 + 32 * static_cast<int32_t>(threadIdx.x); j < j1; j += 32 * kThreads)
+    asm volatile("prefetch.global.L2 [%0];" :: "l"(noise + j));
+  pdl_wait();
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const T* target = static_cast<const T*>(p.target) + b * (p.S + 1) * p.target_ld;
   const D* draft = p.draft ? static_cast<const D*>(p.draft) + b * p.S * p.draft_ld : nullptr;
@@ -394,12 +405,8 @@ __global__ void __launch_bounds__(kThreads, kRaceCtas) race_kernel(const Params 
   const Row rt = s_target[n], rd = s_draft[n];
   const bool usable = rt.usable() && (!falls || rd.usable());
   const T* xt = target + n * p.target_ld;
-  const float* noise = p.noise + b * p.noise_ld;
   unsigned long long best = 0;
   if (usable) {
-    const int32_t rounds = static_cast<int32_t>((p.V + kRound - 1) / kRound);   // whole ones a CTA, but for the last
-    const int32_t j0 = static_cast<int32_t>(static_cast<int64_t>(rounds) * rank / p.ctas) * kRound;
-    const int32_t j1 = min(static_cast<int32_t>(p.V), static_cast<int32_t>(static_cast<int64_t>(rounds) * (rank + 1) / p.ctas) * kRound);
     Lead lead;
     if (falls && draft)
       lead = race<true>(xt, draft + n * p.draft_ld, noise, rt, rd, p.k2, -1, j0, j1);

@@ -13,6 +13,7 @@ import ctypes
 import math
 import os
 from array import array
+from itertools import chain
 
 import numpy as np
 import torch
@@ -573,8 +574,8 @@ def _bytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
-def _same_type(name, *tensors):
-    if any(t is not None and t.dtype is not tensors[0].dtype for t in tensors):
+def _same_type(a, b, name):
+    if a.dtype is not b.dtype:
         raise MiniteError(f"{name}: the matrices have one type")
 
 
@@ -584,7 +585,7 @@ def minite_moe_permute_rows(x, topk_ids, E, rows, expert_offsets, perm_src, dest
     name = "minite_moe_permute_rows"
     T, H = _shape(x, 2, name, "x")
     k = _shape(topk_ids, 2, name, "topk_ids")[1]
-    _same_type(name, x, rows)
+    _same_type(x, rows, name)
     if rows.shape != (T * k, H):
         raise MiniteError(f"{name}: rows is [T * k, H]")
     d = _device(x)
@@ -602,7 +603,7 @@ def minite_moe_spread_rows(x, dest_row, rows, status=None, stream=None):
     name = "minite_moe_spread_rows"
     T, H = _shape(x, 2, name, "x")
     k = _shape(dest_row, 2, name, "dest_row")[1]
-    _same_type(name, x, rows)
+    _same_type(x, rows, name)
     M, Hr = _shape(rows, 2, name, "rows")
     if Hr != H:
         raise MiniteError(f"{name}: shapes of x and rows do not match")
@@ -619,7 +620,7 @@ def minite_moe_combine_rows(rows, dest_row, weights, y, status=None, stream=None
     name = "minite_moe_combine_rows"
     M, H = _shape(rows, 2, name, "rows")
     T, k = _shape(dest_row, 2, name, "dest_row")
-    _same_type(name, rows, y)
+    _same_type(rows, y, name)
     if y.shape != (T, H):
         raise MiniteError(f"{name}: y is [T, H]")
     d = _device(rows)
@@ -637,7 +638,9 @@ def minite_moe_combine_rows_backward(dy, rows, dest_row, weights, drows, dweight
     name = "minite_moe_combine_rows_backward"
     T, H = _shape(dy, 2, name, "dy")
     k = _shape(dest_row, 2, name, "dest_row")[1]
-    _same_type(name, dy, rows, drows)
+    _same_type(dy, drows, name)
+    if rows is not None:
+        _same_type(dy, rows, name)
     M, Hr = _shape(drows, 2, name, "drows")
     if Hr != H or (rows is not None and rows.shape != (M, H)):
         raise MiniteError(f"{name}: shapes of dy, rows and drows do not match")
@@ -675,18 +678,14 @@ def _grad_table(grads, outs, name):
     places = [t.get_device() for t in tensors]
     if places.count(d) != len(places):
         raise _elsewhere("tensor", next(i for i in places if i != d), d)
-    table = array("q", bytes(32 * len(grads)))
-    table[0::4] = array("q", at)
-    table[1::4] = array("q", out_at)
-    table[2::4] = array("q", sizes)
-    table[3::4] = array("q", [a | b << 32 for a, b in zip(kinds, out_kinds)])
-    return table, d, sum(sizes)
+    both = [a | b << 32 for a, b in zip(kinds, out_kinds)]
+    return array("q", chain.from_iterable(zip(at, out_at, sizes, both))), d, sum(sizes)
 
 
-def minite_grad_norm(grads, order, max_norm, norm, factor, workspace, stream=None, table=None):
+def minite_grad_norm(grads, order, max_norm, norm, factor, workspace, stream=None):
     """grads: contiguous bf16 or fp32 tensors; norm and factor fp32 [1], one of them may be None."""
     name = "minite_grad_norm"
-    table, d, _ = _grad_table(grads, grads, name) if table is None else table
+    table, d, _ = _grad_table(grads, grads, name)
     rc = load().minite_grad_norm(table.buffer_info()[0], len(grads), order, max_norm,
                                  _f32(norm, (1,), name, "norm", d), _f32(factor, (1,), name, "factor", d),
                                  _ptr(workspace, d), _bytes(workspace), _raw(stream, d))
@@ -965,10 +964,16 @@ def combine_rows_backward(dy, rows, dest_row, weights, out=None, status=None, st
 def _norm_of(grads, max_norm, order, stream, table, name):
     if order not in (2, math.inf):
         raise MiniteError(f"{name}: order is 2 or inf, not {order}")
+    table, d, elements = table
     like = grads[0]
     norm, scale = _empty((1,), torch.float32, like, stream), _empty((1,), torch.float32, like, stream)
-    minite_grad_norm(grads, NORM_2 if order == 2 else NORM_MAX, max_norm, norm, scale,
-                     _workspace(OP_GRAD_NORM, like, stream, len(grads), table[2]), stream, table)
+    lib = load()
+    n = lib.minite_workspace_bytes(OP_GRAD_NORM, len(grads), elements, 0, 0)
+    ws = _empty((n,), torch.uint8, like, stream) if n else None
+    rc = lib.minite_grad_norm(table.buffer_info()[0], len(grads), NORM_2 if order == 2 else NORM_MAX, max_norm,
+                              norm.data_ptr(), scale.data_ptr(), ws.data_ptr() if n else None, n, _raw(stream, d))
+    if rc:
+        _check(rc, "minite_grad_norm")
     return {"norm": norm, "scale": scale}
 
 
