@@ -255,6 +255,7 @@ template <int CAP, bool MAX, Kind KIND>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_kernel(const __grid_constant__ Batch<CAP> b,
                                                                       double* partial) {
   pdl_wait();
+  pdl_trigger();
   const double part = part_of<CAP, MAX, KIND>(b, blockIdx.x, gridDim.x);
   if (threadIdx.x == 0) partial[blockIdx.x] = part;
 }
@@ -288,6 +289,7 @@ template <bool MAX>
 __global__ void __launch_bounds__(kThreads) finish_kernel(const double* partial, int n, double max_norm, float* norm,
                                                           float* factor) {
   pdl_wait();
+  pdl_trigger();
   double v = 0.0;
   for (int i = threadIdx.x; i < n; i += kThreads) v = join<MAX>(v, partial[i]);
   const double total = block_join<MAX>(v);

@@ -240,7 +240,12 @@ __global__ void __launch_bounds__(kRangeThreads, 1) range_kernel(
   Word<B> va[U], vb[U];
   fetch(wid, va);
   const int c0 = t0 / (TABLE ? ct : 1);   // the first token's chunk
+  int my_e = -1, my_rank = 0;   // TABLE: slot tid of the range (a chunk has 512 at most)
   if constexpr (TABLE) {
+    if (tid < own) {
+      my_e = ids[p0 + tid];
+      my_rank = rank[p0 + tid];
+    }
     constexpr int kAhead = 8;
     for (int e0 = wid; e0 < E; e0 += kAhead * kRangeWarps) {
       int all[kAhead] = {}, before[kAhead] = {}, first[kAhead] = {};
@@ -306,13 +311,13 @@ __global__ void __launch_bounds__(kRangeThreads, 1) range_kernel(
   if (blockIdx.x == 0 && tid == 0) offsets[E] = used;
   // rows of this CTA's slots
   if constexpr (TABLE) {
-    for (int p = tid; p < own; p += kRangeThreads) {
-      const int e = ids[p0 + p];
+    if (tid < own) {
+      const int t = t0 + tid / k;
       int dest = -1;
-      if (e >= 0 && e < E) dest = s_before[e] + ((t0 + p / k) / ct > c0 ? s_first[e] : 0) + rank[p0 + p];
-      s_dest[p] = dest;
-      dest_row[p0 + p] = dest;
-      if (dest >= 0) perm_src[dest] = t0 + p / k;
+      if (my_e >= 0 && my_e < E) dest = s_before[my_e] + (t / ct > c0 ? s_first[my_e] : 0) + my_rank;
+      s_dest[tid] = dest;
+      dest_row[p0 + tid] = dest;
+      if (dest >= 0) perm_src[dest] = t;
     }
   } else if (wid == 0) {   // 32 at a time, in their order
     for (int b = 0; b < own; b += 32) {
