@@ -819,9 +819,10 @@ int minite_moe_combine_rows_backward(const void* dy, int dtype, int64_t dy_strid
  *   factor = min(1, max_norm / (norm + 1e-6))
  * Squares are added in FP32 up to 64 at a time, all else in 64 bits, in an order that
  * depends on the tensors' sizes, their addresses modulo 32 and the device alone. Nothing overflows or
- * vanishes on the way: norm is infinite only where it does not fit FP32. A NaN
- * among the gradients makes both NaN, an infinity norm infinite and factor 0. No
- * elements: norm 0.
+ * vanishes on the way: norm is infinite only where it does not fit FP32 (factor is
+ * taken from the norm in 64 bits). A NaN among the gradients makes both NaN, an
+ * infinity norm infinite and factor 0. With max_norm infinite factor is 1 (NaN for a
+ * norm of NaN). No elements: norm 0.
  *
  * tensors: HOST array, read during the call (out and out_dtype are ignored).
  * norm, factor: device, float [1], one of them may be NULL.
@@ -846,7 +847,7 @@ int minite_grad_norm(const minite_grad_tensor* tensors, int64_t n_tensors, int o
  * minite_clip_grads -- out = grad * factor[0] for many tensors, in FP32, rounded
  * once to out_dtype. out may be grad itself (of the same type); where that holds
  * for every tensor, a factor of exactly 1 leaves them untouched. Otherwise no
- * overlap. factor: device, float [1], as minite_grad_norm wrote it, say.
+ * overlap, and no tensor twice. factor: device, float [1], as minite_grad_norm wrote it, say.
  */
 int minite_clip_grads(const minite_grad_tensor* tensors, int64_t n_tensors, const float* factor,
                       minite_stream_t stream);

@@ -246,7 +246,8 @@ __device__ __forceinline__ double part_of(const Batch<CAP>& b, int64_t first, in
 template <bool MAX>
 __device__ __forceinline__ void write_norm(double total, double max_norm, float* norm, float* factor) {
   const double r = MAX ? total : sqrt(total);
-  const double f = max_norm / (r + 1e-6);
+  // without a limit 1, whatever the norm: infinity over infinity is none of its business
+  const double f = isinf(max_norm) && r == r ? 1.0 : max_norm / (r + 1e-6);
   if (norm) *norm = static_cast<float>(r);
   if (factor) *factor = f > 1.0 ? 1.0f : static_cast<float>(f);   // NaN stays
 }

@@ -177,7 +177,9 @@ __device__ __forceinline__ void segment(const T* row, int64_t V, int seg, int se
     return;
   }
   float r;
-  if (__any_sync(0xffffffffu, mine == m)) {
+  // |m| k beyond 2^100 (rows of the type's lowest value, say): the difference first, too
+  const float mk = -(m * k);
+  if (__any_sync(0xffffffffu, mine == m) || !(fabsf(mk) < 0x1p100f)) {
     float n = 0.0f;
     r = 0.0f;
     auto add = [&](float x) {
@@ -199,12 +201,12 @@ __device__ __forceinline__ void segment(const T* row, int64_t V, int seg, int se
       r += __shfl_xor_sync(0xffffffffu, r, o);
       n += __shfl_xor_sync(0xffffffffu, n, o);
     }
-    bool first = true;
+    bool first = s_max[wid] == m;
     for (int w = 0; w < wid; ++w) first &= s_max[w] != m;
     r += first ? n - 1.0f : n;
   } else {
     // x k - m k in one operation: what the product m k lost is a factor of every term
-    const float mk = -(m * k), lost = fmaf(m, k, mk);
+    const float lost = fmaf(m, k, mk);
     uint64_t acc = pair(ex2(fmaf(xh, k, mk)), ex2(fmaf(xt, k, mk)));
     const uint64_t minus = pair(mk, mk), k2 = pair(k, k);
 #pragma unroll

@@ -682,6 +682,13 @@ def _grad_table(grads, outs, name):
     return array("q", chain.from_iterable(zip(at, out_at, sizes, both))), d, sum(sizes)
 
 
+def _need_distinct(table, name):
+    """A tensor that is written twice would be scaled twice, or once and a half."""
+    at = [a for a, n in zip(table[1::4], table[2::4]) if n]
+    if len(set(at)) != len(at):
+        raise MiniteError(f"{name}: a destination appears twice")
+
+
 def minite_grad_norm(grads, order, max_norm, norm, factor, workspace, stream=None):
     """grads: contiguous bf16 or fp32 tensors; norm and factor fp32 [1], one of them may be None."""
     name = "minite_grad_norm"
@@ -696,7 +703,10 @@ def minite_grad_norm(grads, order, max_norm, norm, factor, workspace, stream=Non
 def minite_clip_grads(grads, outs, factor, stream=None, table=None):
     """outs[i] = grads[i] * factor; outs[i] may be grads[i]; factor fp32 [1]."""
     name = "minite_clip_grads"
-    table, d, _ = _grad_table(grads, outs, name) if table is None else table
+    if table is None:
+        table = _grad_table(grads, outs, name)
+        _need_distinct(table[0], name)
+    table, d, _ = table
     rc = load().minite_clip_grads(table.buffer_info()[0], len(grads), _f32(factor, (1,), name, "factor", d),
                                   _raw(stream, d))
     if rc:
@@ -989,6 +999,7 @@ def clip_grads(grads, max_norm, order=2.0, out=None, stream=None):
     (of either type). Returns grad_norm's dict."""
     out = grads if out is None else out
     table = _grad_table(grads, out, "clip_grads")
+    _need_distinct(table[0], "clip_grads")
     r = _norm_of(grads, max_norm, order, stream, table, "clip_grads")
     minite_clip_grads(grads, out, r["scale"], stream, table)
     return r

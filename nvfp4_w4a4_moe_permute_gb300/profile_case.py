@@ -14,6 +14,9 @@ command line, without the memory of a whole layer step.
         --rows 32768 --cols 1536 --inner 2048 --experts 128
     python -m nvfp4_w4a4_moe_permute_gb300.profile_case logprobs --rows 1024 --cols 131072 [--backward]
     python -m nvfp4_w4a4_moe_permute_gb300.profile_case adamw --rows 100000000 --bits 8
+    python -m nvfp4_w4a4_moe_permute_gb300.profile_case moe_rows --step combine --tokens 16384 --cols 2048
+    python -m nvfp4_w4a4_moe_permute_gb300.profile_case grad_norm --rows 200000000 --bits 32 [--clip]
+    python -m nvfp4_w4a4_moe_permute_gb300.profile_case verify --rows 128 --drafts 4 --cols 131072
 
 Expert sizes follow a Zipf(1.5) draw over the experts (a skewed routing);
 every call's device status is checked at the end.
@@ -205,7 +208,56 @@ def adamw(args, M, dev, status):
         opt.step(grads)
 
 
-CASES = {"grouped_bf16": grouped_bf16, "logprobs": logprobs, "adamw": adamw,
+def moe_rows(args, M, dev, status):
+    """`--tokens` BF16 rows of `--cols` columns into the order of `--experts` (top-8)
+    and back: one step of it."""
+    gen = torch.Generator(device=dev).manual_seed(args.seed)
+    T, k = args.tokens, 8
+    x = torch.randn((T, args.cols), device=dev, generator=gen).to(torch.bfloat16)
+    ids = torch.rand((T, args.experts), device=dev, generator=gen).topk(k, dim=1).indices.to(torch.int32)
+    w = torch.rand((T, k), device=dev, generator=gen)
+    r = M.permute_rows(x, ids, args.experts, status=status)
+    y, drows = torch.empty_like(x), torch.empty_like(r["rows"])
+    for _ in range(args.reps):
+        if args.step == "permute":
+            M.permute_rows(x, ids, args.experts, into=r, status=status)
+        elif args.step == "spread":
+            M.spread_rows(x, r["dest_row"], drows, status=status)
+        elif args.step == "combine":
+            M.combine_rows(r["rows"], r["dest_row"], w, out=y, status=status)
+        else:
+            M.combine_rows_backward(x, r["rows"], r["dest_row"], w, out=drows, status=status)
+
+
+def grad_norm(args, M, dev, status):
+    """The norm of `--rows` BF16 (`--bits` 8) or FP32 gradients in 24 tensors, with
+    `--clip` also those gradients clipped into BF16 ones."""
+    gen = torch.Generator(device=dev).manual_seed(args.seed)
+    dtype = torch.float32 if args.bits == 32 else torch.bfloat16
+    g = [torch.randn(args.rows // 24, device=dev, generator=gen).to(dtype) for _ in range(24)]
+    out = [torch.empty_like(t, dtype=torch.bfloat16) for t in g] if args.clip else None
+    for _ in range(args.reps):
+        if args.clip:
+            M.clip_grads(g, 1.0, out=out)
+        else:
+            M.grad_norm(g, 1.0)
+
+
+def verify(args, M, dev, status):
+    """`--drafts` drafted tokens of `--rows` sequences, BF16 logits of `--cols` tokens."""
+    gen = torch.Generator(device=dev).manual_seed(args.seed)
+    B, S, V = args.rows, args.drafts, args.cols
+    target = (torch.randn((B, S + 1, V), device=dev, generator=gen) * 2).to(torch.bfloat16)
+    draft = (target[:, :S].float() + torch.randn((B, S, V), device=dev, generator=gen) * 0.5).to(torch.bfloat16)
+    tokens = draft.argmax(2).to(torch.int32)
+    u = torch.rand((B, S), device=dev, generator=gen)
+    e = torch.empty((B, V), device=dev).exponential_(generator=gen)
+    for _ in range(args.reps):
+        M.verify_drafts(target, tokens, u, e, draft_logits=draft, status=status)
+
+
+CASES = {"moe_rows": moe_rows, "grad_norm": grad_norm, "verify": verify,
+         "grouped_bf16": grouped_bf16, "logprobs": logprobs, "adamw": adamw,
          "quantize_tokens": quantize_tokens, "quantize_weights": quantize_weights,
          "permute_swiglu": permute_swiglu, "gemm": gemm}
 
@@ -227,7 +279,11 @@ def main(argv=None) -> int:
     ap.add_argument("--even", action="store_true", help="grouped_bf16: as many rows for every expert")
     ap.add_argument("--alternatives", type=int, default=0)
     ap.add_argument("--backward", action="store_true", help="logprobs: the gradient")
-    ap.add_argument("--bits", type=int, default=8, choices=[8, 32], help="adamw: the states'")
+    ap.add_argument("--bits", type=int, default=8, choices=[8, 32], help="adamw: the states'; grad_norm: the gradients' (8: BF16)")
+    ap.add_argument("--step", default="combine", choices=["permute", "spread", "combine", "combine_grad"],
+                    help="moe_rows: which")
+    ap.add_argument("--clip", action="store_true", help="grad_norm: the clipped gradients too")
+    ap.add_argument("--drafts", type=int, default=4, help="verify: a sequence")
     ap.add_argument("--beta2", type=float, default=0.95, help="adamw: above 0.95 8-bit codes are drawn")
     ap.add_argument("--reps", type=int, default=3)
     ap.add_argument("--seed", type=int, default=0)

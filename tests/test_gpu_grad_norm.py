@@ -89,6 +89,15 @@ def test_non_finite_gradients(n, order, dtype):
                 assert got == w or (math.isnan(got) and math.isnan(w))
 
 
+def test_without_a_limit_the_factor_is_one():
+    for n in (10, 3_000_000):
+        x = torch.ones(n, device=DEV)
+        for bad, factor in ((1.0, 1.0), (math.inf, 1.0), (math.nan, math.nan)):
+            x[n // 3] = bad
+            got = float(M.grad_norm([x])["scale"])
+            assert got == factor or (math.isnan(got) and math.isnan(factor))
+
+
 def test_no_elements():
     r = M.grad_norm([torch.empty(0, device=DEV)], max_norm=2.0)
     assert float(r["norm"]) == 0.0 and float(r["scale"]) == 1.0

@@ -96,6 +96,18 @@ def test_permute_reports_ids_out_of_range(T, k):
     assert int(status) == 0   # a negative id is a slot that is not used
 
 
+@pytest.mark.parametrize("T,k", [(777, 3), (5000, 5)])
+def test_ids_may_start_anywhere(T, k):
+    flat = torch.randint(-1, 9, (T * k + 3,), generator=torch.Generator().manual_seed(T)).to(I32)
+    x = torch.randn(T, 16, device=DEV)
+    dev = flat.to(DEV)
+    for shift in range(4):
+        ids = flat[shift: shift + T * k].view(T, k)
+        r = M.permute_rows(x, dev[shift: shift + T * k].view(T, k), 9)
+        _, dest, offsets = sorted_by_expert(ids, 9)
+        assert torch.equal(r["dest_row"].cpu().long(), dest) and r["offsets"].tolist() == offsets.tolist()
+
+
 def test_permute_of_nothing():
     r = M.permute_rows(torch.empty(0, 8, device=DEV), torch.empty(0, 2, dtype=I32, device=DEV), 3)
     assert r["offsets"].tolist() == [0, 0, 0, 0] and r["rows"].shape == (0, 8)

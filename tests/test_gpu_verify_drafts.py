@@ -136,6 +136,28 @@ def test_masked_tokens():
         assert (r["accepted"] == 1).all() and (r["tokens"][:, :2] == 7).all() and (r["logprobs"] == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("t", [0.01, 1.0, 1e4])
+def test_logits_near_the_ends_of_their_type(dtype, t):
+    """Rows of the type's lowest value alone (all alike then), beside -inf, and of its
+    largest; with temperatures that take m / T out of FP32's range."""
+    V, low, high = 9000, torch.finfo(dtype).min, torch.finfo(dtype).max
+    target = torch.full((5, 1, V), -INF, dtype=dtype, device=DEV)
+    target[0] = low
+    target[1, 0, 5000:] = low
+    target[2, 0, 7] = low
+    target[3] = high
+    target[4, 0, ::3], target[4, 0, 1::3] = high, low
+    ones = [V, 4000, 1, V, 3000]
+    e = torch.empty(5, V).exponential_(generator=torch.Generator().manual_seed(1)).to(DEV)
+    r = M.verify_drafts(target, torch.zeros(5, 0, dtype=I32, device=DEV), torch.zeros(5, 0, device=DEV), e, temperature=t)
+    top = target[:, 0].float() == target[:, 0].float().amax(1, keepdim=True)
+    want = torch.where(top, 1 / e, 0.0).argmax(1)
+    assert r["tokens"][:, 0].tolist() == want.tolist()
+    lp = torch.tensor([-math.log(n) for n in ones])
+    assert ((r["logprobs"][:, 0].cpu() - lp).abs() <= 2.0 ** -17 * (1 + lp.abs())).all()
+
+
 def test_rows_without_probabilities():
     target, draft, tokens, u, e = inputs(3, 6, 2, 40, F32, True, ragged=False)
     u.zero_()                                 # every draft stands that can

@@ -168,6 +168,7 @@ def test_python_calls_refuse_wrong_tensors(calls, monkeypatch):   # noqa: F811
             lambda: M.grad_norm([On(torch.zeros(3, dtype=torch.float16))]),
             lambda: M.grad_norm([On(torch.zeros(4, 4).t()[:2])]),
             lambda: M.clip_grads([On(torch.zeros(3))], 1.0, out=[]),
+            lambda: M.clip_grads([On(torch.zeros(3)), On(torch.zeros(3))], 1.0),    # the same tensor twice
             lambda: M.clip_grads([On(torch.zeros(3))], 1.0, out=[On(torch.zeros(4))]),
             lambda: M.clip_grads([On(torch.zeros(3))], 1.0, out=[On(torch.zeros(3).half())]),
             lambda: M.verify_drafts(logits, drafts, u, e),
