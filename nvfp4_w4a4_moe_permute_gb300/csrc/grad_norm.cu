@@ -10,7 +10,11 @@
 // scaled by a power of two that brings their largest to a harmless size: the norm
 // is right for every finite gradient, FP32 denormals and 3e38 among them.
 //
-// Bound by HBM.
+// Bound by HBM: 604M FP32 gradients 330 us (7.3 TB/s), 250M BF16 ones 79 us (6.3
+// TB/s; a third of its issue slots are busy, and a second chunk in flight is all that
+// the registers hold), 400M FP32 ones clipped into BF16 600 us (4.0 GB, the gradients
+// read twice: the factor is known only when all have been seen). Asynchronous copies
+// through shared memory, four or six chunks ahead, took 343 and 355, 95 and 106 us.
 #include <cmath>
 
 #include "common.cuh"
@@ -262,8 +266,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) norm_kernel(const __gr
 }
 
 // Few elements: one cluster of CTAs, whose parts meet in the first one's shared
-// memory, in place of a second launch and a workspace. 300001 BF16 elements 3.4 us,
-// 5.0 by the two launches.
+// memory, in place of a second launch and a workspace. 300001 BF16 elements take 5.2
+// us on the device, 5.0 by the two launches, but a call 18 to 20 us instead of 28: the
+// host's time is what bounds it.
 constexpr int kCluster = 8;
 template <int CAP, bool MAX>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) small_norm_kernel(
