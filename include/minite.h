@@ -753,8 +753,8 @@ int minite_adamw_step(const minite_adamw_tensor* tensors, int64_t n_tensors, int
  *           bytes, 256-byte aligned, contents on entry ignored; NULL where that is 0.
  * Shape rules: 1 <= H <= 2^24, 1 <= E <= 1024, 1 <= k <= 32, T*k < 2^31, T = 0
  * allowed (offsets become 0), strides at least H and below 2^31. Matrices are
- * aligned to their element; accesses are 32 bytes wide where base addresses, row
- * sizes and strides are multiples of that, 16, 4 or 2 bytes otherwise.
+ * aligned to their element; accesses are wide (32 or 16 bytes) where base addresses,
+ * row sizes and strides are multiples of that, 4 or 2 bytes otherwise.
  */
 int minite_moe_permute_rows(const void* x, int dtype, int64_t x_stride, const int32_t* topk_ids,
                             int64_t T, int64_t H, int32_t E, int32_t k, void* rows,
@@ -794,9 +794,9 @@ int minite_moe_combine_rows(const void* rows, int dtype, int64_t rows_stride,
  * minite_moe_combine_rows_backward -- the gradient of minite_moe_combine_rows:
  *   drows[dest_row[t, j]] = weights[t, j] * dy[t]          (rounded once)
  *   dweights[t, j] = sum_h dy[t, h] * rows[dest_row[t, j], h]   (0 if skipped)
- * The sums are FP32, over pieces of 32 accesses of a row (their width follows from
- * the alignment, see minite_moe_permute_rows) and then over the pieces in order: a
- * result depends on its own two rows and on their alignment alone.
+ * The sums are FP32, in an order that follows from H and from whether base addresses,
+ * strides and row sizes are multiples of 16 bytes: a result depends on its own two rows
+ * and on that alone.
  *
  * rows, dweights: both NULL where the router is not trained. drows may be rows
  * itself (with the same stride), otherwise no overlap; rows that no slot names are

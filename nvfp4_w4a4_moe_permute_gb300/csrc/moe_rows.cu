@@ -214,10 +214,8 @@ __device__ __forceinline__ int scan_before(int v, int* s_warp, int* total) {
 
 template <int B, int U, bool TABLE>
 __global__ void __launch_bounds__(kRangeThreads, 1) range_kernel(
-    Matrix x, int64_t T, int64_t words, int k, int E, const int32_t* ids,
-    const int32_t* table, const int32_t* rank, int ct, int nchunks,
-    int32_t* offsets, int32_t* perm_src, int32_t* dest_row, Matrix out,
-    int32_t* status) {
+    Matrix x, int64_t T, int64_t words, int k, int E, const int32_t* ids, const int32_t* table, const int32_t* rank,
+    int ct, int nchunks, int32_t* offsets, int32_t* perm_src, int32_t* dest_row, Matrix out, int32_t* status) {
   extern __shared__ int32_t sm[];
   __shared__ int s_warp[kRangeWarps];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -411,8 +409,8 @@ struct CombineShared {
 };
 template <typename T>
 __global__ void __launch_bounds__(32 * kCombineWarps, 1) combine_kernel(
-    Matrix rows, const int32_t* dest_row, const float* weights, int64_t T_, int64_t M,
-    int64_t row_bytes, int k, Matrix y, int32_t* status) {
+    Matrix rows, const int32_t* dest_row, const float* weights, int64_t T_, int64_t M, int64_t row_bytes, int k, Matrix y,
+    int32_t* status) {
   using V = Values<T, 16>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -501,10 +499,9 @@ __global__ void __launch_bounds__(32 * kCombineWarps, 1) combine_kernel(
 
 // The same for rows of any alignment, U elements of 32 lanes a unit.
 template <typename T, int B, int U>
-__global__ void __launch_bounds__(kThreads, 2) combine_any_kernel(Matrix rows, const int32_t* dest_row,
-                                                              const float* weights, int64_t T_,
-                                                              int64_t M, int64_t words, int k, Matrix y,
-                                                              int32_t* status) {
+__global__ void __launch_bounds__(kThreads, 2) combine_any_kernel(
+    Matrix rows, const int32_t* dest_row, const float* weights, int64_t T_, int64_t M, int64_t words, int k, Matrix y,
+    int32_t* status) {
   using V = Values<T, B>;
   pdl_wait();
   const int lane = threadIdx.x & 31;
