@@ -656,7 +656,7 @@ def minite_moe_combine_rows_backward(dy, rows, dest_row, weights, drows, dweight
 
 def _grad_table(grads, outs, name):
     """struct minite_grad_tensor of every gradient and its destination (outs may be
-    grads), the device, and the number of elements."""
+    grads, None: they are only read), the device, and the number of elements."""
     if len(grads) == 0:
         raise MiniteError(f"{name}: needs gradients")
     d = _device(grads[0])
@@ -665,7 +665,7 @@ def _grad_table(grads, outs, name):
     kinds = [_DTYPES.get(g.dtype) for g in grads]
     tensors = grads
     out_at, out_kinds = at, kinds
-    if outs is not grads:
+    if outs is not None and outs is not grads:
         if [o.numel() for o in outs] != sizes:
             raise MiniteError(f"{name}: one destination a gradient, of its size")
         out_at = [o.data_ptr() for o in outs]
@@ -678,21 +678,19 @@ def _grad_table(grads, outs, name):
     places = [t.get_device() for t in tensors]
     if places.count(d) != len(places):
         raise _elsewhere("tensor", next(i for i in places if i != d), d)
+    if outs is not None and len(set(out_at)) != len(out_at):
+        # a tensor that is written twice would be scaled twice, or once and a half
+        used = [a for a, n in zip(out_at, sizes) if n]
+        if len(set(used)) != len(used):
+            raise MiniteError(f"{name}: a destination appears twice")
     both = [a | b << 32 for a, b in zip(kinds, out_kinds)]
     return array("q", chain.from_iterable(zip(at, out_at, sizes, both))), d, sum(sizes)
-
-
-def _need_distinct(table, name):
-    """A tensor that is written twice would be scaled twice, or once and a half."""
-    at = [a for a, n in zip(table[1::4], table[2::4]) if n]
-    if len(set(at)) != len(at):
-        raise MiniteError(f"{name}: a destination appears twice")
 
 
 def minite_grad_norm(grads, order, max_norm, norm, factor, workspace, stream=None):
     """grads: contiguous bf16 or fp32 tensors; norm and factor fp32 [1], one of them may be None."""
     name = "minite_grad_norm"
-    table, d, _ = _grad_table(grads, grads, name)
+    table, d, _ = _grad_table(grads, None, name)
     rc = load().minite_grad_norm(table.buffer_info()[0], len(grads), order, max_norm,
                                  _f32(norm, (1,), name, "norm", d), _f32(factor, (1,), name, "factor", d),
                                  _ptr(workspace, d), _bytes(workspace), _raw(stream, d))
@@ -703,10 +701,7 @@ def minite_grad_norm(grads, order, max_norm, norm, factor, workspace, stream=Non
 def minite_clip_grads(grads, outs, factor, stream=None, table=None):
     """outs[i] = grads[i] * factor; outs[i] may be grads[i]; factor fp32 [1]."""
     name = "minite_clip_grads"
-    if table is None:
-        table = _grad_table(grads, outs, name)
-        _need_distinct(table[0], name)
-    table, d, _ = table
+    table, d, _ = _grad_table(grads, outs, name) if table is None else table
     rc = load().minite_clip_grads(table.buffer_info()[0], len(grads), _f32(factor, (1,), name, "factor", d),
                                   _raw(stream, d))
     if rc:
@@ -991,7 +986,7 @@ def grad_norm(grads, max_norm=math.inf, order=2.0, stream=None):
     """The global norm of a list of gradients (bf16 and fp32 may be mixed), and the
     factor min(1, max_norm / (norm + 1e-6)) for ``AdamW.step(grad_scale=)``:
     dict(norm [1], scale [1]), on the device. order: 2 or math.inf (the largest |g|)."""
-    return _norm_of(grads, max_norm, order, stream, _grad_table(grads, grads, "grad_norm"), "grad_norm")
+    return _norm_of(grads, max_norm, order, stream, _grad_table(grads, None, "grad_norm"), "grad_norm")
 
 
 def clip_grads(grads, max_norm, order=2.0, out=None, stream=None):
@@ -999,7 +994,6 @@ def clip_grads(grads, max_norm, order=2.0, out=None, stream=None):
     (of either type). Returns grad_norm's dict."""
     out = grads if out is None else out
     table = _grad_table(grads, out, "clip_grads")
-    _need_distinct(table[0], "clip_grads")
     r = _norm_of(grads, max_norm, order, stream, table, "clip_grads")
     minite_clip_grads(grads, out, r["scale"], stream, table)
     return r

@@ -296,3 +296,27 @@ def test_large_offsets():
     assert torch.equal(rows[dest[:, 0].long()], (x.float() * 2).to(BF))
     want = (x.double() ** 2).sum(1)
     assert ((dw[:, 0].double() - want).abs() <= (H / 24 + 40) * 2.0 ** -24 * want).all()
+
+
+def test_permute_of_rows_beyond_two_to_the_31_elements():
+    H = 1 << 20
+    for T, k in ((2100, 1), (270, 8)):   # x, or the rows in expert order, pass it
+        x = torch.zeros(T, H, dtype=BF, device=DEV)
+        x[:, 0] = torch.arange(T, device=DEV) % 251
+        x[:, -1] = torch.arange(T, device=DEV) % 241
+        ids = route(5, T, k, 7)
+        r = M.permute_rows(x, ids.to(DEV), 7)
+        order, dest, _ = sorted_by_expert(ids, 7)
+        assert torch.equal(r["dest_row"].cpu().long(), dest)
+        src = (order // k).to(DEV)
+        assert torch.equal(r["rows"][:, 0], x[src, 0]) and torch.equal(r["rows"][:, -1], x[src, -1])
+        assert not r["rows"][:, 1:-1].any()
+        del x, r
+    # and by ranking, scan and copies
+    T, k, H = 40000, 8, 7168
+    x = torch.randn(T, H, device=DEV).to(BF)
+    ids = route(6, T, k, 12)
+    r = M.permute_rows(x, ids.to(DEV), 12)
+    src = (sorted_by_expert(ids, 12)[0] // k).to(DEV)
+    for a in range(0, T * k, 32000):
+        assert torch.equal(r["rows"][a: a + 32000], x[src[a: a + 32000]])

@@ -281,3 +281,17 @@ def test_no_sequences():
     r = M.verify_drafts(torch.empty(0, 3, 10, device=DEV), torch.empty(0, 2, dtype=I32, device=DEV),
                         torch.empty(0, 2, device=DEV), torch.empty(0, 10, device=DEV))
     assert r["tokens"].shape == (0, 3)
+
+
+def test_logits_beyond_two_to_the_31_elements():
+    B, V = 17000, 131072
+    g = torch.Generator(device=DEV).manual_seed(1)
+    target = torch.zeros(B, 1, V, dtype=BF, device=DEV)
+    noise = torch.ones(B, V, device=DEV)
+    none = torch.zeros(B, 0, dtype=I32, device=DEV), torch.zeros(B, 0, device=DEV)
+    want = torch.randint(0, V, (B,), generator=g, device=DEV)
+    target[torch.arange(B, device=DEV), 0, want] = 5.0
+    r = M.verify_drafts(target, *none, noise)
+    assert torch.equal(r["tokens"][:, 0].long(), want)
+    lp = 5.0 - math.log(math.exp(5.0) + V - 1)
+    assert ((r["logprobs"] - lp).abs() <= 2.0 ** -17 * 8).all()

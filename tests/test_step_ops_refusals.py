@@ -211,12 +211,26 @@ def test_operands_on_another_device(calls):   # noqa: F811
         accepted=torch.zeros(2, dtype=I32), logprobs=torch.zeros(2, 4), workspace=ws, status=torch.zeros(1, dtype=I32)))
 
 
+class At(On):
+    """A tensor at an address of its own."""
+
+    def __init__(self, t, at):
+        super().__init__(t)
+        self.at = at
+
+    def data_ptr(self):
+        return self.at
+
+
 def test_the_gradients_table(calls):   # noqa: F811
     """What a descriptor says: addresses, size, both types."""
-    g = [On(torch.zeros(3)), On(torch.zeros(2, 5, dtype=BF))]
-    o = [On(torch.zeros(3, dtype=BF)), On(torch.zeros(10))]
+    g = [At(torch.zeros(3), 4096), At(torch.zeros(2, 5, dtype=BF), 8192)]
+    o = [At(torch.zeros(3, dtype=BF), 12288), At(torch.zeros(10), 16384)]
     t, d, elements = M._grad_table(g, o, "x")
     assert d == 0 and elements == 13
     d = np.frombuffer(t, dtype=GRAD_TENSOR)
     assert d["n"].tolist() == [3, 10] and d["grad_dtype"].tolist() == [1, 0] and d["out_dtype"].tolist() == [0, 1]
-    assert (d["grad"] == 1 << 12).all() and (d["out"] == 1 << 12).all()
+    assert d["grad"].tolist() == [4096, 8192] and d["out"].tolist() == [12288, 16384]
+    empty = [At(torch.zeros(0), 0), At(torch.zeros(0), 0), g[0]]
+    assert M._grad_table(empty, empty, "x")[2] == 3          # no elements: no place of its own
+    assert M._grad_table([g[0], g[0]], None, "x")[2] == 6    # read twice: counted twice
