@@ -132,17 +132,6 @@ __device__ __forceinline__ float2 join(float2 a, float2 b, float k) {
   r += b.x == m ? b.y : cb * (b.y + 1.0f);
   return make_float2(m, r);
 }
-__device__ __forceinline__ float2 warp_join(float2 v, float k) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    float2 u;
-    u.x = __shfl_xor_sync(0xffffffffu, v.x, o);
-    u.y = __shfl_xor_sync(0xffffffffu, v.y, o);
-    v = join(v, u, k);
-  }
-  return v;
-}
-
 // One segment of one row: its largest logit, then the sum over the others. Only the
 // warps that hold the largest look at every element for it; the rest add two
 // elements an instruction.
@@ -278,12 +267,22 @@ struct Row {
   __device__ __forceinline__ float p(float x, float k, float shift) const { return ex2(fmaf(x - m, k, -shift)); }
   __device__ __forceinline__ float p(float x, float k) const { return p(x, k, log_s * kLog2e); }
 };
-// From its segments, by a warp.
-__device__ __forceinline__ Row row_of(const float2* part, int segs, float k) {
-  float2 v = make_float2(-INFINITY, 0.0f);
-  for (int s = threadIdx.x & 31; s < segs; s += 32) v = join(v, part[s], k);
-  v = warp_join(v, k);
-  return {v.x, log1pf(v.y)};
+// A row's first 32 segments, one a lane of a warp, and the row that all of them make.
+__device__ __forceinline__ float2 first_part(const float2* part, int segs) {
+  const int lane = threadIdx.x & 31;
+  return lane < segs ? part[lane] : make_float2(-INFINITY, 0.0f);
+}
+__device__ __forceinline__ Row row_of(float2 v, const float2* part, int segs, float k) {
+  for (int s = 32 + (threadIdx.x & 31); s < segs; s += 32) v = join(v, part[s], k);
+  float m = v.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const bool top = v.x == m;
+  float r = top ? v.y : ex2((v.x - m) * k) * (v.y + 1.0f);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+  r += static_cast<float>(__popc(__ballot_sync(0xffffffffu, top)) - 1);   // one maximum is left out
+  return {m, log1pf(r)};   // m is not finite: not usable, whatever r is
 }
 
 // The race: the largest weight / variate, the lower index where they are equal. No
@@ -383,16 +382,22 @@ __global__ void __launch_bounds__(kThreads, kRaceCtas) race_kernel(const Params 
   const int32_t* drafts = p.draft_tokens + b * p.S;
   for (int i = wid; i <= p.S; i += kWarps) {   // a warp a position
     const int before = i > 0 ? drafts[i - 1] : 0, x = i < p.S ? drafts[i] : -1;
+    // asked for together; where the row is not reached they were not written, and are not used
+    const float2* target_part = p.target_part + (b * (p.S + 1) + i) * p.target_segs;
+    const float2* draft_part = p.draft_part + (b * p.S + i) * p.draft_segs;
+    const bool with_draft = draft && i < p.S;
+    const float2 vt = first_part(target_part, p.target_segs);
+    const float2 vd = first_part(draft_part, with_draft ? p.draft_segs : 0);
     const bool reached = before >= 0 && before < p.V, given = x >= 0 && x < p.V;
-    Row rt = {0.0f, 0.0f}, rd = {0.0f, 0.0f};
     float xt = 0.0f, xd = 0.0f, u = 0.0f;
-    if (given) {   // asked for before the segments are waited for
+    if (given) {
       xt = value(target[i * p.target_ld + x]);
       if (draft) xd = value(draft[i * p.draft_ld + x]);
       u = p.uniforms[b * p.S + i];
     }
-    if (reached) rt = row_of(p.target_part + (b * (p.S + 1) + i) * p.target_segs, p.target_segs, p.k2);
-    if (given && draft) rd = row_of(p.draft_part + (b * p.S + i) * p.draft_segs, p.draft_segs, p.k2);
+    const Row rt = row_of(vt, target_part, p.target_segs, p.k2);
+    Row rd = {0.0f, 0.0f};
+    if (with_draft) rd = row_of(vd, draft_part, p.draft_segs, p.k2);
     if (lane == 0) {
       bool stands = false;
       if (reached && given && rt.usable() && rd.usable()) {
