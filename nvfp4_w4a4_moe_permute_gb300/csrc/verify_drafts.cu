@@ -404,7 +404,6 @@ __global__ void __launch_bounds__(kThreads, kRaceCtas) race_kernel(const Params 
         const float qx = draft ? rd.p(xd, p.k2) : 1.0f;
         stands = u * qx < rt.p(xt, p.k2);
       }
-      if (rank == 0 && x >= p.V) set_status(p.status, MINITE_ERR_BAD_TOKEN);
       s_target[i] = rt;
       s_draft[i] = rd;
       s_given[i] = given;
@@ -447,7 +446,12 @@ __global__ void __launch_bounds__(kThreads, kRaceCtas) race_kernel(const Params 
   }
   if (wid != 0) return;
   const int32_t next = best ? static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(best)) : -1;
-  if (lane == 0) p.accepted[b] = n;
+  if (lane == 0) {
+    p.accepted[b] = n;
+    int given = 0;   // what ends the drafts may be a token out of range
+    while (given < p.S && s_given[given]) ++given;
+    if (given < p.S && drafts[given] >= 0) set_status(p.status, MINITE_ERR_BAD_TOKEN);
+  }
   if (lane <= p.S) {
     const int32_t x = lane < n ? drafts[lane] : lane == n ? next : -1;
     p.tokens[b * (p.S + 1) + lane] = x;

@@ -188,6 +188,12 @@ def test_draft_tokens_out_of_range():
     status = torch.zeros(1, dtype=I32, device=DEV)
     M.verify_drafts(target[2:], tokens[2:], u[2:], e[2:], draft_logits=draft[2:], status=status)
     assert int(status) == 0
+    tokens[2, 2], tokens[3, 2] = -1, 40       # nor is one out of range there
+    M.verify_drafts(target[2:], tokens[2:], u[2:], e[2:], draft_logits=draft[2:], status=status)
+    assert int(status) == 0
+    tokens[3, 1] = 41                         # the one that ends the drafts is
+    M.verify_drafts(target[2:], tokens[2:], u[2:], e[2:], draft_logits=draft[2:], status=status)
+    assert int(status) == 1 << M.ERR_BAD_TOKEN
 
 
 def test_the_same_model_accepts_everything():
