@@ -18,11 +18,11 @@
 // every draft (each CTA for itself) and runs the race over its part of the one row
 // that is sampled from; the CTAs' winners meet in one 64-bit maximum.
 //
-// 64 sequences with up to four drafts of 100003 BF16 tokens take 33 us, 19 of them the
-// statistics (92 MB, 4.8 TB/s, 64% of the issue slots in longer runs), 14 the race (45
-// MB; some 6 of it are its start, the chain of loads by which a CTA learns which row
+// 64 sequences with up to four drafts of 100003 BF16 tokens take 32 us, 19 of them the
+// statistics (92 MB, 4.8 TB/s, 64% of the issue slots in longer runs), 13 the race (45
+// MB; some 5 of it are its start, the chain of loads by which a CTA learns which row
 // is sampled from, and the meeting of the winners). 128 sequences with four drafts of
-// 131072: 82 us (437 MB). One sequence: 8 us of latency, and 24 of the host's.
+// 131072: 82 us (437 MB). One sequence: 7.5 us of latency, and 24 of the host's.
 //
 // Sums are kept without the maximum's own term, r = s - 1, and log s = log1p(r):
 // the log probability of an almost certain token is not lost beside the 1.
@@ -472,7 +472,7 @@ cudaError_t launch(Params& p, int64_t B, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   // CTAs of a sequence: one round of its threads' loads each where sequences are
   // few, otherwise as many as are resident at once (the look at the drafts costs every
-  // CTA some 3 us)
+  // CTA some 2 us)
   int64_t ctas = (p.V + kRound - 1) / kRound;
   const int64_t resident = kRaceCtas * static_cast<int64_t>(num_sms());
   const int64_t fill = resident / B > 1 ? resident / B : 1;
