@@ -742,23 +742,22 @@ __global__ void __launch_bounds__(kThreads, 2) combine_backward_any_kernel(
       float sum = 0.0f;
       for (int part = 0; part < parts; ++part) {
         const int64_t w0 = static_cast<int64_t>(part) * (32 * U) + lane;
-        float d[U][V::kN];
-        Word<B> v[kSlots][U];
+        // every word is used under the condition under which it is loaded: one that
+        // was set to 0 first made each load wait for the one before it (95 us for
+        // 12000 tokens of 201 columns)
+        Word<B> d[U], v[kSlots][U];
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-          Word<B> u = {};
-          if (w0 + 32 * i < words) u.load(dy.p + t * dy.ld + (w0 + 32 * i) * B);
-          V::get(u, d[i]);
-        }
+        for (int i = 0; i < U; ++i)
+          if (w0 + 32 * i < words) d[i].load(dy.p + t * dy.ld + (w0 + 32 * i) * B);
         if constexpr (DOT) {
 #pragma unroll
           for (int jj = 0; jj < kSlots; ++jj) {
             const int to = __shfl_sync(0xffffffffu, mine, (j0 + jj) & 31);
             const char* row = rows.p + to * rows.ld;
+            if (j0 + jj < k && to >= 0) {
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-              v[jj][i] = {};
-              if (j0 + jj < k && to >= 0 && w0 + 32 * i < words) v[jj][i].load(row + (w0 + 32 * i) * B);
+              for (int i = 0; i < U; ++i)
+                if (w0 + 32 * i < words) v[jj][i].load(row + (w0 + 32 * i) * B);
             }
           }
         }
@@ -771,19 +770,21 @@ __global__ void __launch_bounds__(kThreads, 2) combine_backward_any_kernel(
           if (j0 + jj < k && to >= 0) {
             char* row = drows.p + to * drows.ld;
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-              float f[V::kN];
-              if constexpr (DOT) {
-                V::get(v[jj][i], f);
+            for (int i = 0; i < U; ++i)
+              if (w0 + 32 * i < words) {
+                float x[V::kN], f[V::kN];
+                V::get(d[i], x);
+                if constexpr (DOT) {
+                  V::get(v[jj][i], f);
 #pragma unroll
-                for (int c = 0; c < V::kN; ++c) dot[jj] = fmaf(d[i][c], f[c], dot[jj]);
+                  for (int c = 0; c < V::kN; ++c) dot[jj] = fmaf(x[c], f[c], dot[jj]);
+                }
+#pragma unroll
+                for (int c = 0; c < V::kN; ++c) f[c] = w * x[c];
+                Word<B> o;
+                V::put(o, f);
+                o.store(row + (w0 + 32 * i) * B);
               }
-#pragma unroll
-              for (int c = 0; c < V::kN; ++c) f[c] = w * d[i][c];
-              Word<B> o;
-              V::put(o, f);
-              if (w0 + 32 * i < words) o.store(row + (w0 + 32 * i) * B);
-            }
           }
         }
         if constexpr (DOT) sum += warp_sum8(dot);
