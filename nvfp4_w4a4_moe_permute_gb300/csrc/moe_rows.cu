@@ -365,19 +365,6 @@ __global__ void __launch_bounds__(kRangeThreads, 1) range_kernel(
   for (int i = used + blockIdx.x * kRangeThreads + tid; i < pairs; i += gridDim.x * kRangeThreads) perm_src[i] = -1;
 }
 
-// 16 bytes of global memory to a slot of shared memory that only this thread uses.
-__device__ __forceinline__ void ask16(void* slot, const char* p) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(slot)), "l"(p) : "memory");
-}
-__device__ __forceinline__ void close_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void wait_groups() {
-  asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
-}
-__device__ __forceinline__ Word<16> slot_word(const uint4& u) { return {{u.x, u.y, u.z, u.w}}; }
-
-constexpr int kDepth = 4;             // steps of a warp in flight
-constexpr int kPieceBytes = 32 * 16;  // of a row, a warp's
-
 // Eight values a lane to their sums over the warp: lane l returns the sum of
 // value l / 4.
 __device__ __forceinline__ float warp_sum8(float (&v)[8]) {
@@ -397,109 +384,14 @@ __device__ __forceinline__ float warp_sum8(float (&v)[8]) {
   return r;
 }
 
-// y[t] = sum over slots of weight * row, for rows of whole 16-byte words (32768
-// tokens: 189 us; with loads into registers, no step ahead, 215). A step is
-// a 512-byte piece of a token's row in up to 8 of its slots; a warp asks for four
-// steps ahead, by asynchronous copies to places that only the asking lane reads (no
-// barrier, few registers, 192 KB in flight on an SM), and for their routing eight
-// steps ahead (one step more than the copies' left every step waiting for it).
-constexpr int kCombineWarps = 12;
-struct CombineShared {
-  uint4 stage[kCombineWarps][kDepth][kSlots][32];
-};
-template <typename T>
-__global__ void __launch_bounds__(32 * kCombineWarps, 1) combine_kernel(
-    Matrix rows, const int32_t* dest_row, const float* weights, int64_t T_, int64_t M, int64_t row_bytes, int k, Matrix y,
-    int32_t* status) {
-  using V = Values<T, 16>;
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  uint4 (*stage)[kSlots][32] = reinterpret_cast<CombineShared*>(smem_raw)->stage[wid];
-  pdl_wait();
-  const int64_t warp = static_cast<int64_t>(blockIdx.x) * kCombineWarps + wid;
-  const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kCombineWarps;
-  const int64_t parts = (row_bytes + kPieceBytes - 1) / kPieceBytes;
-  const int64_t units = T_ * parts;
-  const int groups = (k + kSlots - 1) / kSlots;
-  const int64_t steps = warp < units ? ((units - warp - 1) / nwarps + 1) * groups : 0;
-  struct Route {
-    int dest;     // lane j: of slot 8 g + j
-    float w;
-    int64_t t;
-    int32_t col;  // in bytes; row_bytes or more: none for this lane
-  };
-  auto route = [&](int64_t i) {
-    Route r = {-1, 1.0f, 0, 0};
-    if (i < steps) {
-      const int64_t turn = div_nonneg(i, groups);
-      const int64_t u = warp + turn * nwarps;
-      r.t = div_nonneg(u, parts);
-      r.col = static_cast<int32_t>((u - r.t * parts) * kPieceBytes) + 16 * lane;
-      const int j = static_cast<int>(i - turn * groups) * kSlots + lane;
-      if (lane < kSlots && j < k) {
-        r.dest = dest_row[r.t * k + j];
-        if (weights) r.w = weights[r.t * k + j];
-      }
-    }
-    return r;
-  };
-  auto ask = [&](Route& r, int s) {
-    if (r.dest >= M) {
-      set_status(status, MINITE_ERR_BAD_ROUTING);
-      r.dest = -1;
-    }
-#pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
-      const int d = __shfl_sync(0xffffffffu, r.dest, j);
-      if (d >= 0 && r.col < row_bytes) ask16(&stage[s][j][lane], rows.p + d * rows.ld + r.col);
-    }
-    close_group();
-  };
-  Route r[kDepth], next[kDepth];
-#pragma unroll
-  for (int s = 0; s < kDepth; ++s) r[s] = route(s);
-#pragma unroll
-  for (int s = 0; s < kDepth; ++s) next[s] = route(kDepth + s);
-#pragma unroll
-  for (int s = 0; s < kDepth; ++s) ask(r[s], s);
-  float acc[V::kN];
-#pragma unroll
-  for (int c = 0; c < V::kN; ++c) acc[c] = 0.0f;
-  int g = 0;
-  for (int64_t i = 0; i < steps;) {
-#pragma unroll
-    for (int s = 0; s < kDepth; ++s, ++i) {
-      if (i >= steps) break;
-      wait_groups<kDepth - 1>();
-#pragma unroll
-      for (int j = 0; j < kSlots; ++j) {
-        const int d = __shfl_sync(0xffffffffu, r[s].dest, j);
-        const float w = __shfl_sync(0xffffffffu, r[s].w, j);
-        if (d >= 0) {
-          float f[V::kN];
-          V::get(slot_word(stage[s][j][lane]), f);
-#pragma unroll
-          for (int c = 0; c < V::kN; ++c) acc[c] = fmaf(w, f[c], acc[c]);
-        }
-      }
-      if (++g == groups) {
-        Word<16> o;
-        V::put(o, acc);
-        if (r[s].col < row_bytes) o.store(y.p + r[s].t * y.ld + r[s].col);
-#pragma unroll
-        for (int c = 0; c < V::kN; ++c) acc[c] = 0.0f;
-        g = 0;
-      }
-      r[s] = next[s];
-      ask(r[s], s);
-      next[s] = route(i + 2 * kDepth);
-    }
-  }
-}
-
-// The same for rows of any alignment, U elements of 32 lanes a unit.
+// y[t] = sum over slots of weight * row. A unit is a token and U words a lane of its
+// row, in eight slots at once: 64 registers of loads, two CTAs an SM. Rows of whole
+// 16-byte words take two of them a lane, 1 KB of each row a warp (32768 tokens of 8
+// slots 179 us; one word of 32 bytes 215, four of 8 bytes 180, two of 8 bytes, with
+// more CTAs, 254 to 319; asynchronous copies through shared memory, four steps
+// ahead, 189). Others take eight of 4 or of 2 bytes.
 template <typename T, int B, int U>
-__global__ void __launch_bounds__(kThreads, 2) combine_any_kernel(
+__global__ void __launch_bounds__(kThreads, 2) combine_kernel(
     Matrix rows, const int32_t* dest_row, const float* weights, int64_t T_, int64_t M, int64_t words, int k, Matrix y,
     int32_t* status) {
   using V = Values<T, B>;
@@ -571,180 +463,60 @@ __global__ void __launch_bounds__(kThreads, 2) combine_any_kernel(
   }
 }
 
-// drows[d] = weight * dy[t] and, with DOT, dweights = <dy[t], rows[d]>, for rows of
-// whole 16-byte words. `team` warps of a CTA share a token: member m takes the
-// 512-byte pieces m, m + team, ... of its row. A step is one piece in up to 8 slots,
-// asked for four steps ahead as in combine_kernel. A member's dot products stay in
-// its lanes until its last piece, and wait in shared memory for the other members';
-// every kHeld tokens all are added, in the members' order. team follows from the
-// row's size alone, so the sums do not depend on the other tokens. drows may be
-// rows: a piece is read by the warp that writes it, before it does.
+// drows[d] = weight * dy[t] and, with DOT, dweights = <dy[t], rows[d]>. `team` warps of
+// a CTA share a token: member m takes pieces m, m + team, ... of its row, a piece being
+// U words of 32 lanes, in eight slots at once. A member's dot products stay in its
+// lanes until its last piece and then wait in shared memory for the other members';
+// every kHeld items (a token and eight slots) all are added, in the members' order.
+// team follows from the row's size alone, so the sums do not depend on the other
+// tokens. drows may be rows: a piece is read by the warp that writes it, before it does.
 constexpr int kHeld = 16;
-struct BackwardShared {
-  uint4 stage[kWarps][kDepth][kSlots + 1][32];   // the last: dy
-  float dot[kHeld][kWarps][kSlots];
-};
-template <typename T, bool DOT>
-__global__ void __launch_bounds__(kThreads, 1) combine_backward_kernel(
-    Matrix dy, Matrix rows, const int32_t* dest_row, const float* weights, int64_t T_,
-    int64_t M, int64_t row_bytes, int k, int team, Matrix drows, float* dweights, int32_t* status) {
-  using V = Values<T, 16>;
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  BackwardShared& S = *reinterpret_cast<BackwardShared*>(smem_raw);
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  uint4 (*stage)[kSlots + 1][32] = S.stage[wid];
+template <typename T, int B, int U, bool DOT>
+__global__ void __launch_bounds__(kThreads, 2) combine_backward_kernel(
+    Matrix dy, Matrix rows, const int32_t* dest_row, const float* weights, int64_t T_, int64_t M, int64_t words, int k,
+    int team, Matrix drows, float* dweights, int32_t* status) {
+  using V = Values<T, B>;
+  __shared__ float s_dot[kHeld][kWarps][kSlots];
   pdl_wait();
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int teams = kWarps / team, mine = wid / team, member = wid % team;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * teams;   // the CTA's first token
   const int64_t stride = static_cast<int64_t>(gridDim.x) * teams;
+  const int64_t turns = first < T_ ? (T_ - first - 1) / stride + 1 : 0;   // the same for every team
   const int groups = (k + kSlots - 1) / kSlots;
-  const int parts = static_cast<int>((row_bytes + kPieceBytes - 1) / kPieceBytes);
-  const int pieces = (parts + team - 1) / team;   // steps of an item, the last may have no piece
-  // an item is a token and 8 of its slots: item i of a team is group i % groups of
-  // its token i / groups; the same number for every team of the CTA
-  const int64_t items = first < T_ ? ((T_ - first - 1) / stride + 1) * groups : 0;
-  const int64_t steps = items * pieces;
-  struct Route {
-    int dest;
-    float w;
-    int64_t t;
-    int32_t col;
-  };
-  auto route = [&](int64_t i) {
-    Route r = {-1, 0.0f, 0, 0x7FFFFFFF};
-    if (i < steps) {
-      const int64_t item = div_nonneg(i, pieces);
-      const int piece = static_cast<int>(i - item * pieces) * team + member;
-      const int64_t turn = div_nonneg(item, groups);
-      r.t = first + mine + turn * stride;
-      const int j = static_cast<int>(item - turn * groups) * kSlots + lane;
-      if (r.t < T_ && piece < parts) {
-        r.col = piece * kPieceBytes + 16 * lane;
-        if (lane < kSlots && j < k) {
-          r.dest = dest_row[r.t * k + j];
-          r.w = weights[r.t * k + j];
-        }
-      }
-    }
-    return r;
-  };
-  auto ask = [&](Route& r, int s) {
-    if (r.dest >= M) {
-      set_status(status, MINITE_ERR_BAD_ROUTING);
-      r.dest = -1;
-    }
-    if (r.col < row_bytes) ask16(&stage[s][kSlots][lane], dy.p + r.t * dy.ld + r.col);
-    if constexpr (DOT) {
-#pragma unroll
-      for (int j = 0; j < kSlots; ++j) {
-        const int d = __shfl_sync(0xffffffffu, r.dest, j);
-        if (d >= 0 && r.col < row_bytes) ask16(&stage[s][j][lane], rows.p + d * rows.ld + r.col);
-      }
-    }
-    close_group();
-  };
-  Route r[kDepth], next[kDepth];
-#pragma unroll
-  for (int s = 0; s < kDepth; ++s) r[s] = route(s);
-#pragma unroll
-  for (int s = 0; s < kDepth; ++s) next[s] = route(kDepth + s);
-#pragma unroll
-  for (int s = 0; s < kDepth; ++s) ask(r[s], s);
-  float dot[kSlots];
-#pragma unroll
-  for (int j = 0; j < kSlots; ++j) dot[j] = 0.0f;
-  int piece = 0, held = 0;
-  int64_t item0 = 0;   // the first item that is held
-  for (int64_t i = 0; i < steps;) {
-#pragma unroll
-    for (int s = 0; s < kDepth; ++s, ++i) {
-      if (i >= steps) break;
-      wait_groups<kDepth - 1>();
-      const bool live = r[s].col < row_bytes;
-      float d[V::kN];
-      V::get(slot_word(stage[s][kSlots][lane]), d);
-#pragma unroll
-      for (int j = 0; j < kSlots; ++j) {
-        const int to = __shfl_sync(0xffffffffu, r[s].dest, j);
-        const float w = __shfl_sync(0xffffffffu, r[s].w, j);
-        if (to >= 0 && live) {
-          float f[V::kN];
-          if constexpr (DOT) {
-            V::get(slot_word(stage[s][j][lane]), f);
-#pragma unroll
-            for (int c = 0; c < V::kN; ++c) dot[j] = fmaf(d[c], f[c], dot[j]);
-          }
-#pragma unroll
-          for (int c = 0; c < V::kN; ++c) f[c] = w * d[c];
-          Word<16> o;
-          V::put(o, f);
-          o.store(drows.p + to * drows.ld + r[s].col);
-        }
-      }
-      r[s] = next[s];
-      ask(r[s], s);
-      next[s] = route(i + 2 * kDepth);
-      if constexpr (DOT) {
-        if (++piece == pieces) {
-          const float sum = warp_sum8(dot);
-          if ((lane & 3) == 0) S.dot[held][wid][lane >> 2] = sum;
-#pragma unroll
-          for (int j = 0; j < kSlots; ++j) dot[j] = 0.0f;
-          piece = 0;
-          if (++held == kHeld || i + 1 == steps) {
-            __syncthreads();
-            for (int x = threadIdx.x; x < held * teams * kSlots; x += kThreads) {
-              const int j = x % kSlots, q = x / kSlots % teams;
-              const int64_t item = item0 + x / (kSlots * teams);
-              const int64_t turn = div_nonneg(item, groups), t = first + q + turn * stride;
-              const int slot = static_cast<int>(item - turn * groups) * kSlots + j;
-              if (t < T_ && slot < k) {
-                float v = 0.0f;
-                for (int m = 0; m < team; ++m) v += S.dot[x / (kSlots * teams)][q * team + m][j];
-                dweights[t * k + slot] = v;
-              }
-            }
-            __syncthreads();
-            item0 += held;
-            held = 0;
-          }
-        }
-      }
-    }
-  }
-}
-
-// The same for rows of any alignment, U elements of 32 lanes a piece, a warp a
-// token: a piece's dot products are summed over the warp, then over the pieces in
-// order.
-template <typename T, int B, int U, bool DOT>
-__global__ void __launch_bounds__(kThreads, 2) combine_backward_any_kernel(
-    Matrix dy, Matrix rows, const int32_t* dest_row, const float* weights,
-    int64_t T_, int64_t M, int64_t words, int k, Matrix drows, float* dweights,
-    int32_t* status) {
-  using V = Values<T, B>;
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
   const int parts = static_cast<int>((words + 32 * U - 1) / (32 * U));
-  const int64_t nwarps = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); t < T_; t += nwarps) {
-    int mine = -1;
-    float my_w = 0.0f;
-    if (lane < k) {
-      mine = dest_row[t * k + lane];
-      my_w = weights[t * k + lane];
-      if (mine >= M) {
-        set_status(status, MINITE_ERR_BAD_ROUTING);
-        mine = -1;
-      }
+  int next = -1;
+  float next_w = 0.0f;
+  auto ask = [&](int64_t turn) {
+    const int64_t t = first + mine + turn * stride;
+    next = -1;
+    if (turn < turns && t < T_ && lane < k) {
+      next = dest_row[t * k + lane];
+      next_w = weights[t * k + lane];
     }
-    for (int j0 = 0; j0 < k; j0 += kSlots) {
-      float sum = 0.0f;
-      for (int part = 0; part < parts; ++part) {
+  };
+  ask(0);
+  int held = 0;
+  int64_t item0 = 0;   // the first item that is held
+  for (int64_t turn = 0; turn < turns; ++turn) {
+    const int64_t t = first + mine + turn * stride;
+    int dest = next;
+    const float my_w = next_w;
+    ask(turn + 1);
+    if (dest >= M) {
+      set_status(status, MINITE_ERR_BAD_ROUTING);
+      dest = -1;
+    }
+    for (int g = 0; g < groups; ++g) {
+      const int j0 = g * kSlots;
+      float dot[kSlots];
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) dot[j] = 0.0f;
+      for (int part = t < T_ ? member : parts; part < parts; part += team) {
         const int64_t w0 = static_cast<int64_t>(part) * (32 * U) + lane;
         // every word is used under the condition under which it is loaded: one that
-        // was set to 0 first made each load wait for the one before it (95 us for
-        // 12000 tokens of 201 columns)
+        // was set to 0 first made each load wait for the one before it (95 us in
+        // place of 24 for 12000 tokens of 201 columns)
         Word<B> d[U], v[kSlots][U];
 #pragma unroll
         for (int i = 0; i < U; ++i)
@@ -752,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 2) combine_backward_any_kernel(
         if constexpr (DOT) {
 #pragma unroll
           for (int jj = 0; jj < kSlots; ++jj) {
-            const int to = __shfl_sync(0xffffffffu, mine, (j0 + jj) & 31);
+            const int to = __shfl_sync(0xffffffffu, dest, (j0 + jj) & 31);
             const char* row = rows.p + to * rows.ld;
             if (j0 + jj < k && to >= 0) {
 #pragma unroll
@@ -761,12 +533,10 @@ __global__ void __launch_bounds__(kThreads, 2) combine_backward_any_kernel(
             }
           }
         }
-        float dot[kSlots];
 #pragma unroll
         for (int jj = 0; jj < kSlots; ++jj) {
-          const int to = __shfl_sync(0xffffffffu, mine, (j0 + jj) & 31);
+          const int to = __shfl_sync(0xffffffffu, dest, (j0 + jj) & 31);
           const float w = __shfl_sync(0xffffffffu, my_w, (j0 + jj) & 31);
-          dot[jj] = 0.0f;
           if (j0 + jj < k && to >= 0) {
             char* row = drows.p + to * drows.ld;
 #pragma unroll
@@ -787,10 +557,27 @@ __global__ void __launch_bounds__(kThreads, 2) combine_backward_any_kernel(
               }
           }
         }
-        if constexpr (DOT) sum += warp_sum8(dot);
       }
-      if constexpr (DOT)
-        if ((lane & 3) == 0 && j0 + (lane >> 2) < k) dweights[t * k + j0 + (lane >> 2)] = sum;
+      if constexpr (DOT) {
+        const float sum = warp_sum8(dot);
+        if ((lane & 3) == 0) s_dot[held][wid][lane >> 2] = sum;
+        if (++held == kHeld || (turn + 1 == turns && g + 1 == groups)) {
+          __syncthreads();
+          for (int x = threadIdx.x; x < held * teams * kSlots; x += kThreads) {
+            const int j = x % kSlots, q = x / kSlots % teams, h = x / (kSlots * teams);
+            const int64_t at = div_nonneg(item0 + h, groups), token = first + q + at * stride;
+            const int slot = static_cast<int>(item0 + h - at * groups) * kSlots + j;
+            if (token < T_ && slot < k) {
+              float sum_of = 0.0f;
+              for (int m = 0; m < team; ++m) sum_of += s_dot[h][q * team + m][j];
+              dweights[token * k + slot] = sum_of;
+            }
+          }
+          __syncthreads();
+          item0 += held;
+          held = 0;
+        }
+      }
     }
   }
 }
@@ -854,44 +641,43 @@ cudaError_t copy(const Matrix& x, int64_t T, int64_t row_bytes, int k, const Rou
   }
 }
 
+template <typename T, int B, int U>
+cudaError_t combine_as(const Matrix& rows, const int32_t* dest_row, const float* weights, int64_t T_, int64_t M,
+                       int64_t H, int k, const Matrix& y, int32_t* status, cudaStream_t s) {
+  const int64_t words = H * static_cast<int64_t>(sizeof(T)) / B, parts = (words + 32 * U - 1) / (32 * U);
+  return launch_pdl(combine_kernel<T, B, U>, dim3(blocks_for(T_ * parts, 2)), dim3(kThreads), 0, s, rows, dest_row,
+                    weights, T_, M, words, k, y, status);
+}
 template <typename T>
 cudaError_t combine(const Matrix& rows, const int32_t* dest_row, const float* weights, int64_t T_, int64_t M,
                     int64_t H, int k, const Matrix& y, int32_t* status, cudaStream_t s) {
-  const int64_t row_bytes = H * static_cast<int64_t>(sizeof(T));
-  if (width(row_bytes, {rows, y}) < 16) {
-    const int64_t parts = (H + 255) / 256;
-    return launch_pdl(combine_any_kernel<T, sizeof(T), 8>, dim3(blocks_for(T_ * parts, 2)), dim3(kThreads), 0, s,
-                      rows, dest_row, weights, T_, M, H, k, y, status);
-  }
-  static std::atomic<uint64_t> devices{0};
-  const cudaError_t e = allow_smem(devices, combine_kernel<T>, sizeof(CombineShared));
-  if (e != cudaSuccess) return e;
-  const int64_t units = T_ * ((row_bytes + kPieceBytes - 1) / kPieceBytes);
-  int64_t ctas = (units + kCombineWarps - 1) / kCombineWarps;
-  if (ctas > num_sms()) ctas = num_sms();
-  return launch_pdl(combine_kernel<T>, dim3(static_cast<unsigned>(ctas)), dim3(32 * kCombineWarps),
-                    sizeof(CombineShared), s, rows, dest_row, weights, T_, M, row_bytes, k, y, status);
+  const int w = width(H * static_cast<int64_t>(sizeof(T)), {rows, y});
+  if (w >= 16) return combine_as<T, 16, 2>(rows, dest_row, weights, T_, M, H, k, y, status, s);
+  if constexpr (sizeof(T) == 2)
+    if (w == 2) return combine_as<T, 2, 8>(rows, dest_row, weights, T_, M, H, k, y, status, s);
+  return combine_as<T, 4, 8>(rows, dest_row, weights, T_, M, H, k, y, status, s);
 }
 
+template <typename T, int B, int U, bool DOT>
+cudaError_t backward_as(const Matrix& dy, const Matrix& rows, const int32_t* dest_row, const float* weights,
+                        int64_t T_, int64_t M, int64_t H, int k, const Matrix& drows, float* dweights,
+                        int32_t* status, cudaStream_t s) {
+  const int64_t words = H * static_cast<int64_t>(sizeof(T)) / B, parts = (words + 32 * U - 1) / (32 * U);
+  int team = 1;
+  while (team < kWarps && team < parts) team *= 2;
+  return launch_pdl(combine_backward_kernel<T, B, U, DOT>, dim3(blocks_for(T_ * team, 2)), dim3(kThreads), 0, s, dy,
+                    rows, dest_row, weights, T_, M, words, k, team, drows, dweights, status);
+}
 template <typename T, bool DOT>
 cudaError_t backward(const Matrix& dy, const Matrix& rows, const int32_t* dest_row, const float* weights, int64_t T_,
                      int64_t M, int64_t H, int k, const Matrix& drows, float* dweights, int32_t* status,
                      cudaStream_t s) {
   const int64_t row_bytes = H * static_cast<int64_t>(sizeof(T));
-  if ((DOT ? width(row_bytes, {dy, rows, drows}) : width(row_bytes, {dy, drows})) < 16)
-    return launch_pdl(combine_backward_any_kernel<T, sizeof(T), 8, DOT>, dim3(blocks_for(T_, 2)), dim3(kThreads), 0, s,
-                      dy, rows, dest_row, weights, T_, M, H, k, drows, dweights, status);
-  static std::atomic<uint64_t> devices{0};
-  const cudaError_t e = allow_smem(devices, combine_backward_kernel<T, DOT>, sizeof(BackwardShared));
-  if (e != cudaSuccess) return e;
-  int team = 1;
-  while (team < kWarps && team * kPieceBytes < row_bytes) team *= 2;
-  const int teams = kWarps / team;
-  int64_t ctas = (T_ + teams - 1) / teams;
-  if (ctas > num_sms()) ctas = num_sms();
-  return launch_pdl(combine_backward_kernel<T, DOT>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads),
-                    sizeof(BackwardShared), s, dy, rows, dest_row, weights, T_, M, row_bytes, k, team, drows, dweights,
-                    status);
+  const int w = DOT ? width(row_bytes, {dy, rows, drows}) : width(row_bytes, {dy, drows});
+  if (w >= 16) return backward_as<T, 16, 2, DOT>(dy, rows, dest_row, weights, T_, M, H, k, drows, dweights, status, s);
+  if constexpr (sizeof(T) == 2)
+    if (w == 2) return backward_as<T, 2, 8, DOT>(dy, rows, dest_row, weights, T_, M, H, k, drows, dweights, status, s);
+  return backward_as<T, 4, 8, DOT>(dy, rows, dest_row, weights, T_, M, H, k, drows, dweights, status, s);
 }
 
 // The shape rules that all four entry points share.
