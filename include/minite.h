@@ -753,7 +753,7 @@ int minite_adamw_step(const minite_adamw_tensor* tensors, int64_t n_tensors, int
  *           bytes, 256-byte aligned, contents on entry ignored; NULL where that is 0.
  * Shape rules: 1 <= H <= 2^24, 1 <= E <= 1024, 1 <= k <= 32, T*k < 2^31, T = 0
  * allowed (offsets become 0), strides at least H and below 2^31. Matrices are
- * aligned to their element; accesses are wide (32 or 16 bytes) where base addresses,
+ * aligned to their element; accesses are 16 bytes wide where base addresses,
  * row sizes and strides are multiples of that, 4 or 2 bytes otherwise.
  */
 int minite_moe_permute_rows(const void* x, int dtype, int64_t x_stride, const int32_t* topk_ids,

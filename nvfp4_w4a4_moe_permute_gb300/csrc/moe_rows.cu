@@ -37,20 +37,9 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSlots = 8;   // rows of a token in flight at once
 
-// B bytes, one access of a lane. Loads are volatile and clobber memory, so that
-// they stay behind pdl_wait().
+// B bytes, one access of a lane (32 bytes were 4% slower in the copies, more in the
+// sums).
 template <int B> struct Word;
-template <> struct Word<32> {
-  uint32_t w[8];
-  __device__ __forceinline__ void load(const char* p) {
-    asm volatile("ld.global.cs.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
-                   "=r"(w[7]) : "l"(p) : "memory");
-  }
-  __device__ __forceinline__ void store(char* p) const {
-    st_global_v8(p, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
-  }
-};
 template <> struct Word<16> {
   uint32_t w[4];
   __device__ __forceinline__ void load(const char* p) {
@@ -589,7 +578,7 @@ inline int64_t size_of(int d) { return d == MINITE_OUT_FP32 ? 4 : 2; }
 inline int width(int64_t row_bytes, std::initializer_list<Matrix> ms) {
   uintptr_t bits = static_cast<uintptr_t>(row_bytes);
   for (const Matrix& m : ms) bits |= reinterpret_cast<uintptr_t>(m.p) | static_cast<uintptr_t>(m.ld);
-  for (int b : {32, 16, 4}) if (bits % b == 0) return b;
+  for (int b : {16, 4}) if (bits % b == 0) return b;
   return 2;
 }
 
@@ -624,8 +613,7 @@ template <bool TABLE>
 cudaError_t range(const Matrix& x, int64_t T, int64_t row_bytes, int k, int E, const Routing& r, const Sorted& o,
                   const Matrix& out, int32_t* status, cudaStream_t s) {
   switch (width(row_bytes, {x, out})) {
-    case 32: return range_as<32, 2, TABLE>(x, T, row_bytes, k, E, r, o, out, status, s);
-    case 16: return range_as<16, 4, TABLE>(x, T, row_bytes, k, E, r, o, out, status, s);
+    case 16: return range_as<16, 8, TABLE>(x, T, row_bytes, k, E, r, o, out, status, s);
     case 4: return range_as<4, 8, TABLE>(x, T, row_bytes, k, E, r, o, out, status, s);
     default: return range_as<2, 8, TABLE>(x, T, row_bytes, k, E, r, o, out, status, s);
   }
@@ -634,7 +622,6 @@ cudaError_t range(const Matrix& x, int64_t T, int64_t row_bytes, int k, int E, c
 cudaError_t copy(const Matrix& x, int64_t T, int64_t row_bytes, int k, const Routing& r, const Matrix& out,
                  int64_t M, int32_t* status, cudaStream_t s) {
   switch (width(row_bytes, {x, out})) {
-    case 32: return copy_as<32, 4>(x, T, row_bytes, k, r, out, M, status, s);
     case 16: return copy_as<16, 4>(x, T, row_bytes, k, r, out, M, status, s);
     case 4: return copy_as<4, 8>(x, T, row_bytes, k, r, out, M, status, s);
     default: return copy_as<2, 8>(x, T, row_bytes, k, r, out, M, status, s);
@@ -652,7 +639,7 @@ template <typename T>
 cudaError_t combine(const Matrix& rows, const int32_t* dest_row, const float* weights, int64_t T_, int64_t M,
                     int64_t H, int k, const Matrix& y, int32_t* status, cudaStream_t s) {
   const int w = width(H * static_cast<int64_t>(sizeof(T)), {rows, y});
-  if (w >= 16) return combine_as<T, 16, 2>(rows, dest_row, weights, T_, M, H, k, y, status, s);
+  if (w == 16) return combine_as<T, 16, 2>(rows, dest_row, weights, T_, M, H, k, y, status, s);
   if constexpr (sizeof(T) == 2)
     if (w == 2) return combine_as<T, 2, 8>(rows, dest_row, weights, T_, M, H, k, y, status, s);
   return combine_as<T, 4, 8>(rows, dest_row, weights, T_, M, H, k, y, status, s);
@@ -674,7 +661,7 @@ cudaError_t backward(const Matrix& dy, const Matrix& rows, const int32_t* dest_r
                      cudaStream_t s) {
   const int64_t row_bytes = H * static_cast<int64_t>(sizeof(T));
   const int w = DOT ? width(row_bytes, {dy, rows, drows}) : width(row_bytes, {dy, drows});
-  if (w >= 16) return backward_as<T, 16, 2, DOT>(dy, rows, dest_row, weights, T_, M, H, k, drows, dweights, status, s);
+  if (w == 16) return backward_as<T, 16, 2, DOT>(dy, rows, dest_row, weights, T_, M, H, k, drows, dweights, status, s);
   if constexpr (sizeof(T) == 2)
     if (w == 2) return backward_as<T, 2, 8, DOT>(dy, rows, dest_row, weights, T_, M, H, k, drows, dweights, status, s);
   return backward_as<T, 4, 8, DOT>(dy, rows, dest_row, weights, T_, M, H, k, drows, dweights, status, s);
