@@ -1,6 +1,6 @@
-"""Rows by expert on a device that is new to them: their kernels get their shared
-memory there too (see test_second_device.py, whose stand-in for the CUDA runtime
-answers here)."""
+"""Rows by expert on a device that is new to them: their launches, with the shared
+memory that they ask for, go through there too (see test_second_device.py, whose
+stand-in for the CUDA runtime answers here)."""
 import ctypes
 import os
 import shutil
