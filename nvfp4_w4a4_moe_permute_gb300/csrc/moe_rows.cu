@@ -15,10 +15,9 @@
 // Bound by HBM, reads at up to 7.3 TB/s and writes at 6.4. BF16 rows of 2048 columns,
 // top-8 of 128 experts, a pass among others (in brackets what the bytes take at the
 // measured copy rate): 32768 tokens permuted 199 us (181), combined 180 (181); a
-// micro-batch of 4096 permuted 28.5 (22.6), summed back 24.0 (22.6), weighted gradient
-// 48.8 (42.7). What a micro-batch permuted has above that is the sort (7 us, of which
-// the copies hide little) and the start and end of a kernel that runs for 25 us. One
-// token takes 3 us.
+// micro-batch of 4096 permuted 25.8 (22.6), summed back 24.0 (22.6), weighted gradient
+// 48.8 (42.7). What a micro-batch permuted has above its writes (21) is the sort, 5 us.
+// One token takes 3.5 us.
 #include <initializer_list>
 
 #include "common.cuh"
@@ -163,23 +162,25 @@ __global__ void __launch_bounds__(kThreads) copy_kernel(Matrix x, int64_t T, int
       r.perm_src[i] = -1;
 }
 
-// Permutations of up to kTablePairs slots, without a scan kernel: every CTA has a
-// range of tokens and finds out by itself how many slots of each expert come before
-// them and in all.
-//   TABLE false, up to kDirectPairs slots: one launch. The CTA reads all ids and
-//     counts them by atomics in shared memory (10 cycles each 32 ids).
-//   TABLE true: after the ranking kernel, whose counts of each expert in each chunk
-//     of 512 slots it adds up.
-// With rows of 32 bytes, top-8 of 128 experts, on the device: 1024 tokens 4.3 us in
-// the first form and 6.0 in the second, 2048 tokens 6.4 and 6.1 (a call of the first
-// costs the host 8 us less), 4096 tokens 10.3 and 7.2; 11.0 by ranking, scan kernel
-// and copies.
+// Permutations of up to kClusterPairs slots in one launch: every CTA has a range of
+// tokens, and finds out by itself how many slots of each expert come before them and
+// in all. It counts by atomics in shared memory (10 cycles each 32 ids): up to
+// kDirectPairs slots all ids, above that a CL-th of them, what the CTAs of a cluster
+// have counted being added up from one another's shared memory. A thread has one slot
+// of the range; those of the warps in front are a row of 16 bytes for each expert.
+// With rows of 32 bytes, top-8 of 128 experts, on the device: 1024 tokens 4.1 us, 2048
+// 5.5, 4096 in clusters 7.4 and 8192 9.9; by ranking, scan kernel and copies 4096 take
+// 11.0, and the host 9 us more a call. In 76 clusters of 2 they take 7.5 and 11.5; of
+// clusters of 8 only 15 are resident, too few for 8192.
+// Rows are written faster by somewhat fewer SMs than there are: rows of 4 KB, 4096
+// tokens, in 104 CTAs 28.0 us, 112 26.8, 120 and 124 26.0, 136 27.8, 144 27.6; rows of
+// 14 KB, 5000 tokens, 110, 110, 109, 118, 114. Rows of 32 bytes take 0.9 us less in 144.
 constexpr int64_t kDirectPairs = 16384;
-constexpr int64_t kTablePairs = 65536;
-constexpr int64_t kTableEntries = 16384;   // of chunks x experts: what a CTA reads
+constexpr int64_t kClusterPairs = 65536;
+constexpr int kRangeCluster = 4;
+constexpr int kRangeSms = 80;   // CTAs in clusters, of 100 SMs (95 would be resident)
 constexpr int kRangeThreads = 512;
 constexpr int kRangeWarps = kRangeThreads / 32;
-// A range is no longer than a chunk then (65536 / 152 slots), and lies in two at most.
 
 // Sum of v over the threads in front of this one, and over all.
 __device__ __forceinline__ int scan_before(int v, int* s_warp, int* total) {
@@ -203,24 +204,31 @@ __device__ __forceinline__ int scan_before(int v, int* s_warp, int* total) {
   return before + in - v;
 }
 
-template <int B, int U, bool TABLE>
-__global__ void __launch_bounds__(kRangeThreads, 1) range_kernel(
-    Matrix x, int64_t T, int64_t words, int k, int E, const int32_t* ids, const int32_t* table, const int32_t* rank,
-    int ct, int nchunks, int32_t* offsets, int32_t* perm_src, int32_t* dest_row, Matrix out, int32_t* status) {
-  extern __shared__ int32_t sm[];
+template <int B, int U, int CL>
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(kRangeThreads, 1) range_kernel(
+    Matrix x, int64_t T, int64_t words, int k, int E, const int32_t* ids, int32_t* offsets, int32_t* perm_src,
+    int32_t* dest_row, Matrix out, int32_t* status) {
+  extern __shared__ __align__(16) int32_t sm[];
   __shared__ int s_warp[kRangeWarps];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int member = static_cast<int>(blockIdx.x) % CL;
   const int per = static_cast<int>((T + gridDim.x - 1) / gridDim.x);
   const int t0 = min(static_cast<int>(T), static_cast<int>(blockIdx.x) * per), t1 = min(static_cast<int>(T), t0 + per);
   const int p0 = t0 * k, own = (t1 - t0) * k, pairs = static_cast<int>(T) * k;
-  int32_t* s_before = sm;            // [E] slots before the range; then the row of the first in it
-  int32_t* s_all = sm + E;           // [E] slots after that; TABLE: in all
-  int32_t* s_first = sm + 2 * E;     // [E] TABLE: slots in the range's first chunk
-  int32_t* s_dest = sm + 3 * E;      // [per * k] ids, then rows
-  if constexpr (!TABLE) {
-    for (int e = tid; e < 2 * E; e += kRangeThreads) sm[e] = 0;
-    __syncthreads();
-  }
+  // the cluster's first slot, and the slots that this CTA counts
+  const int first = min(static_cast<int>(T), (static_cast<int>(blockIdx.x) - member) * per) * k;
+  const int share = (pairs + 4 * CL - 1) / (4 * CL) * 4;
+  const int lo = min(pairs, member * share), hi = min(pairs, lo + share);
+  int32_t* s_before = sm;            // [E] counted slots before the cluster's first
+  int32_t* s_after = sm + E;         // [E] the others
+  int32_t* s_own = sm + 2 * E;       // [E] slots of the range
+  int32_t* s_first = sm + 3 * E;     // [E] row of the range's first slot
+  // [E][kRangeWarps] the slots of each warp's 32 of the range, a byte each; [per * k] rows
+  uint8_t* s_warps = reinterpret_cast<uint8_t*>(sm + 4 * E);
+  int32_t* s_dest = sm + 8 * E;
+  for (int e = tid; e < 3 * E; e += kRangeThreads) sm[e] = 0;
+  for (int e = tid; e < E; e += kRangeThreads) reinterpret_cast<uint4*>(s_warps)[e] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
   pdl_wait();
   // units of this CTA: a token and U words a lane
   const int parts = static_cast<int>((words + 32 * U - 1) / (32 * U));
@@ -235,103 +243,80 @@ __global__ void __launch_bounds__(kRangeThreads, 1) range_kernel(
   };
   Word<B> va[U], vb[U];
   fetch(wid, va);
-  const int c0 = t0 / (TABLE ? ct : 1);   // the first token's chunk
-  int my_e = -1, my_rank = 0;   // TABLE: slot tid of the range (a chunk has 512 at most)
-  if constexpr (TABLE) {
-    if (tid < own) {
-      my_e = ids[p0 + tid];
-      my_rank = rank[p0 + tid];
+  bool bad = false;
+  auto count = [&](int p, int e) {
+    bad |= e >= E;
+    if (e >= 0 && e < E) atomicAdd((p < first ? s_before : s_after) + e, 1);
+  };
+  if ((reinterpret_cast<uintptr_t>(ids) & 15) == 0) {
+    const int4* ids4 = reinterpret_cast<const int4*>(ids);
+    for (int q = lo / 4 + tid; q < hi / 4; q += kRangeThreads) {
+      const int4 a = ids4[q];
+      count(4 * q, a.x);
+      count(4 * q + 1, a.y);
+      count(4 * q + 2, a.z);
+      count(4 * q + 3, a.w);
     }
-    constexpr int kAhead = 8;
-    for (int e0 = wid; e0 < E; e0 += kAhead * kRangeWarps) {
-      int all[kAhead] = {}, before[kAhead] = {}, first[kAhead] = {};
-      for (int c = lane; c < nchunks; c += 32) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          const int e = e0 + i * kRangeWarps;
-          const int n = e < E ? table[e * nchunks + c] : 0;
-          all[i] += n;
-          if (c < c0) before[i] += n;
-          if (c == c0) first[i] = n;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int e = e0 + i * kRangeWarps;
-        const int a = __reduce_add_sync(0xffffffffu, all[i]), f = __reduce_add_sync(0xffffffffu, before[i]),
-                  g = __reduce_add_sync(0xffffffffu, first[i]);
-        if (lane == 0 && e < E) {
-          s_all[e] = a;
-          s_before[e] = f;
-          s_first[e] = g;
-        }
-      }
-    }
+    for (int p = max(lo, hi & ~3) + tid; p < hi; p += kRangeThreads) count(p, ids[p]);
   } else {
-    bool bad = false;
-    auto count = [&](int p, int e) {
-      const bool valid = e >= 0 && e < E;
-      bad |= e >= E;
-      if (valid) atomicAdd(sm + (p < p0 ? e : E + e), 1);
-      if (p >= p0 && p < p0 + own) s_dest[p - p0] = valid ? e : -1;
-    };
-    if ((reinterpret_cast<uintptr_t>(ids) & 15) == 0) {
-      const int4* ids4 = reinterpret_cast<const int4*>(ids);
-      for (int q = tid; q < pairs / 4; q += kRangeThreads) {
-        const int4 a = ids4[q];
-        count(4 * q, a.x);
-        count(4 * q + 1, a.y);
-        count(4 * q + 2, a.z);
-        count(4 * q + 3, a.w);
-      }
-      for (int p = (pairs & ~3) + tid; p < pairs; p += kRangeThreads) count(p, ids[p]);
-    } else {
-      for (int p = tid; p < pairs; p += kRangeThreads) count(p, ids[p]);
-    }
-    if (bad && blockIdx.x == 0) set_status(status, MINITE_ERR_BAD_ROUTING);
+    for (int p = lo + tid; p < hi; p += kRangeThreads) count(p, ids[p]);
   }
-  __syncthreads();
+  // slot tid of the range, which has no more than threads
+  const int id = tid < own ? ids[p0 + tid] : -1;
+  const int my_e = id >= 0 && id < E ? id : E;
+  const uint32_t same = same_id_lanes(my_e, E);
+  const int in_warp = __popc(same & ((1u << lane) - 1u));
+  if (my_e < E && in_warp == 0) {
+    s_warps[my_e * kRangeWarps + wid] = static_cast<uint8_t>(__popc(same));
+    if (CL > 1) atomicAdd(s_own + my_e, __popc(same));
+  }
+  if (bad && blockIdx.x < CL) set_status(status, MINITE_ERR_BAD_ROUTING);
+  if constexpr (CL > 1) cluster_sync_all(); else __syncthreads();
   int used = 0;
   for (int base = 0; base < E; base += kRangeThreads) {
     const int e = base + tid;
-    const int n = e < E ? s_all[e] + (TABLE ? 0 : s_before[e]) : 0;
-    int total;
-    const int at = used + scan_before(n, s_warp, &total);
+    int before = 0, after = 0, others = 0;   // others: of the cluster's ranges in front
     if (e < E) {
-      s_before[e] += at;
+      if constexpr (CL > 1) {
+#pragma unroll
+        for (int m = 0; m < CL; ++m) {
+          const uint32_t at = mapa_shared(smem_u32(sm + e), m);
+          before += static_cast<int>(ld_shared_cluster(at));
+          after += static_cast<int>(ld_shared_cluster(at + 4 * E));
+          const int n = static_cast<int>(ld_shared_cluster(at + 8 * E));
+          if (m < member) others += n;
+        }
+      } else {
+        before = s_before[e];
+        after = s_after[e];
+      }
+    }
+    int total;
+    const int at = used + scan_before(before + after, s_warp, &total);
+    if (e < E) {
+      s_first[e] = at + before + others;
       if (blockIdx.x == 0) offsets[e] = at;
     }
     used += total;
     __syncthreads();
   }
+  if constexpr (CL > 1) cluster_arrive();   // nobody leaves while its counts are read
   if (blockIdx.x == 0 && tid == 0) offsets[E] = used;
-  // rows of this CTA's slots
-  if constexpr (TABLE) {
-    if (tid < own) {
-      const int t = t0 + tid / k;
-      int dest = -1;
-      if (my_e >= 0 && my_e < E) dest = s_before[my_e] + (t / ct > c0 ? s_first[my_e] : 0) + my_rank;
-      s_dest[tid] = dest;
-      dest_row[p0 + tid] = dest;
-      if (dest >= 0) perm_src[dest] = t;
-    }
-  } else if (wid == 0) {   // 32 at a time, in their order
-    for (int b = 0; b < own; b += 32) {
-      const int p = b + lane;
-      const int e = p < own ? s_dest[p] : -1;
-      const uint32_t same = same_id_lanes(e >= 0 ? e : E, E);
-      const int before = __popc(same & ((1u << lane) - 1u));
-      const int at = e >= 0 ? s_before[e] : 0;
-      __syncwarp();
-      if (e >= 0 && before == 0) s_before[e] = at + __popc(same);
-      __syncwarp();
-      if (p < own) {
-        const int dest = e >= 0 ? at + before : -1;
-        s_dest[p] = dest;
-        dest_row[p0 + p] = dest;
-        if (dest >= 0) perm_src[dest] = t0 + p / k;
+  if (tid < own) {
+    int dest = -1;
+    if (my_e < E) {   // after the slots of the warps in front
+      dest = s_first[my_e] + in_warp;
+      const uint4 c = reinterpret_cast<const uint4*>(s_warps)[my_e];
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = min(max(wid - 4 * i, 0), 4);   // of these four bytes
+        dest += __dp4a(w[i], n == 4 ? 0x01010101u : 0x01010101u & ((1u << (8 * n)) - 1u), 0u);
       }
+      perm_src[dest] = t0 + tid / k;
     }
+    s_dest[tid] = dest;
+    dest_row[p0 + tid] = dest;
   }
   __syncthreads();
   auto spread = [&](int u, const Word<B> (&v)[U]) {
@@ -354,6 +339,10 @@ __global__ void __launch_bounds__(kRangeThreads, 1) range_kernel(
     spread(u + kRangeWarps, vb);
   }
   for (int i = used + blockIdx.x * kRangeThreads + tid; i < pairs; i += gridDim.x * kRangeThreads) perm_src[i] = -1;
+  if constexpr (CL > 1) {
+    __syncwarp();
+    cluster_wait();
+  }
 }
 
 // Eight values a lane to their sums over the warp: lane l returns the sum of
@@ -602,22 +591,25 @@ struct Sorted {   // what a permutation writes besides the rows
   int32_t* perm_src;
   int32_t* dest_row;
 };
-template <int B, int U, bool TABLE>
-cudaError_t range_as(const Matrix& x, int64_t T, int64_t row_bytes, int k, int E, const Routing& r, const Sorted& o,
+template <int B, int U, int CL>
+cudaError_t range_as(const Matrix& x, int64_t T, int64_t row_bytes, int k, int E, const int32_t* ids, const Sorted& o,
                      const Matrix& out, int32_t* status, cudaStream_t s) {
-  const int64_t grid = T < num_sms() ? T : num_sms();
-  const size_t smem = (3 * static_cast<size_t>(E) + static_cast<size_t>((T + grid - 1) / grid) * k) * sizeof(int32_t);
-  return launch_pdl(range_kernel<B, U, TABLE>, dim3(static_cast<unsigned>(grid)), dim3(kRangeThreads), smem, s, x, T,
-                    row_bytes / B, k, E, r.ids, r.table, r.rank, r.ct, r.nchunks, o.offsets, o.perm_src, o.dest_row,
-                    out, status);
+  const int64_t tokens = kRangeThreads / k;   // a range has no more: a thread a slot
+  const int64_t many = CL == 1 ? num_sms() : num_sms() * kRangeSms / 100 / CL * CL;
+  int64_t grid = T < many ? T : many;
+  if (grid * tokens < T) grid = (T + tokens - 1) / tokens;
+  grid = (grid + CL - 1) / CL * CL;
+  const size_t smem = (8 * static_cast<size_t>(E) + static_cast<size_t>((T + grid - 1) / grid) * k) * sizeof(int32_t);
+  return launch_pdl(range_kernel<B, U, CL>, dim3(static_cast<unsigned>(grid)), dim3(kRangeThreads), smem, s, x, T,
+                    row_bytes / B, k, E, ids, o.offsets, o.perm_src, o.dest_row, out, status);
 }
-template <bool TABLE>
-cudaError_t range(const Matrix& x, int64_t T, int64_t row_bytes, int k, int E, const Routing& r, const Sorted& o,
+template <int CL>
+cudaError_t range(const Matrix& x, int64_t T, int64_t row_bytes, int k, int E, const int32_t* ids, const Sorted& o,
                   const Matrix& out, int32_t* status, cudaStream_t s) {
   switch (width(row_bytes, {x, out})) {
-    case 16: return range_as<16, 8, TABLE>(x, T, row_bytes, k, E, r, o, out, status, s);
-    case 4: return range_as<4, 8, TABLE>(x, T, row_bytes, k, E, r, o, out, status, s);
-    default: return range_as<2, 8, TABLE>(x, T, row_bytes, k, E, r, o, out, status, s);
+    case 16: return range_as<16, 8, CL>(x, T, row_bytes, k, E, ids, o, out, status, s);
+    case 4: return range_as<4, 8, CL>(x, T, row_bytes, k, E, ids, o, out, status, s);
+    default: return range_as<2, 8, CL>(x, T, row_bytes, k, E, ids, o, out, status, s);
   }
 }
 
@@ -687,7 +679,7 @@ inline Matrix matrix(const void* p, int dtype, int64_t stride) {
 
 // 0: minite_moe_permute_rows takes one launch and needs none.
 size_t permute_rows_workspace_bytes(int64_t T, int E, int k) {
-  return T * k <= rows::kDirectPairs ? 0 : routing_workspace_bytes(T, E, k);
+  return T * k <= rows::kClusterPairs ? 0 : routing_workspace_bytes(T, E, k);
 }
 
 }  // namespace minite
@@ -717,23 +709,20 @@ extern "C" int minite_moe_permute_rows(const void* x, int dtype, int64_t x_strid
   const Matrix from = matrix(x, dtype, x_stride), to = matrix(rows_out, dtype, rows_stride);
   const int64_t row_bytes = H * size_of(dtype);
   const Sorted o = {expert_offsets, perm_src, dest_row};
-  Routing r = {};
-  r.ids = topk_ids;
-  r.offsets = expert_offsets;
-  r.E = E;
-  r.dest_row = dest_row;
-  r.perm_src = perm_src;
   cudaError_t e;
-  if (need == 0) {
-    e = range<false>(from, T, row_bytes, k, E, r, o, to, status, s);
+  if (T * k <= kDirectPairs) {
+    e = range<1>(from, T, row_bytes, k, E, topk_ids, o, to, status, s);
+  } else if (need == 0) {
+    e = range<kRangeCluster>(from, T, row_bytes, k, E, topk_ids, o, to, status, s);
   } else {
-    const int64_t chunks = (T + permute_chunk_tokens(k) - 1) / permute_chunk_tokens(k);
-    const int64_t range_tokens = (T + num_sms() - 1) / num_sms();
-    const bool scan = T * k > kTablePairs || chunks * E > kTableEntries || range_tokens > permute_chunk_tokens(k);
-    launch_routing(topk_ids, T, k, E, workspace, scan ? expert_offsets : nullptr, &r.table, &r.rank, &r.ct,
-                   &r.nchunks, status, s);
-    e = scan ? copy(from, T, row_bytes, k, r, to, T * k, status, s)
-             : range<true>(from, T, row_bytes, k, E, r, o, to, status, s);
+    Routing r = {};
+    r.ids = topk_ids;
+    r.offsets = expert_offsets;
+    r.E = E;
+    r.dest_row = dest_row;
+    r.perm_src = perm_src;
+    launch_routing(topk_ids, T, k, E, workspace, expert_offsets, &r.table, &r.rank, &r.ct, &r.nchunks, status, s);
+    e = copy(from, T, row_bytes, k, r, to, T * k, status, s);
   }
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MINITE_OK : MINITE_ERR_CUDA;
 }

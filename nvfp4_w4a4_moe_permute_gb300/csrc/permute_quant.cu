@@ -196,9 +196,8 @@ __global__ void __launch_bounds__(kPermThreads) permute_scan_kernel(
 }
 
 // The ranking and scan alone, for permutations that place rows themselves: a
-// pair's row is expert_offsets[e] + table[e][t / ct] + rank[pair]. Without
-// expert_offsets the ranking alone: table[e][c] is chunk c's count. A negative id
-// is a slot that is not used, without a status bit. Any T >= 1, E <= 1024, k <= 32.
+// pair's row is expert_offsets[e] + table[e][t / ct] + rank[pair]. A negative id is
+// a slot that is not used, without a status bit. Any T >= 1, E <= 1024, k <= 32.
 size_t routing_workspace_bytes(int64_t T, int E, int k) {
   return perm_ws_base_bytes(T, E, k) + align256(static_cast<size_t>(T) * k * 4);
 }
@@ -214,7 +213,6 @@ void launch_routing(const int32_t* ids, int64_t T, int k, int E, void* workspace
   launch_pdl(permute_rank_kernel, dim3(*nchunks), dim3(kRankThreads),
              kRankWarps * E * sizeof(uint16_t), s, ids, T, k, E, *ct, *nchunks, w.table, r, w.counter,
              true, status);
-  if (!expert_offsets) return;   // the chunks' counts themselves
   launch_pdl(permute_scan_kernel, dim3(E), dim3(kPermThreads), 0, s, w.table, *nchunks, E, w.counter,
              w.totals, expert_offsets, static_cast<int32_t*>(nullptr));
 }

@@ -51,7 +51,7 @@ def matrix(g, rows, cols, dtype, pad=0, shift=0):
     return flat[shift:].view(rows, cols + pad)[:, :cols]
 
 
-# T, k, E, H: one launch up to 16384 slots, two up to 65536, three above or with many experts
+# T, k, E, H: one launch up to 65536 slots, clusters of CTAs above 16384, three launches above
 SORTS = [(1, 1, 1, 1), (1, 8, 128, 2048), (3, 2, 5, 7), (31, 32, 1024, 16), (152, 3, 9, 33), (153, 8, 7, 64),
          (1024, 8, 128, 24), (2049, 8, 128, 16), (4096, 8, 128, 40), (2100, 31, 3, 8), (65536, 1, 60, 8), (9000, 7, 17, 8),
          (3000, 8, 700, 16), (8193, 8, 128, 8), (70000, 2, 257, 8)]
@@ -78,6 +78,14 @@ def test_permute(T, k, E, H, dtype, dropped, skew, pad, shift):
     assert torch.equal(r["perm_src"][:n].cpu().long(), order // k) and (r["perm_src"][n:] == -1).all()
     assert torch.equal(out[:n, :H], x[(order // k).to(DEV)])
     assert (out[n:] == 7).all() and (out[:, H:] == 7).all()   # what no slot has stays
+
+
+# the longest ranges of a CTA: 512 slots, or the last number of tokens below that
+@pytest.mark.parametrize("T,k,E,H", [(7680, 8, 5, 8), (7681, 8, 128, 3), (7704, 8, 128, 4), (8192, 8, 256, 8), (1923, 32, 257, 8),
+                                     (3850, 16, 60, 1), (30785, 2, 1024, 16), (61441, 1, 9, 2), (2113, 31, 1024, 2),
+                                     (16384, 1, 1024, 8), (16385, 1, 2, 8), (512, 32, 700, 3), (513, 32, 3, 8)])
+def test_longest_ranges(T, k, E, H):
+    test_permute(T, k, E, H, BF, 0.2, 1.0, 0, 0)
 
 
 @pytest.mark.parametrize("T,k", [(5, 2), (5000, 8), (70000, 1)])
