@@ -868,21 +868,22 @@ int minite_clip_grads(const minite_grad_tensor* tensors, int64_t n_tensors, cons
  *   next = argmax_j max(p_n(j) - q_n(j), 0) / e_j   where draft n fell,
  *          argmax_j p_n(j) / e_j                     where there is none
  * equal quotients by the lower id. Where p_n - q_n leaves nothing above 0 (by
- * rounding), p_n is taken. With draft NULL the drafts were looked up: q_i is 1 at x_i.
+ * rounding) that its variate lets win, p_n is taken. With draft NULL the drafts were looked up: q_i is 1 at x_i.
  * logprobs[b, i] = log p_i(tokens[b, i]), 0 behind the last token.
  * Probabilities are FP32: a draft within some 2^-20 of the border, or two quotients as
  * near to each other, may go either way. A masked token (-inf) has probability 0; where
  * a row has no probabilities (a NaN or +inf logit, or none above -inf) a draft does not
- * stand, and a row to sample from that has none, or whose draft's row has none, gives
- * token -1 with logprob NaN. A draft at or above V sets bit 1<<MINITE_ERR_BAD_TOKEN and
+ * stand, and a row to sample from that has none, or whose draft's row has none, or of
+ * which no variate lets a token win, gives token -1 with logprob NaN. A draft at or above V sets bit 1<<MINITE_ERR_BAD_TOKEN and
  * ends its sequence's drafts.
  *
  * target: device, BF16 or FP32 [B * (S + 1), V], rows `target_stride` elements apart;
  * draft:  device, BF16 or FP32 [B * S, V] or NULL. Both aligned to the element.
  * draft_tokens: device, int32 [B, S]; uniforms: device, float [B, S], in [0, 1).
  * noise:  device, float [B, V], rows `noise_stride` apart: exponential variates, of
- *         2^-100 to 2^90 (a token whose variate is negative or NaN never wins, one whose
- *         variate is 0 wins where its weight is above 0).
+ *         2^-100 to 2^90. A token whose variate is negative, NaN or infinite never wins,
+ *         one whose variate is 0 wins where its probability, less q_n's, is above 0 (-0 is
+ *         0: -log(1 - uniform) makes it).
  * tokens: device, int32 [B, S + 1]; accepted: device, int32 [B]; logprobs: device, float
  *         [B, S + 1] or NULL.
  * workspace: device, >= minite_workspace_bytes(MINITE_OP_VERIFY_DRAFTS, B, V, S, 0)

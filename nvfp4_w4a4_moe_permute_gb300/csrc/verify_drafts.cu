@@ -290,10 +290,12 @@ __device__ __forceinline__ Row row_of(float2 v, const float2* part, int segs, fl
 struct Lead {
   float v = 0.0f;
   int32_t j = 0;
-  // weight times the variate's reciprocal, within 2 units; offered in rising order
+  // Weight (0 or more) times the variate's reciprocal, within 2 units; offered in
+  // rising order. Negative variates and NaN make a quotient that leads nothing, and so
+  // does a weight of 0 with any variate. The sum takes -0 to 0.
   __device__ __forceinline__ void offer(float weight, float e, int32_t at) {
     float q;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(e));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(e + 0.0f));
     q *= weight;
     if (q > v) {
       v = q;
@@ -328,7 +330,7 @@ __device__ __forceinline__ Lead race(const T* xt, const D* xd, const float* nois
   const float st = rt.log_s * kLog2e, sd = rd.log_s * kLog2e;
   auto weight = [&](T a, D b, int32_t j) {
     float w = rt.p(value(a), k, st);
-    if (WITH_Q) w -= rd.p(value(b), k, sd);
+    if (WITH_Q) w = fmaxf(w - rd.p(value(b), k, sd), 0.0f);   // below 0 a negative variate would make it win
     else if (j == without) w = 0.0f;
     return w;
   };
