@@ -862,7 +862,8 @@ int minite_clip_grads(const minite_grad_tensor* tensors, int64_t n_tensors, cons
  *
  * p_i = softmax(target[b, i] / temperature), q_i = softmax(draft[b, i] / temperature),
  * x_i = draft_tokens[b, i], u_i = uniforms[b, i], e = noise[b]. A sequence's drafts are
- * those before its first negative token. Draft i stands while u_i q_i(x_i) < p_i(x_i)
+ * those before its first negative token. All sequences of a call share one temperature;
+ * one near 0 leaves a row its largest logits alone (greedy decoding). Draft i stands while u_i q_i(x_i) < p_i(x_i)
  * and all before it stand. With n that stand,
  *   tokens[b] = x_0 ... x_(n-1), next, -1 ...;  accepted[b] = n
  *   next = argmax_j max(p_n(j) - q_n(j), 0) / e_j   where draft n fell,

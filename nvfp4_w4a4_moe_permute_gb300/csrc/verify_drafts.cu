@@ -172,9 +172,11 @@ __device__ __forceinline__ void segment(const T* row, int64_t V, int seg, int se
     return;
   }
   float r;
-  // |m| k beyond 2^100 (rows of the type's lowest value, say): the difference first, too
+  // |m| k at or above 2^24 (a temperature near 0, rows of the type's lowest value): the
+  // difference first, too. What the product below loses is up to 2^-24 of it, and
+  // would be no factor that FP32 holds.
   const float mk = -(m * k);
-  if (__any_sync(0xffffffffu, mine == m) || !(fabsf(mk) < 0x1p100f)) {
+  if (__any_sync(0xffffffffu, mine == m) || !(fabsf(mk) < 0x1p24f)) {
     float n = 0.0f;
     r = 0.0f;
     auto add = [&](float x) {
@@ -200,7 +202,8 @@ __device__ __forceinline__ void segment(const T* row, int64_t V, int seg, int se
     for (int w = 0; w < wid; ++w) first &= s_max[w] != m;
     r += first ? n - 1.0f : n;
   } else {
-    // x k - m k in one operation: what the product m k lost is a factor of every term
+    // x k - m k in one operation: what the product m k lost, at most 1/2, is a factor of
+    // every term
     const float lost = fmaf(m, k, mk);
     uint64_t acc = pair(ex2(fmaf(xh, k, mk)), ex2(fmaf(xt, k, mk)));
     const uint64_t minus = pair(mk, mk), k2 = pair(k, k);
