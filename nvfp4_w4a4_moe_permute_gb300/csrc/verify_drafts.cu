@@ -514,8 +514,9 @@ extern "C" int minite_verify_drafts(const void* target, int target_dtype, int64_
                                     minite_stream_t stream) {
   using namespace verify;
   const bool tf = target_dtype == MINITE_OUT_FP32, df = draft_dtype == MINITE_OUT_FP32;
+  const float k2 = static_cast<float>(1.4426950408889634 / static_cast<double>(temperature));   // one rounding
   if ((!tf && target_dtype != MINITE_OUT_BF16) || (draft && !df && draft_dtype != MINITE_OUT_BF16) ||
-      !(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(kLog2e / temperature))
+      !(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(k2))
     return MINITE_ERR_INVALID_ARG;
   if (B < 0 || S < 0 || S > kMaxDrafts || V < 1 || V > (int64_t(1) << 30) || B > (int64_t(1) << 31) ||
       B * (S + 1) * V > (int64_t(1) << 42) || B * (2 * S + 1) > (int64_t(1) << 24) || target_stride < V ||
@@ -548,7 +549,7 @@ extern "C" int minite_verify_drafts(const void* target, int target_dtype, int64_
   p.V = V;
   p.S = S;
   p.inv_t = 1.0f / temperature;
-  p.k2 = p.inv_t * kLog2e;
+  p.k2 = k2;
   p.target_segs = tf ? segments<float>(V) : segments<uint16_t>(V);
   p.draft_segs = !draft ? 0 : df ? segments<float>(V) : segments<uint16_t>(V);
   p.tokens = tokens;
