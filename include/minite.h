@@ -798,9 +798,10 @@ int minite_moe_combine_rows(const void* rows, int dtype, int64_t rows_stride,
  * strides and row sizes are multiples of 16 bytes: a result depends on its own two rows
  * and on that alone.
  *
- * rows, dweights: both NULL where the router is not trained. drows may be rows
- * itself (with the same stride), otherwise no overlap; rows that no slot names are
- * left as they were. Rules as minite_moe_combine_rows; weights is not NULL (see
+ * rows, dweights: both NULL where the router is not trained (with M = 0, where every
+ * slot is skipped, rows and drows may be NULL all the same: dweights becomes 0). drows
+ * may be rows itself (with the same stride), otherwise no overlap; rows that no slot
+ * names are left as they were. Rules as minite_moe_combine_rows; weights is not NULL (see
  * minite_moe_spread_rows).
  */
 int minite_moe_combine_rows_backward(const void* dy, int dtype, int64_t dy_stride,

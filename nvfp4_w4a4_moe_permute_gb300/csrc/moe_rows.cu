@@ -772,9 +772,10 @@ extern "C" int minite_moe_combine_rows_backward(const void* dy, int dtype, int64
   using namespace rows;
   const int rc = check(dtype, T, M, H, k, {dy_stride, rows_in ? rows_stride : H, drows_stride});
   if (rc != MINITE_OK) return rc;
-  if ((rows_in == nullptr) != (dweights == nullptr)) return MINITE_ERR_INVALID_ARG;
-  if (rows_in == drows && rows_stride != drows_stride) return MINITE_ERR_INVALID_ARG;
   if (T == 0) return MINITE_OK;
+  const bool dot = dweights != nullptr;
+  if ((rows_in && !dot) || (dot && !rows_in && M > 0)) return MINITE_ERR_INVALID_ARG;
+  if (rows_in && rows_in == drows && rows_stride != drows_stride) return MINITE_ERR_INVALID_ARG;
   const uintptr_t a = static_cast<uintptr_t>(size_of(dtype));
   if (!dy || !dest_row || !weights || (!drows && M > 0) || !aligned(dy, a) || !aligned(rows_in, a) ||
       !aligned(drows, a) || !aligned(dest_row, 4) || !aligned(weights, 4) || !aligned(dweights, 4) ||
@@ -785,10 +786,10 @@ extern "C" int minite_moe_combine_rows_backward(const void* dy, int dtype, int64
                o = matrix(drows, dtype, drows_stride);
   cudaError_t e;
   if (dtype == MINITE_OUT_FP32)
-    e = rows_in ? backward<float, true>(d, r, dest_row, weights, T, M, H, k, o, dweights, status, s)
-                : backward<float, false>(d, r, dest_row, weights, T, M, H, k, o, nullptr, status, s);
+    e = dot ? backward<float, true>(d, r, dest_row, weights, T, M, H, k, o, dweights, status, s)
+            : backward<float, false>(d, r, dest_row, weights, T, M, H, k, o, nullptr, status, s);
   else
-    e = rows_in ? backward<uint16_t, true>(d, r, dest_row, weights, T, M, H, k, o, dweights, status, s)
-                : backward<uint16_t, false>(d, r, dest_row, weights, T, M, H, k, o, nullptr, status, s);
+    e = dot ? backward<uint16_t, true>(d, r, dest_row, weights, T, M, H, k, o, dweights, status, s)
+            : backward<uint16_t, false>(d, r, dest_row, weights, T, M, H, k, o, nullptr, status, s);
   return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? MINITE_OK : MINITE_ERR_CUDA;
 }
