@@ -733,9 +733,9 @@ extern "C" int minite_moe_spread_rows(const void* x, int dtype, int64_t x_stride
   using namespace rows;
   const int rc = check(dtype, T, M, H, k, {x_stride, rows_stride});
   if (rc != MINITE_OK) return rc;
-  if (T == 0 || M == 0) return MINITE_OK;
+  if (T == 0 || (M == 0 && !status)) return MINITE_OK;   // without rows: only to report those that are named
   const uintptr_t a = static_cast<uintptr_t>(size_of(dtype));
-  if (!x || !dest_row || !rows_out || !aligned(x, a) || !aligned(rows_out, a) || !aligned(dest_row, 4) ||
+  if (!x || !dest_row || (!rows_out && M > 0) || !aligned(x, a) || !aligned(rows_out, a) || !aligned(dest_row, 4) ||
       !aligned(status, 4))
     return MINITE_ERR_INVALID_ARG;
   Routing r = {};

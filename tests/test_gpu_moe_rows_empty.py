@@ -24,6 +24,7 @@ def test_no_tokens(dtype, m):
     drows, dw = M.combine_rows_backward(dy, rows, dest, w, out=rows)
     assert drows is rows and (rows == 2).all() and dw.shape == (0, K)
     assert M.combine_rows_backward(dy, None, dest, w, out=rows)[1] is None
+    assert M.spread_rows(dy, dest, rows) is rows and (rows == 2).all()
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -39,6 +40,7 @@ def test_no_rows(dtype, T):
         assert drows.shape == (0, H) and dw.shape == (T, K) and not dw.any()
     assert M.combine_rows_backward(dy, None, dest, w, out=rows, status=status)[1] is None
     assert not M.permute_rows_backward(rows, dest, status=status).any()
+    M.spread_rows(dy, dest, rows, status=status)
     assert int(status) == 0
 
 
@@ -48,7 +50,8 @@ def test_rows_that_are_not_there_are_reported(dtype):
     dest[4, 1] = 0                            # the first row of none
     for call in (lambda s: M.combine_rows(rows, dest, w, status=s),
                  lambda s: M.combine_rows_backward(dy, rows, dest, w, status=s)[1],
-                 lambda s: M.combine_rows_backward(dy, None, dest, w, out=rows, status=s)[0]):
+                 lambda s: M.combine_rows_backward(dy, None, dest, w, out=rows, status=s)[0],
+                 lambda s: M.spread_rows(dy, dest, rows, status=s)):
         status = torch.zeros(1, dtype=I32, device=DEV)
         assert not call(status).any() and int(status) == 1 << M.ERR_BAD_ROUTING
 

@@ -47,6 +47,11 @@ def child():
         assert launches(lambda: backward(lib, rows=None, drows=None, M_=0, rs=0, status=P)) == 1
         # and without one there is nothing to write, but rows that are not there to report
         assert launches(lambda: backward(lib, rows=None, drows=None, dweights=None, M_=0, rs=0, status=P)) == 1
+        spread = lambda M_, rows, status: lib.minite_moe_spread_rows(P, dtype, 64, P, 8, M_, 64, 2, rows, 64, status, None)
+        assert launches(lambda: spread(0, None, P)) == 1
+        assert launches(lambda: spread(0, None, None)) == 0
+        assert launches(lambda: spread(16, 2 * P, None)) == 1
+        assert spread(16, None, None) == INVALID
     # where there are rows the pair is checked as before
     assert backward(lib, rows=None) == INVALID and backward(lib, dweights=None) == INVALID
     assert backward(lib, drows=None) == INVALID and backward(lib, rows=2 * P, rs=72) == INVALID
