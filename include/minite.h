@@ -828,6 +828,7 @@ int minite_moe_combine_rows_backward(const void* dy, int dtype, int64_t dy_strid
  * tensors: HOST array, read during the call (out and out_dtype are ignored).
  * norm, factor: device, float [1], one of them may be NULL.
  * max_norm: at or above 0, infinity allowed.
+ * At most 2^24 tensors, their elements together below 2^42.
  * workspace: device, >= minite_workspace_bytes(MINITE_OP_GRAD_NORM, n_tensors,
  *          elements of all tensors, 0, 0) bytes, 8-byte aligned, contents on entry
  *          ignored; NULL where that is 0.

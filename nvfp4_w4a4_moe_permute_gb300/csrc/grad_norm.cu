@@ -356,13 +356,12 @@ inline int grid_of(int64_t chunks, int per_sm) {
 // As many tensors as a launch takes into a batch; the next one's index.
 template <int CAP>
 int64_t fill(Batch<CAP>& b, const minite_grad_tensor* t, int64_t i, int64_t n) {
-  int64_t chunks = 0;
+  int64_t chunks = 0;   // below 2^31: check() bounds the elements of all tensors
   b.count = 0;
   for (; i < n && b.count < CAP; ++i) {
     if (t[i].n == 0) continue;
     const int size = t[i].grad_dtype == MINITE_OUT_FP32 ? 4 : 2;
     const int64_t c = ((t[i].n + lead_of(t[i].grad, size)) * size + kChunkBytes - 1) / kChunkBytes;
-    if (b.count > 0 && chunks + c > 0x7FFFFFFF) break;
     b.t[b.count] = {t[i].grad, t[i].out, t[i].n};
     b.fp32[b.count] = static_cast<uint8_t>((t[i].grad_dtype == MINITE_OUT_FP32 ? 1 : 0) |
                                            (t[i].out_dtype == MINITE_OUT_FP32 ? 2 : 0));
@@ -432,8 +431,11 @@ bool dtype_ok(int d) { return d == MINITE_OUT_BF16 || d == MINITE_OUT_FP32; }
 int check(const minite_grad_tensor* t, int64_t n, bool out) {
   if (n < 0 || (n > 0 && !t)) return MINITE_ERR_INVALID_ARG;
   if (n > (int64_t(1) << 24)) return MINITE_ERR_UNSUPPORTED_SHAPE;
+  int64_t elements = 0;
   for (int64_t i = 0; i < n; ++i) {
     if (t[i].n < 0 || t[i].n >= (int64_t(1) << 42)) return MINITE_ERR_UNSUPPORTED_SHAPE;
+    elements += t[i].n;
+    if (elements >= (int64_t(1) << 42)) return MINITE_ERR_UNSUPPORTED_SHAPE;
     if (!dtype_ok(t[i].grad_dtype) || (out && !dtype_ok(t[i].out_dtype))) return MINITE_ERR_INVALID_ARG;
     if (t[i].n == 0) continue;
     if (!t[i].grad || !aligned(t[i].grad, t[i].grad_dtype == MINITE_OUT_FP32 ? 4 : 2)) return MINITE_ERR_INVALID_ARG;
