@@ -871,15 +871,15 @@ int minite_clip_grads(const minite_grad_tensor* tensors, int64_t n_tensors, cons
  *   next = argmax_j max(p_n(j) - q_n(j), 0) / e_j   where draft n fell,
  *          argmax_j p_n(j) / e_j                     where there is none
  * equal quotients by the lower id. Where p_n - q_n leaves nothing above 0 (by
- * rounding) that its variate lets win, p_n is taken. With draft NULL the drafts were looked up: q_i is 1 at x_i.
- * logprobs[b, i] = log p_i(tokens[b, i]), 0 behind the last token.
+ * rounding) that its variate lets win, p_n is taken. With draft NULL the drafts were
+ * looked up: q_i is 1 at x_i. logprobs[b, i] = log p_i(tokens[b, i]), 0 behind the last token.
  * Probabilities are FP32: one of 2^-l is off by at most 2^-17 + 2^-22 (l + log2 V) +
- * V 2^-39 of itself. A draft whose u q is as near to p as both are off, or two quotients
- * as near to each other, may go either way. A masked token (-inf) has probability 0; where
- * a row has no probabilities (a NaN or +inf logit, or none above -inf) a draft does not
- * stand, and a row to sample from that has none, or whose draft's row has none, or of
- * which no variate lets a token win, gives token -1 with logprob NaN. A draft at or above V sets bit 1<<MINITE_ERR_BAD_TOKEN and
- * ends its sequence's drafts.
+ * V 2^-39 of itself, and 0 where l is above 126. A draft whose u q is as near to p as both
+ * are off, or two quotients as near to each other, may go either way. A masked token (-inf)
+ * has probability 0; where a row has no probabilities (a NaN or +inf logit, or none above
+ * -inf) a draft does not stand, and a row to sample from that has none, or whose draft's
+ * row has none, or of which no variate lets a token win, gives token -1 with logprob NaN.
+ * A draft at or above V sets bit 1<<MINITE_ERR_BAD_TOKEN and ends its sequence's drafts.
  *
  * target: device, BF16 or FP32 [B * (S + 1), V], rows `target_stride` elements apart;
  * draft:  device, BF16 or FP32 [B * S, V] or NULL. Both aligned to the element.
